@@ -32,7 +32,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "hq.h")
 HQ_OK, HQ_ERR_INVALID_ARG, HQ_ERR_UNSUPPORTED, HQ_ERR_WORKSPACE, HQ_ERR_HIP, HQ_ERR_INTERNAL = range(6)
 F16, BF16, F32, FP8_E4M3, INT8, U4, FP4_E2M1, E8M0, I32, U8, U2, U3, I4 = range(13)
 ZP_NONE, ZP_FIXED, ZP_PER_GROUP_U4 = range(3)
-ASCALE_NONE, ASCALE_PER_TOKEN_F32, ASCALE_MX_E8M0 = range(3)
+ASCALE_NONE, ASCALE_PER_TOKEN_F32, ASCALE_MX_E8M0, ASCALE_BLOCK_F32 = range(4)
 GEMM_DENSE, GEMM_GROUPED = range(2)
 EPI_NONE, EPI_SILU_MUL, EPI_SILU_MUL_QFP8, EPI_TOPK_COMBINE, EPI_I32_ACC = range(5)
 PEAK_F16, PEAK_BF16, PEAK_FP8, PEAK_FP8_FP4, PEAK_FP4, PEAK_INT8 = range(6)
@@ -160,6 +160,15 @@ def w4a4_mxfp4(out: str = "bf16") -> QuantDesc:
     return QuantDesc(FP4_E2M1, 4, 32, E8M0, ZP_NONE, 0, FP4_E2M1, ASCALE_MX_E8M0, _DT[out])
 
 
+def w8a8_block(out: str = "bf16") -> QuantDesc:
+    """fp8 e4m3 weights with one fp32 scale per 128 x 128 x fp8 e4m3 activations
+    with one fp32 scale per row and 128 k.  Repack takes codes uint8 (or
+    float8_e4m3fn) [N, K] and scales float32 [ceil(N/128), K/128] (stacked
+    [E, ...] for a grouped plan); a_scale is float32 [K/128, m], as
+    quantize_blocks writes it."""
+    return QuantDesc(FP8_E4M3, 8, 128, F32, ZP_NONE, 0, FP8_E4M3, ASCALE_BLOCK_F32, _DT[out])
+
+
 # ---------------------------------------------------------------- library --
 _lib = None
 
@@ -196,6 +205,8 @@ _SIGS = {
     "hq_quantize_per_token": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int] +
                               [ctypes.c_void_p] * 4),
     "hq_quantize_mxfp4": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p] * 4),
+    "hq_quantize_blocks": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int] +
+                           [ctypes.c_void_p] * 4),
     "hq_plan_autotune": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 6 +
                          [ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p,
                           ctypes.POINTER(AutotuneResult)]),
@@ -368,7 +379,20 @@ class Plan:
             self._ws[dev] = ws
         return ws
 
+    @property
+    def _block8(self) -> bool:
+        return self.quant.act_scale == ASCALE_BLOCK_F32
+
     # -- repack ---------------------------------------------------------
+    def _check_block_weight(self, codes, scales):
+        if not self._block8:
+            return
+        if codes.numel() * codes.element_size() != self.num_experts * self.n * self.k:
+            raise ValueError(f"codes must hold {self.num_experts} x [{self.n}, {self.k}] bytes")
+        if scales is None or scales.dtype != torch.float32 or \
+                scales.numel() != self.num_experts * (-(-self.n // 128)) * (self.k // 128):
+            raise ValueError(f"scales must be float32, {self.num_experts} x [{-(-self.n // 128)}, {self.k // 128}]")
+
     def _repack_outputs(self, device):
         wb, mb = self.repacked_bytes()
         w = torch.empty(wb, dtype=torch.uint8, device=device)
@@ -382,6 +406,7 @@ class Plan:
         for t, nm in ((scales, "scales"), (zeros, "zeros"), (e8m0, "e8m0")):
             if t is not None:
                 _dev(t, nm)
+        self._check_block_weight(codes, scales)
         w, meta = self._repack_outputs(codes.device)
         zx = e8m0 if e8m0 is not None else zeros
         _check(lib().hq_repack(self._h, _ptr(codes), _ptr(scales), _ptr(zx), _ptr(w), _ptr(meta),
@@ -396,6 +421,7 @@ class Plan:
             if t is not None and t.is_cuda:
                 raise ValueError("repack_host takes CPU tensors")
         codes, scales, zeros, e8m0 = ts
+        self._check_block_weight(codes, scales)
         w, meta = self._repack_outputs("cpu")
         zx = e8m0 if e8m0 is not None else zeros
         _check(lib().hq_repack_host(self._h, _ptr(codes), _ptr(scales), _ptr(zx), _ptr(w), _ptr(meta)))
@@ -412,6 +438,11 @@ class Plan:
             if a_scale.dtype != (torch.uint8 if act4 else torch.float32):
                 raise ValueError("a_scale must be uint8 E8M0 [m, k/32] (MXFP4 activations) or float32 [m]")
         m = a.shape[0]
+        if self._block8:
+            if a_scale is None or a_scale.numel() != m * (self.k // 128):
+                raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
+            if a.element_size() != 1:
+                raise ValueError("a must hold one-byte fp8 codes")
         if act4:  # MXFP4 codes two per byte: [m, k/2] bytes (or [m, k/8] int32 words)
             if a.dim() != 2 or a.shape[1] * a.element_size() != self.k // 2:
                 raise ValueError(f"a must hold [m, {self.k // 2}] bytes of packed MXFP4 codes")
@@ -436,7 +467,8 @@ class Plan:
         """out = x . W_deq^T for 16-bit activations x [m, k]: a plan that runs
         8-bit activations quantises x per token first (hq_quantize_per_token:
         fp8 e4m3 or int8), one that runs MXFP4 activations block-quantises it
-        (hq_quantize_mxfp4), a 16-bit plan -- including one that fell back --
+        (hq_quantize_mxfp4), one that runs fp8 with block scales quantises it
+        by row and 128 k (hq_quantize_blocks), a 16-bit plan -- including one that fell back --
         multiplies x as it is.  Every step is a library kernel on x's stream;
         the activation codes live in a buffer kept per device and m."""
         _dev(x, "x")
@@ -448,6 +480,9 @@ class Plan:
                 raise ValueError(f"this plan multiplies {_DT_NAME[q.act]} activations")
             return self.gemm(x, w, meta, out=out, ws=ws)
         m = x.shape[0]
+        if self._block8:
+            codes, sc = quantize_blocks(x)
+            return self.gemm(codes, w, meta, a_scale=sc, out=out, ws=ws)
         key = (x.device, m)
         buf = self._act_buf.get(key)
         if q.act == FP4_E2M1:
@@ -609,6 +644,34 @@ def quantize_per_token(x: torch.Tensor, out: str = "fp8", codes: Optional[torch.
     return codes, scales
 
 
+def quantize_blocks(x: torch.Tensor, silu_mul: bool = False, codes: Optional[torch.Tensor] = None,
+                    scales: Optional[torch.Tensor] = None):
+    """fp8 e4m3 quantisation of fp16 / bf16 activations by row and 128 columns
+    (see hq_quantize_blocks): x [m, k], or with silu_mul the [m, 2k] output of
+    a gate_up GEMM, of which SiLU(x[:, :k]) * x[:, k:] is quantised.  Returns
+    (codes uint8 [m, k], scales float32 [k/128, m]), the (a, a_scale) of a
+    w8a8_block GEMM."""
+    _dev(x, "x")
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("x must be fp16 / bf16 [m, k]")
+    m, k = x.shape
+    if silu_mul:
+        if k % 2:
+            raise ValueError("x must be [m, 2k] with silu_mul")
+        k //= 2
+    if codes is None:
+        codes = torch.empty((m, k), dtype=torch.uint8, device=x.device)
+    elif _dev(codes, "codes").shape != (m, k) or codes.element_size() != 1 or codes.device != x.device:
+        raise ValueError("codes must be 1-byte [m, k] on x's device")
+    if scales is None:
+        scales = torch.empty((k // 128, m), dtype=torch.float32, device=x.device)
+    elif _dev(scales, "scales").shape != (k // 128, m) or scales.dtype != torch.float32 or scales.device != x.device:
+        raise ValueError("scales must be float32 [k/128, m] on x's device")
+    _check(lib().hq_quantize_blocks(m, k, BF16 if x.dtype == torch.bfloat16 else F16, 1 if silu_mul else 0,
+                                    x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream_ptr(x.device)))
+    return codes, scales
+
+
 def mx_scales_group_major(e8m0_rows: torch.Tensor) -> torch.Tensor:
     """Row-major E8M0 block scales [m, K/32] -> the group-major words
     [K/128, m, 4] that a W4A4 GEMM reads (a copy; runs where the tensor is)."""
@@ -714,7 +777,15 @@ class MoePlan(Plan):
             else:
                 out = torch.empty((mp, self.n), dtype=_TORCH_OUT[self.quant.out], device=dev)
         if self.epi == EPI_SILU_MUL_QFP8 and out_scale is None:
-            out_scale = torch.empty(mp, dtype=torch.float32, device=dev)
+            shape = (self.n // 256, mp) if self._block8 else (mp,)
+            out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
+        if self._block8:
+            rows = mp if self.epi == EPI_TOPK_COMBINE else t
+            if mp != need:
+                raise ValueError(f"sorted_ids must hold {need} ids: the block scales are laid out for that many rows")
+            if a_scale is None or a_scale.dtype != torch.float32 or a_scale.numel() != rows * (self.k // 128) or \
+                    a.element_size() != 1 or a.numel() != rows * self.k:
+                raise ValueError(f"a must hold [{rows}, {self.k}] one-byte codes and a_scale float32 [{self.k // 128}, {rows}]")
         if ws is None:
             ws = self.moe_workspace(t, topk, dev)
         ws_bytes = 0 if ws is None else ws.numel()
@@ -786,6 +857,12 @@ def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: to
     if down.epi != EPI_TOPK_COMBINE or gate_up.epi not in (EPI_SILU_MUL, EPI_SILU_MUL_QFP8):
         raise ValueError("moe_layer takes a gate_up plan (silu_mul / silu_mul_qfp8) and a topk_combine plan")
     fp8 = gate_up.epi == EPI_SILU_MUL_QFP8
+    if gate_up._block8:
+        if by_slot:
+            raise ValueError("w8a8_block layers have no by-slot path")
+        by_slot = False
+        if x_scale is None:
+            x, x_scale = quantize_blocks(x)
     if by_slot is None:
         by_slot = moe_uses_by_slot(t, topk, fp8)
     if by_slot:

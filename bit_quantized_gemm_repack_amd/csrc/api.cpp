@@ -16,6 +16,7 @@
 #include <new>
 #include <string>
 
+#include "block8.h"
 #include "hq_internal.h"
 #include "jit.h"
 
@@ -85,6 +86,15 @@ hq_status classify(const hq_quant_desc& q, int* fmt) {
       return fail(HQ_ERR_UNSUPPORTED, "INT%d weights are implemented with fp16 / bf16 activations", bits);
     if (bits == 2) *fmt = q.act == HQ_F16 ? hq::FMT_W2F16 : hq::FMT_W2BF16;
     else *fmt = q.act == HQ_F16 ? hq::FMT_W3F16 : hq::FMT_W3BF16;
+    return HQ_OK;
+  }
+  if (q.w_elem == HQ_FP8_E4M3) {
+    if (q.w_bits != 8) return fail(HQ_ERR_UNSUPPORTED, "fp8 weights have w_bits 8 (got %d)", q.w_bits);
+    if (q.group_size != 128 || q.scale != HQ_F32 || q.zp != HQ_ZP_NONE)
+      return fail(HQ_ERR_UNSUPPORTED, "fp8 weights take one fp32 scale per 128 x 128 and no zero point");
+    if (q.act != HQ_FP8_E4M3 || q.act_scale != HQ_ASCALE_BLOCK_F32)
+      return fail(HQ_ERR_UNSUPPORTED, "fp8 weights are implemented with fp8 activations of one scale per row and 128 k");
+    *fmt = hq::FMT_B8;
     return HQ_OK;
   }
   if (q.w_bits != 4) return fail(HQ_ERR_UNSUPPORTED, "this weight element needs w_bits 4 (got %d)", q.w_bits);
@@ -164,6 +174,7 @@ const char* fmt_name(int fmt) {
     case hq::FMT_Q8: return "w4a8-fp8";
     case hq::FMT_F4: return "w4a8-mxfp4";
     case hq::FMT_F44: return "w4a4-mxfp4";
+    case hq::FMT_B8: return "w8a8-block";
   }
   return "?";
 }
@@ -172,7 +183,8 @@ const char* fmt_name(int fmt) {
 hq_mfma_in implied_mfma(int fmt) {
   switch (fmt) {
     case hq::FMT_I8: return HQ_MFMA_INT8;
-    case hq::FMT_Q8: return HQ_MFMA_FP8;
+    case hq::FMT_Q8:
+    case hq::FMT_B8: return HQ_MFMA_FP8;
     case hq::FMT_F4: return HQ_MFMA_FP8_FP4;
     case hq::FMT_F44: return HQ_MFMA_FP4;
   }
@@ -212,7 +224,49 @@ static const hq_tuning* tuned_for(const hq_plan* p, int64_t m) {
   return &p->user;
 }
 
+// fp8 x fp8 with 128-block scales (block8.h): the weight-streaming kernel for
+// few rows, the tiled one beyond.
+static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
+  Exec e{};
+  const int64_t N = p->layer.n, G = p->layer.k / kFragK, mm = m > 0 ? m : 1;
+  const bool skinny = u.kernel ? u.kernel == KER_SKINNY : mm <= 64;
+  int64_t split = 1;
+  if (skinny) {
+    e.kernel = KER_SKINNY;
+    SkinnyCfg& c = e.sk;
+    c.mb = mm <= 16 ? 1 : (mm <= 32 ? 2 : 4);
+    c.nb = 1;
+    c.waves = 8;
+    c.stages = 1;
+    if (u.tile_m) c.mb = u.tile_m / 16;
+    if (u.tile_n) c.nb = u.tile_n / 16;
+    if (u.waves) c.waves = u.waves;
+    e.tiles_m = cdiv(mm, 16 * std::max(1, c.mb));
+    e.tiles_n = cdiv(N / 16, std::max(1, c.nb));
+    split = u.split_k ? u.split_k : 1;
+  } else {
+    e.kernel = KER_TILED;
+    e.tl.bm = mm <= 16 ? 16 : (mm <= 32 ? 32 : (mm <= 64 ? 64 : 128));
+    e.tl.nbw = mm <= 64 ? 2 : 4;
+    e.tl.gm = u.tile_group ? u.tile_group : 8;
+    if (u.tile_m) e.tl.bm = u.tile_m;
+    if (u.tile_n) e.tl.nbw = u.tile_n / 64;
+    e.tl.stages = u.stages ? u.stages : (e.tl.nbw == 4 ? (e.tl.bm <= 32 ? 3 : 2) : (e.tl.bm <= 64 ? 4 : 3));
+    e.tiles_m = cdiv(mm, std::max(1, e.tl.bm));
+    e.tiles_n = cdiv(N, 64 * std::max(1, e.tl.nbw));
+    const int64_t tiles = e.tiles_m * e.tiles_n;
+    if (u.split_k) split = u.split_k;
+    else if (tiles < 256) split = std::min<int64_t>(cdiv(256, tiles), std::max<int64_t>(1, G / 2));
+  }
+  split = std::max<int64_t>(1, std::min<int64_t>({split, G, 64}));
+  split = cdiv(G, cdiv(G, split));  // no empty split
+  (skinny ? e.sk.split : e.tl.split) = (int)split;
+  e.ws_bytes = split > 1 ? align256((size_t)split * (size_t)mm * (size_t)N * 4) : 0;
+  return e;
+}
+
 Exec choose_exec(const hq_plan* p, int64_t m, const hq_tuning* up) {
+  if (p->fmt == FMT_B8) return choose_exec_b8(p, m, up ? *up : *tuned_for(p, m));
   Exec e{};
   e.kernel = KER_SKINNY;
   const int64_t N = p->layer.n;
@@ -368,6 +422,18 @@ namespace {
 
 hq_status check_exec(const hq_plan* p, const hq::Exec& e) {
   if (p->user.split_k < 0 || p->user.split_k > 64) return fail(HQ_ERR_INVALID_ARG, "split_k must be 1..64");
+  if (p->fmt == hq::FMT_B8) {
+    if (e.kernel == hq::KER_TILED) {
+      if (!hq::b8_tile_ok(hq::B8_DENSE, {e.tl.bm, 64 * e.tl.nbw, e.tl.split, e.tl.stages}))
+        return fail(HQ_ERR_INVALID_ARG, "no fp8 block tile of %d x %d with %d stages", e.tl.bm, 64 * e.tl.nbw, e.tl.stages);
+      if (e.tl.gm < 1 || e.tl.gm > 64) return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_group must be 1..64");
+      if (e.tiles_m * e.tiles_n > (int64_t(1) << 31) - 1) return fail(HQ_ERR_UNSUPPORTED, "too many tiles");
+    } else if (!hq::b8_skinny_ok({e.sk.mb, e.sk.nb, e.sk.waves, e.sk.split})) {
+      return fail(HQ_ERR_INVALID_ARG, "no fp8 block skinny shape of %d x %d with %d waves", 16 * e.sk.mb, 16 * e.sk.nb,
+                  e.sk.waves);
+    }
+    return HQ_OK;
+  }
   if (e.kernel == hq::KER_TILED) {
     if (e.tl.bm != 64 && e.tl.bm != 128) return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_m must be 64 or 128");
     if (e.tl.nbw != 2 && e.tl.nbw != 4) return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_n must be 128 or 256");
@@ -475,8 +541,17 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
         return fail(HQ_ERR_INVALID_ARG, "unknown epilogue");
     }
     if (compute->kind == HQ_GEMM_GROUPED) {
-      if (fmt != hq::FMT_W16F16 && fmt != hq::FMT_W16BF16 && fmt != hq::FMT_Q8)
-        return fail(HQ_ERR_UNSUPPORTED, "grouped GEMM supports INT4 weights with fp16/bf16/fp8 activations");
+      if (fmt != hq::FMT_W16F16 && fmt != hq::FMT_W16BF16 && fmt != hq::FMT_Q8 && fmt != hq::FMT_B8)
+        return fail(HQ_ERR_UNSUPPORTED, "grouped GEMM supports INT4 weights with fp16/bf16/fp8 activations, and fp8 "
+                                        "weights with block scales");
+      if (fmt == hq::FMT_B8) {
+        if (compute->epi != HQ_EPI_SILU_MUL_QFP8 && compute->epi != HQ_EPI_TOPK_COMBINE)
+          return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers are gate_up with the fp8 requant, or down with the combine");
+        if (compute->epi == HQ_EPI_SILU_MUL_QFP8 && layer->n % 256)
+          return fail(HQ_ERR_UNSUPPORTED, "fp8 block gate_up needs n (gate + up) a multiple of 256");
+        if (tuning && (tuning->kernel == hq::KER_SKINNY || (tuning->tile_n && tuning->tile_n != 256)))
+          return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers run 256-column tiles");
+      }
       if ((compute->epi == HQ_EPI_SILU_MUL || compute->epi == HQ_EPI_SILU_MUL_QFP8) && layer->n % 32)
         return fail(HQ_ERR_UNSUPPORTED, "SiLU * mul needs n (gate + up) a multiple of 32");
       if (compute->epi == HQ_EPI_TOPK_COMBINE && layer->n % 64)
@@ -487,7 +562,7 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
           return fail(HQ_ERR_UNSUPPORTED, "grouped tile_m must be 16 or 32 (skinny), 64 or 128 (tiled)");
         if (tuning->kernel == hq::KER_SKINNY && tm > 32)
           return fail(HQ_ERR_UNSUPPORTED, "the skinny grouped kernel uses 16- or 32-row blocks");
-        if (tuning->kernel == hq::KER_TILED && (tm == 16 || tm == 32))
+        if (tuning->kernel == hq::KER_TILED && (tm == 16 || tm == 32) && fmt != hq::FMT_B8)
           return fail(HQ_ERR_UNSUPPORTED, "the tiled grouped kernel uses 64- or 128-row blocks");
         if (tn != 0 && tn != 16 && tn != 32 && tn != 64 && tn != 128 && tn != 256)
           return fail(HQ_ERR_UNSUPPORTED, "grouped tile_n must be 128 or 256 (tiled), 16, 32 or 64 (by slot)");
@@ -504,7 +579,10 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
     p->fmt = fmt;
     const int64_t N = layer->n, K = layer->k, G = K / 128;
     p->w_bytes_per_expert = (size_t)N * (size_t)K * (size_t)hq::frag_bytes(fmt) / (size_t)(hq::kFragN * hq::kFragK);
-    if (hq::nvfp4_weights(fmt)) {
+    if (fmt == hq::FMT_B8) {
+      p->scale_region_bytes = (size_t)((N + 127) / 128 * G * 4);
+      p->meta_bytes_per_expert = p->scale_region_bytes;
+    } else if (hq::nvfp4_weights(fmt)) {
       p->scale_region_bytes = 0;  // E4M3 region, then the fp32 tensor scale (16 bytes)
       p->meta_bytes_per_expert = (size_t)(N * K / 16 + 16);
     } else if (hq::e8m0_meta(fmt)) {
@@ -575,7 +653,9 @@ hq_status hq_repacked_bytes(const hq_plan* p, size_t* w_bytes, size_t* meta_byte
 static hq_status check_repack_args(const hq_plan* p, const void* codes, const void* scales, const void* zx,
                                    const void* w_out, const void* meta_out) {
   if (!p || !codes || !w_out || !meta_out) return fail(HQ_ERR_INVALID_ARG, "null argument");
-  if (hq::nvfp4_weights(p->fmt)) {
+  if (p->fmt == hq::FMT_B8) {
+    if (!scales) return fail(HQ_ERR_INVALID_ARG, "fp8 repack needs the fp32 block scales");
+  } else if (hq::nvfp4_weights(p->fmt)) {
     if (!zx || !scales) return fail(HQ_ERR_INVALID_ARG, "NVFP4 repack needs the E4M3 block scales and the tensor scale");
   } else if (hq::e8m0_meta(p->fmt)) {
     if (!zx) return fail(HQ_ERR_INVALID_ARG, "MXFP4 / MXINT4 repack needs the E8M0 scales");
@@ -594,7 +674,9 @@ hq_status hq_repack(const hq_plan* p, const void* codes, const void* scales, con
     if (s != HQ_OK) return s;
     if (!aligned16(codes) || !aligned16(w_out) || !aligned16(meta_out))
       return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
-    int err = hq::launch_repack(p, codes, scales, zx, w_out, meta_out, stream);
+    int err = p->fmt == hq::FMT_B8 ? hq::launch_b8_repack(p->layer.n, p->layer.k, p->layer.num_experts, codes, scales,
+                                                          w_out, meta_out, stream)
+                                   : hq::launch_repack(p, codes, scales, zx, w_out, meta_out, stream);
     if (err != hipSuccess) return fail(HQ_ERR_HIP, "repack launch: %s", hipGetErrorString((hipError_t)err));
     return ok();
   } catch (...) {
@@ -609,6 +691,14 @@ hq_status hq_repack_host(const hq_plan* p, const void* codes, const void* scales
     if (s != HQ_OK) return s;
     const int64_t N = p->layer.n, K = p->layer.k, E = p->layer.num_experts, G = K / 128;
     uint32_t* wo = static_cast<uint32_t*>(w_out);
+    if (p->fmt == hq::FMT_B8) {
+      const int64_t wpe = N * K / 4;
+      const uint8_t* cb = static_cast<const uint8_t*>(codes);
+      for (int64_t e = 0; e < E; ++e)
+        for (int64_t i = 0; i < wpe; ++i) wo[e * wpe + i] = hq::repack_word_b8(cb + e * N * K, K, i);
+      std::memcpy(meta_out, scales, p->meta_bytes_per_expert * (size_t)E);
+      return ok();
+    }
     if (hq::w3_weights(p->fmt)) {
       const int64_t wpe3 = N * K * 3 / 32;
       const uint32_t* cw = static_cast<const uint32_t*>(codes);
@@ -682,7 +772,7 @@ hq_status dense_args_check(const hq_plan* p, int64_t m, const void* a, const voi
   if (!aligned16(a) || !aligned16(w) || !aligned16(meta) || !aligned16(out))
     return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
   const bool act4 = p->fmt == hq::FMT_F44;
-  const bool act8 = p->fmt == hq::FMT_I8 || p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_F4;
+  const bool act8 = p->fmt == hq::FMT_I8 || p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_F4 || p->fmt == hq::FMT_B8;
   if (act8 && !a_scale) return fail(HQ_ERR_INVALID_ARG, "8-bit activations need a_scale");
   if (act4 && !a_scale) return fail(HQ_ERR_INVALID_ARG, "MXFP4 activations need their E8M0 scales in a_scale");
   if (act4 && !aligned16(a_scale)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
@@ -696,7 +786,7 @@ hq_status dense_run(const hq_plan* p, const hq::Exec& e, int64_t m, const void* 
                     const hq::TimingEvents& ev) {
   {
     const bool act4 = p->fmt == hq::FMT_F44;
-    const bool act8 = p->fmt == hq::FMT_I8 || p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_F4;
+    const bool act8 = p->fmt == hq::FMT_I8 || p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_F4 || p->fmt == hq::FMT_B8;
     const float* a_scale_f = act8 ? static_cast<const float*>(a_scale) : nullptr;
     const uint8_t* a_e8m0 = act4 ? static_cast<const uint8_t*>(a_scale) : nullptr;
     hq_status s = check_exec(p, e);
@@ -718,6 +808,37 @@ hq_status dense_run(const hq_plan* p, const hq::Exec& e, int64_t m, const void* 
       const int64_t act_bytes2 = hq::act16_fmt(p->fmt) ? 4 : (act4 ? 1 : 2);
       if (m * K * act_bytes2 / 2 >= (int64_t(1) << 31) || (int64_t)p->w_bytes_per_expert >= (int64_t(1) << 31))
         return fail(HQ_ERR_UNSUPPORTED, "activations and weights must each stay below 2 GiB");
+    }
+    if (p->fmt == hq::FMT_B8) {
+      const bool tiled = e.kernel == hq::KER_TILED;
+      const int split = tiled ? e.tl.split : e.sk.split;
+      hq::B8Args b{};
+      b.a = static_cast<const uint8_t*>(a);
+      b.a_scale = a_scale_f;
+      b.w = static_cast<const uint8_t*>(w);
+      b.w_scale = static_cast<const float*>(meta);
+      b.out = out;
+      b.part = split > 1 ? static_cast<float*>(ws) : nullptr;
+      b.M = (int)m;
+      b.N = (int)N;
+      b.K = (int)K;
+      b.G = (int)G;
+      b.a_rows = (int)m;
+      b.out_bf16 = p->layer.q.out == HQ_BF16;
+      b.gps = (int)cdiv(G, split);
+      b.tiles_m = (int)e.tiles_m;
+      b.tiles_n = (int)e.tiles_n;
+      b.group_m = (int)std::min<int64_t>(e.tl.gm, std::max<int64_t>(1, e.tiles_m));
+      hq::arm_timing({ev.start, split > 1 ? nullptr : ev.stop});
+      int err = tiled ? hq::launch_b8_tiled(hq::B8_DENSE, {e.tl.bm, 64 * e.tl.nbw, split, e.tl.stages}, b, 0, stream)
+                      : hq::launch_b8_skinny({e.sk.mb, e.sk.nb, e.sk.waves, split}, b, stream);
+      if (err == hipSuccess && split > 1) {
+        hq::arm_timing({nullptr, ev.stop});
+        err = hq::launch_splitk_reduce(b.part, split, m * N, out, b.out_bf16, stream);
+      }
+      hq::arm_timing({nullptr, nullptr});
+      if (err != hipSuccess) return fail(HQ_ERR_HIP, "gemm launch: %s", hipGetErrorString((hipError_t)err));
+      return ok();
     }
     if (e.kernel == hq::KER_TILED) {
       hq::TiledArgs t{};
@@ -871,6 +992,15 @@ static MoeChoice moe_choice(const hq_plan* p, int64_t t, int topk) {
   const hq_tuning& u = p->user;
   const int64_t N = p->layer.n;
   const double per_expert = (double)t * topk / p->layer.num_experts;
+  if (p->fmt == hq::FMT_B8) {
+    c.tiled = true;
+    c.bm = u.tile_m ? u.tile_m : (per_expert <= 12 ? 16 : (per_expert <= 24 ? 32 : (per_expert <= 64 ? 64 : 128)));
+    c.tl.bm = c.bm;
+    c.tl.nbw = 4;
+    c.tl.split = 1;
+    c.tl.stages = c.bm <= 32 ? 3 : 2;
+    return c;
+  }
   bool tiled;
   if (u.kernel == hq::KER_TILED) tiled = true;
   else if (u.kernel == hq::KER_SKINNY) tiled = false;
@@ -994,7 +1124,8 @@ struct MoeWs {
 static MoeWs moe_ws(const hq_plan* p, int64_t t, int topk) {
   MoeWs w{};
   const int64_t mp = moe_max_padded(t, topk, p->layer.num_experts, moe_choice(p, t, topk).bm);
-  if (p->compute.epi == HQ_EPI_SILU_MUL_QFP8) w.act32 = align256((size_t)mp * (size_t)(p->layer.n / 2) * 4);
+  // (the fp8 block gate_up requantises inside its tile: no fp32 rows)
+  if (p->compute.epi == HQ_EPI_SILU_MUL_QFP8 && p->fmt != hq::FMT_B8) w.act32 = align256((size_t)mp * (size_t)(p->layer.n / 2) * 4);
   if (p->compute.epi == HQ_EPI_TOPK_COMBINE)
     w.rows = align256((size_t)t * topk * (size_t)moe_down_cols(p, t, topk, moe_choice(p, t, topk).bm) * 2);
   w.total = w.act32 + w.rows;
@@ -1024,7 +1155,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       return fail(HQ_ERR_INVALID_ARG, "null device pointer");
     if (!aligned16(a) || !aligned16(w) || !aligned16(meta) || !aligned16(out))
       return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
-    const bool act8 = p->fmt == hq::FMT_Q8;
+    const bool act8 = p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_B8;
     if (act8 && !a_scale) return fail(HQ_ERR_INVALID_ARG, "8-bit activations need a_scale");
     if (!act8 && a_scale) return fail(HQ_ERR_INVALID_ARG, "16-bit activations take no a_scale");
     const int epi = p->compute.epi;
@@ -1045,7 +1176,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       // down GEMM) and one expert's W through 32-bit buffer ranges
       const int64_t act_bytes = (p->fmt == hq::FMT_W16F16 || p->fmt == hq::FMT_W16BF16) ? 2 : 1;
       const int64_t a_rows = epi == HQ_EPI_TOPK_COMBINE ? mp : t;
-      if (a_rows * K * act_bytes >= (int64_t(1) << 31) || N * K / 2 >= (int64_t(1) << 31))
+      if (a_rows * K * act_bytes >= (int64_t(1) << 31) || (int64_t)p->w_bytes_per_expert >= (int64_t(1) << 31))
         return fail(HQ_ERR_UNSUPPORTED, "activations and one expert's weights must each stay below 2 GiB");
     }
     const uint32_t* zeros = p->layer.q.zp == HQ_ZP_PER_GROUP_U4
@@ -1076,6 +1207,42 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     const int64_t blocks = std::min<int64_t>(mp / bm, t * topk);
     const int n_slots = (int)(t * topk);
     int err;
+    if (p->fmt == hq::FMT_B8) {
+      const bool down = epi == HQ_EPI_TOPK_COMBINE;
+      hq::B8Args b{};
+      b.a = static_cast<const uint8_t*>(a);
+      b.a_scale = a_scale;
+      b.w = static_cast<const uint8_t*>(w);
+      b.w_scale = static_cast<const float*>(meta);
+      b.out = out;
+      b.M = (int)mp;
+      b.N = (int)N;
+      b.K = (int)K;
+      b.G = (int)G;
+      b.a_rows = (int)(down ? mp : t);
+      b.gps = (int)G;
+      b.tiles_n = (int)cdiv(N, 256);
+      b.sorted_ids = sorted_ids;
+      b.block_expert = block_expert;
+      b.num_padded = num_padded;
+      b.topk_w = topk_w;
+      b.topk = topk;
+      b.n_slots = n_slots;
+      b.w_expert = (int64_t)p->w_bytes_per_expert;
+      b.s_expert = (int64_t)(p->meta_bytes_per_expert / 4);
+      b.out_scale = out_scale;
+      b.out_rows = (int)mp;
+      b.rows16 = rows16;
+      hq::arm_timing({ev.start, down ? nullptr : ev.stop});
+      err = hq::launch_b8_tiled(down ? hq::B8_DOWN : hq::B8_GATE_UP, {bm, 256, 1, mc.tl.stages}, b, blocks, stream);
+      if (err == hipSuccess && down) {
+        hq::arm_timing({nullptr, ev.stop});
+        err = hq::launch_moe_combine(rows16, topk, t, N, 0, N, out, p->layer.q.out == HQ_BF16, stream);
+      }
+      hq::arm_timing({nullptr, nullptr});
+      if (err != hipSuccess) return fail(HQ_ERR_HIP, "grouped gemm launch: %s", hipGetErrorString((hipError_t)err));
+      return ok();
+    }
     const bool second = epi == HQ_EPI_SILU_MUL_QFP8 || epi == HQ_EPI_TOPK_COMBINE;
     hq::arm_timing({ev.start, second ? nullptr : ev.stop});
     // the down projection with a short K: activations resident in registers,
@@ -1209,6 +1376,8 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* p, int64_t t, int topk, const void*
   try {
     if (!p) return fail(HQ_ERR_INVALID_ARG, "null plan");
     if (p->compute.kind != HQ_GEMM_GROUPED) return fail(HQ_ERR_INVALID_ARG, "hq_moe_gemm_by_slot needs a grouped plan");
+    if (p->fmt == hq::FMT_B8)
+      return fail(HQ_ERR_UNSUPPORTED, "fp8 block layers run few tokens through hq_moe_layer_few");
     if (t < 0 || t > p->max_m) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, max_m]");
     if (topk < 1 || topk > 64) return fail(HQ_ERR_INVALID_ARG, "topk must be 1..64");
     if (t == 0) return ok();
@@ -1349,6 +1518,26 @@ hq_status hq_quantize_per_token(int64_t m, int64_t k, hq_dtype in, hq_dtype out,
   return ok();
 }
 
+hq_status hq_quantize_blocks(int64_t m, int64_t k, hq_dtype in, int silu_mul, const void* x, void* codes,
+                             float* scales, void* stream) {
+  const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
+  if (in != HQ_F16 && in != HQ_BF16) return fail(HQ_ERR_UNSUPPORTED, "input must be fp16 or bf16");
+  if (silu_mul != 0 && silu_mul != 1) return fail(HQ_ERR_INVALID_ARG, "silu_mul must be 0 or 1");
+  if (m < 0 || m > (int64_t(1) << 24)) return fail(HQ_ERR_INVALID_ARG, "m out of range [0, 2^24]");
+  if (k < 128 || k % 128 || k > (int64_t(1) << 24))
+    return fail(HQ_ERR_INVALID_ARG, "k must be a multiple of 128 in [128, 2^24]");
+  if (m * (k / 128) >= (int64_t(1) << 31) - 16) return fail(HQ_ERR_UNSUPPORTED, "m * k / 128 above 2^31");
+  if (m == 0) return ok();
+  if (!x || !codes || !scales) return fail(HQ_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  hq::arm_timing(ev);
+  const int err = hq::launch_quantize_blocks(m, k, in == HQ_BF16, silu_mul, x, codes, scales, stream);
+  hq::arm_timing({nullptr, nullptr});
+  if (err != hipSuccess) return fail(HQ_ERR_HIP, "quantize launch: %s", hipGetErrorString((hipError_t)err));
+  return ok();
+}
+
 hq_status hq_quantize_mxfp4(int64_t m, int64_t k, hq_dtype in, const void* x, void* codes, uint8_t* e8m0,
                             void* stream) {
   const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
@@ -1408,6 +1597,21 @@ bool same_tuning(const hq_tuning& a, const hq_tuning& b) {
 // kernel from 17 rows on (tile shape, ring depth, K split).
 std::vector<hq_tuning> tuning_candidates(const hq_plan* p, int64_t m) {
   std::vector<hq_tuning> c;
+  if (p->fmt == hq::FMT_B8) {
+    // shapes without a kernel are skipped by the caller (check_exec)
+    if (m <= 128)
+      for (int tm : {16, 32, 64})
+        for (int tn : {16, 32})
+          for (int waves : {4, 8, 16})
+            for (int split : {1, 2, 4, 8}) c.push_back(hq_tuning{hq::KER_SKINNY, tm, tn, waves, split, 0, 0, 0});
+    for (int bm : {16, 32, 64, 128, 256}) {
+      if (bm > 16 && bm / 2 >= m) continue;  // no tile taller than the rows need
+      for (int tn : {128, 256})
+        for (int stages : {2, 3, 4})
+          for (int split : {1, 2, 4, 8, 16}) c.push_back(hq_tuning{hq::KER_TILED, bm, tn, 0, split, stages, 0, 0});
+    }
+    return c;
+  }
   if (m <= 64) {
     for (int mb : {1, 2, 4}) {
       if (mb > 1 && 16 * (mb / 2) >= m) continue;  // no tile taller than the rows need
@@ -1478,6 +1682,8 @@ hq_status hq_plan_set_jit(hq_plan* p, int enable, const char* cache_dir) {
   if (enable != 0 && enable != 1) return fail(HQ_ERR_INVALID_ARG, "enable must be 0 or 1");
   if (p->compute.kind != HQ_GEMM_DENSE)
     return fail(HQ_ERR_UNSUPPORTED, "run-time specialisation covers dense plans only");
+  if (p->fmt == hq::FMT_B8)
+    return fail(HQ_ERR_UNSUPPORTED, "run-time specialisation does not cover fp8 weights with block scales");
   if (cache_dir && std::strlen(cache_dir) >= sizeof(p->jit_dir))
     return fail(HQ_ERR_INVALID_ARG, "cache directory path longer than %zu bytes", sizeof(p->jit_dir) - 1);
   p->jit = enable;
@@ -1490,6 +1696,8 @@ hq_status hq_jit_cache_key(const hq_plan* p, int64_t m, const char* arch, char* 
     if (!p || !arch || !key) return fail(HQ_ERR_INVALID_ARG, "null argument");
     if (p->compute.kind != HQ_GEMM_DENSE)
       return fail(HQ_ERR_UNSUPPORTED, "run-time specialisation covers dense plans only");
+    if (p->fmt == hq::FMT_B8)
+      return fail(HQ_ERR_UNSUPPORTED, "run-time specialisation does not cover fp8 weights with block scales");
     if (m < 1 || m > p->max_m) return fail(HQ_ERR_INVALID_ARG, "m out of range [1, max_m]");
     const hq::Exec e = hq::choose_exec(p, m);
     const int64_t N = p->layer.n, K = p->layer.k;
@@ -1509,6 +1717,8 @@ hq_status hq_jit_prepare(const hq_plan* p, int64_t m, const char* arch) {
     if (!p || !arch) return fail(HQ_ERR_INVALID_ARG, "null argument");
     if (p->compute.kind != HQ_GEMM_DENSE)
       return fail(HQ_ERR_UNSUPPORTED, "run-time specialisation covers dense plans only");
+    if (p->fmt == hq::FMT_B8)
+      return fail(HQ_ERR_UNSUPPORTED, "run-time specialisation does not cover fp8 weights with block scales");
     if (m < 1 || m > p->max_m) return fail(HQ_ERR_INVALID_ARG, "m out of range [1, max_m]");
     const hq::Exec e = hq::choose_exec(p, m);
     const int64_t N = p->layer.n, K = p->layer.k;

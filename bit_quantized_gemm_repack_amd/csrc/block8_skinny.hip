@@ -1,0 +1,158 @@
+// fp8 x fp8 GEMM with 128-block scales, few rows: bound by reading the weight
+// once.  A workgroup owns NB 16-column blocks and 16 RB rows; its waves take
+// the 128-k groups of its K range in turn, weights straight from memory to
+// registers (no other wave needs them), ST groups of loads in flight per wave.
+// The waves' partial sums meet in LDS in wave order; with K split over
+// workgroups each stores fp32 partials for the reduce kernel, so results do
+// not depend on timing.
+#include <hip/hip_ext.h>
+#include <hip/hip_runtime.h>
+
+#include "block8.h"
+#include "block8_device.h"
+#include "launch.h"
+
+namespace hq {
+
+namespace {
+
+template <int RB, int NB, int ST, int MAXT>
+__global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(16))) f4_t red[];  // [waves][RB * NB][64]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  const int c16 = lane & 15, kq = lane >> 4;
+  const int N = p.N, K = p.K, G = p.G;
+  const int m0 = blockIdx.z * 16 * RB;
+  const int g0 = blockIdx.y * p.gps, g1 = min(G, g0 + p.gps);
+  const int nblocks = N / 16;
+  const int nb0 = blockIdx.x * NB;
+
+  auto rsrc = [](const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+  };
+  const int abytes = p.a_rows * K, sbytes = G * p.a_rows * 4;
+  const auto ra = rsrc(p.a, abytes);
+  const auto rs = rsrc(p.a_scale, sbytes);
+  const auto rw = rsrc(p.w, (int64_t)N * K);
+  const auto rws = rsrc(p.w_scale, (int64_t)((N + 127) / 128) * G * 4);
+  // rows past M load zeros without touching memory (offset past the range)
+  int aoff[RB], soff[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int m = m0 + 16 * b + c16;
+    aoff[b] = m < p.M ? m * K + kq * 16 : (int)0x80000000u;
+    soff[b] = m < p.M ? m * 4 : (int)0x80000000u;
+  }
+  int woff[NB], swoff[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int nb = min(nb0 + j, nblocks - 1);
+    woff[j] = nb * G * 2048 + lane * 16;
+    swoff[j] = (nb / 8) * G * 4;
+  }
+
+  u4_t wr[ST][NB][2], ar[ST][RB][2];
+  uint32_t sw[ST][NB], sa[ST][RB];
+  // Loads are issued without branches, so that the wait before each step's math
+  // is for that step's loads alone; steps past the end take offsets past the
+  // range, which read nothing.
+  auto issue = [&](int slot, int g) {
+    const int past = g < g1 ? 0 : (int)0x80000000u;
+    g = min(g, g1 - 1);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        wr[slot][j][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (woff[j] + 1024 * h) | past, g * 2048, 0));
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ar[slot][b][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (aoff[b] + 64 * h) | past, g * 128, 0));
+      sa[slot][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, soff[b] | past, g * p.a_rows * 4, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) sw[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(rws, swoff[j] | past, g * 4, 0);
+  };
+  f4_t acc[RB][NB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[b][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int s = 0; s < ST; ++s) issue(s, g0 + wave + s * waves);
+  for (int g = g0 + wave; g < g1; g += ST * waves) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      // a step past the end holds zero codes and zero scales: it adds nothing
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const f4_t P = b8_mfma(cat8(wr[s][j][0], wr[s][j][1]), cat8(ar[s][b][0], ar[s][b][1]));
+          const float f = __uint_as_float(sa[s][b]) * __uint_as_float(sw[s][j]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[b][j][q] = fmaf(f, P[q], acc[b][j][q]);
+        }
+      issue(s, g + (s + ST) * waves);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) red[(wave * RB * NB + b * NB + j) * 64 + lane] = acc[b][j];
+  __syncthreads();
+  for (int e = tid; e < RB * NB * 64; e += blockDim.x) {
+    f4_t v = red[e];
+    for (int w = 1; w < waves; ++w) {
+      const f4_t u = red[w * RB * NB * 64 + e];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += u[q];
+    }
+    const int l = e & 63, bj = e >> 6, b = bj / NB, j = bj - b * NB;
+    const int m = m0 + 16 * b + (l & 15), nb = nb0 + j;
+    if (m >= p.M || nb >= nblocks) continue;
+    const int n = nb * 16 + 4 * (l >> 4);
+    if (p.part) {
+      *reinterpret_cast<f4_t*>(p.part + ((int64_t)blockIdx.y * p.M + m) * N + n) = v;
+    } else {
+      auto cv = [&](float x) -> uint32_t { return p.out_bf16 ? float_to_bf16_bits(x) : float_to_f16_bits(x); };
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)m * N + n) =
+          uint2{cv(v[0]) | (cv(v[1]) << 16), cv(v[2]) | (cv(v[3]) << 16)};
+    }
+  }
+#endif
+}
+
+template <int RB, int NB, int ST, int MAXT>
+hipError_t launch_t(const B8Skinny& c, const B8Args& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N / 16 + NB - 1) / NB), (unsigned)c.split, (unsigned)((a.M + 16 * RB - 1) / (16 * RB)));
+  return launch_timed(b8_skinny<RB, NB, ST, MAXT>, grid, dim3(64 * c.waves), (size_t)c.waves * RB * NB * 1024, s, a);
+}
+
+}  // namespace
+
+bool b8_skinny_ok(const B8Skinny& c) {
+  if (c.rb != 1 && c.rb != 2 && c.rb != 4) return false;
+  if (c.nb != 1 && c.nb != 2) return false;
+  if (c.waves < 1 || c.waves > 16 || c.split < 1 || c.split > 64) return false;
+  return c.waves <= 8 || c.rb == 1;
+}
+
+int launch_b8_skinny(const B8Skinny& c, const B8Args& a, void* stream) {
+  if (!b8_skinny_ok(c) || a.G < 1 || a.gps < 1) return (int)hipErrorInvalidValue;
+  if ((int64_t)(c.split - 1) * a.gps >= a.G || (int64_t)c.split * a.gps < a.G) return (int)hipErrorInvalidValue;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (c.waves > 8) {
+    if (c.nb == 1) return (int)launch_t<1, 1, 4, 1024>(c, a, s);
+    return (int)launch_t<1, 2, 2, 1024>(c, a, s);
+  }
+  if (c.rb == 1) return c.nb == 1 ? (int)launch_t<1, 1, 8, 512>(c, a, s) : (int)launch_t<1, 2, 4, 512>(c, a, s);
+  if (c.rb == 2) return c.nb == 1 ? (int)launch_t<2, 1, 4, 512>(c, a, s) : (int)launch_t<2, 2, 4, 512>(c, a, s);
+  return c.nb == 1 ? (int)launch_t<4, 1, 3, 512>(c, a, s) : (int)launch_t<4, 2, 2, 512>(c, a, s);
+}
+
+}  // namespace hq

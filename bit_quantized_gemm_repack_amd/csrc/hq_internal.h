@@ -77,7 +77,8 @@ enum Fmt : int {
   FMT_MX4F16 = 12, // MXINT4 weight (E8M0 per 32 k), fp16 activation, fp16 MFMA
   FMT_MX4BF16 = 13, // MXINT4 weight (E8M0 per 32 k), bf16 activation, bf16 MFMA
   FMT_NV4F16 = 14,  // NVFP4 weight (E4M3 per 16 k + fp32 tensor scale), fp16 activation, fp16 MFMA
-  FMT_NV4BF16 = 15  // NVFP4 weight, bf16 activation, bf16 MFMA
+  FMT_NV4BF16 = 15, // NVFP4 weight, bf16 activation, bf16 MFMA
+  FMT_B8 = 16       // fp8 weight x fp8 activation, fp32 scales per 128 x 128 and per row and 128 k (block8.h)
 };
 
 // INT8 weights: stored as two 4-bit planes (high nibbles, then low nibbles)
@@ -109,7 +110,7 @@ HQ_HD constexpr inline bool f16_act(int fmt) {
 }
 // Weight bytes of one 16 x 128 fragment.
 HQ_HD constexpr inline int frag_bytes(int fmt) {
-  return w8_weights(fmt) ? 2048 : (w2_weights(fmt) ? 512 : (w3_weights(fmt) ? 768 : 1024));
+  return (w8_weights(fmt) || fmt == FMT_B8) ? 2048 : (w2_weights(fmt) ? 512 : (w3_weights(fmt) ? 768 : 1024));
 }
 
 // MXFP4 weights (E2M1 codes in natural order + E8M0 block scales).
@@ -316,7 +317,7 @@ HQ_HD inline int64_t e4m3_src_index(int64_t K, int64_t eidx) {
 enum KernelKind : int { KER_SKINNY = 1, KER_TILED = 2 };
 
 struct TiledCfgRt {
-  int bm;     // rows per workgroup tile (64, 128)
+  int bm;     // rows per workgroup tile (64, 128; FMT_B8: 16 .. 256)
   int nbw;    // 16-column blocks per wave (2, 4); tile width = 64 * nbw
   int split;   // K split over workgroups (dense; partials + reduce kernel)
   int stages;  // groups in the load pipeline (3; dense also 4, 5)

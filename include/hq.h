@@ -52,6 +52,10 @@
  *               k in [G*g, G*g+G).
  *       zeros   uint8 [N, K/G] holding 0..15 (only with HQ_ZP_PER_GROUP_U4).
  *       e8m0    uint8 [N, K/32] (MXFP4, MXINT4): scale 2^(X-127) per 32 k.
+ *       FP8     codes uint8 e4m3 [N, K], one byte per weight; scales fp32
+ *               [ceil(N/128), K/128]: scale (i, j) covers n in [128 i, 128 i +
+ *               128) (the last one N's rest) and k in [128 j, 128 j + 128);
+ *               w = e4m3(q) * s.
  *       NVFP4   codes as MXFP4 (E2M1); block scales uint8 E4M3 [N, K/16],
  *               one per 16 k, passed where the zero points go; the fp32
  *               tensor scale (one float per expert) passed as `scales`.
@@ -113,7 +117,8 @@ typedef enum hq_zp_mode {
 typedef enum hq_ascale_mode {
   HQ_ASCALE_NONE = 0,         /* 16-bit activations, no scale        */
   HQ_ASCALE_PER_TOKEN_F32 = 1, /* 8-bit codes with one fp32 per row  */
-  HQ_ASCALE_MX_E8M0 = 2        /* MXFP4 codes with an E8M0 scale per row and 32-element block */
+  HQ_ASCALE_MX_E8M0 = 2,       /* MXFP4 codes with an E8M0 scale per row and 32-element block */
+  HQ_ASCALE_BLOCK_F32 = 3      /* fp8 codes with one fp32 scale per row and 128 k */
 } hq_ascale_mode;
 
 /* The unified quantisation description: weight codes, scales, zero points
@@ -148,6 +153,10 @@ typedef enum hq_ascale_mode {
  *              act FP4_E2M1, act_scale MX_E8M0, out F16|BF16 (dense only;
  *              W4A4 and MXFP4 are among the supported combinations and
  *              formats of cocoloop.cn, format section)
+ *   W8A8-BLOCK w_elem FP8_E4M3 (w_bits 8), group 128, scale F32 (one per
+ *              128 n x 128 k), zp NONE, act FP8_E4M3, act_scale BLOCK_F32
+ *              (one per row and 128 k), out F16|BF16; dense, and grouped as
+ *              SILU_MUL_QFP8 / TOPK_COMBINE
  * Anything else returns HQ_ERR_UNSUPPORTED from hq_plan_create. */
 typedef struct hq_quant_desc {
   hq_dtype w_elem;
@@ -292,7 +301,9 @@ hq_status hq_repack_host(const hq_plan* plan, const void* codes, const void* sca
  *            bytes) the E8M0 block scales as group-major words uint8
  *            [K/128][m][4], byte j of word (g, r) scaling k-block 4g + j of
  *            row r (so that the 16 rows of one MFMA operand are 64
- *            contiguous bytes); else NULL
+ *            contiguous bytes); for fp8 activations with block scales
+ *            (W8A8-BLOCK) fp32 [K/128][m], one scale per row and 128 k, as
+ *            hq_quantize_blocks writes them; else NULL
  *   w, meta  device, produced by hq_repack
  *   out      device [m, N] in the plan's out dtype; with HQ_EPI_I32_ACC
  *            (W4A8-INT only) int32 [m, N, K/128] holding
@@ -455,6 +466,25 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* plan, int64_t t, int topk, const vo
  * quantisation fused into its epilogue (HQ_EPI_SILU_MUL_QFP8). */
 hq_status hq_quantize_per_token(int64_t m, int64_t k, hq_dtype in, hq_dtype out, const void* x, void* codes,
                                 float* scales, void* stream);
+
+/* Block quantiser: the (a, a_scale) pair of a W8A8-BLOCK GEMM.  A block is 128
+ * consecutive values of a row:
+ *   scales[k/128][r] = max |v| / 448 over the block, computed in fp32 (1 where
+ *                      that is zero)
+ *   codes[r, j]      = v / scale, the correctly rounded fp32 quotient, rounded
+ *                      to the nearest e4m3fn value (ties to even), at most
+ *                      448 in size (-0 gives code 0)
+ * with v = x[r, j], or with silu_mul = 1 v = SiLU(x[r, j]) * x[r, k + j] formed
+ * in fp32, x then being the [m, 2k] output of a gate_up GEMM.  A block that
+ * holds an infinity or a NaN gets a NaN scale, so that the GEMM's row is NaN.
+ *   x       device [m, k] or [m, 2k] fp16 / bf16 (in = HQ_F16 / HQ_BF16)
+ *   codes   device [m, k] bytes, fully overwritten
+ *   scales  device fp32 [k/128, m], fully overwritten
+ * k must be a multiple of 128 (at most 2^24), m at most 2^24 and m * k / 128
+ * below 2^31 - 16; m = 0 is a no-op.  x, codes and scales must not overlap.
+ * Honours hq_time_next_launch (one kernel). */
+hq_status hq_quantize_blocks(int64_t m, int64_t k, hq_dtype in, int silu_mul, const void* x, void* codes,
+                             float* scales, void* stream);
 
 /* MXFP4 block quantiser for W4A4 activations (W4A4 and MXFP4: cocoloop.cn,
  * format section), following the OCP Microscaling v1.0 conversion of a block
