@@ -205,6 +205,13 @@ _SIGS = {
     "hq_quantize_per_token": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int] +
                               [ctypes.c_void_p] * 4),
     "hq_quantize_mxfp4": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p] * 4),
+    "hq_route_topk": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                     ctypes.c_int] + [ctypes.c_void_p] * 3),
+    "hq_moe_few_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                                  ctypes.POINTER(ctypes.c_size_t)]),
+    "hq_moe_layer_few": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int] +
+                         [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
     "hq_quantize_blocks": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int] +
                            [ctypes.c_void_p] * 4),
     "hq_plan_autotune": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 6 +
@@ -279,6 +286,7 @@ def _stream_ptr(device) -> int:
 
 
 _TORCH_OUT = {F16: torch.float16, BF16: torch.bfloat16}
+_LOGITS = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _DT_NAME = {F16: "f16", BF16: "bf16", FP8_E4M3: "fp8", INT8: "int8", FP4_E2M1: "mxfp4"}
 
 
@@ -845,13 +853,75 @@ def moe_uses_by_slot(t: int, topk: int, fp8: bool = False) -> bool:
     return 0 < int(t) * int(topk) <= limit
 
 
+def route_topk(logits: torch.Tensor, topk: int, renormalize: bool = True):
+    """The topk experts of each row of logits [t, experts] (fp32, fp16 or bf16)
+    and their softmax weights (see hq_route_topk): (ids int32 [t, topk],
+    weights float32 [t, topk]), the (topk_ids, topk_w) of moe_layer."""
+    _dev(logits, "logits")
+    if logits.dim() != 2 or logits.dtype not in _LOGITS:
+        raise ValueError("logits must be fp32 / fp16 / bf16 [t, experts]")
+    t, experts = logits.shape
+    ids = torch.empty((t, int(topk)), dtype=torch.int32, device=logits.device)
+    w = torch.empty((t, int(topk)), dtype=torch.float32, device=logits.device)
+    _check(lib().hq_route_topk(t, experts, int(topk), _LOGITS[logits.dtype], logits.data_ptr(), 1 if renormalize else 0,
+                               ids.data_ptr(), w.data_ptr(), _stream_ptr(logits.device)))
+    return ids, w
+
+
+# Tokens up to which a w8a8_block layer runs in two kernels (hq_moe_layer_few).
+MOE_FEW_MAX_TOKENS = 16
+
+
+def _uses_few(gate_up: "MoePlan", t: int, topk: int) -> bool:
+    return gate_up._block8 and 0 < t <= MOE_FEW_MAX_TOKENS and topk <= 16 and gate_up.k <= 98304
+
+
+def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2):
+    for v, nm in ((x, "x"), (ids, "topk_ids"), (w, "topk_w"), (w1, "w1"), (m1, "m1"), (w2, "w2"), (m2, "m2")):
+        if _dev(v, nm).device != x.device:
+            raise ValueError(f"{nm} must be on x's device")
+    t = x.shape[0]
+    if x.dim() != 2 or x.shape[1] != gate_up.k or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x must be fp16 / bf16 [t, {gate_up.k}]")
+    if ids.shape != (t, topk) or ids.dtype != torch.int32 or w.shape != (t, topk) or w.dtype != torch.float32:
+        raise ValueError(f"topk_ids / topk_w must be int32 / float32 [{t}, {topk}]")
+    ws = torch.empty(t * topk * down.k, dtype=torch.float32, device=x.device)
+    out = torch.empty((t, down.n), dtype=_TORCH_OUT[down.quant.out], device=x.device)
+    _check(lib().hq_moe_layer_few(gate_up._h, down._h, t, topk, BF16 if x.dtype == torch.bfloat16 else F16,
+                                  x.data_ptr(), F32 if logits is None else _LOGITS[logits.dtype], _ptr(logits),
+                                  1 if renormalize else 0, ids.data_ptr(), w.data_ptr(), w1.data_ptr(), m1.data_ptr(),
+                                  w2.data_ptr(), m2.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel() * 4,
+                                  _stream_ptr(x.device)))
+    return out
+
+
+def moe_layer_routed(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, logits: torch.Tensor, topk: int,
+                     w1: torch.Tensor, m1: torch.Tensor, w2: torch.Tensor, m2: torch.Tensor, renormalize: bool = True):
+    """An MoE layer from the router's logits [t, experts] on: (y [t, n_down],
+    topk_ids, topk_w).  w8a8_block plans run a few tokens in two kernels
+    (hq_moe_layer_few); otherwise route_topk, then moe_layer."""
+    _dev(logits, "logits")
+    topk = int(topk)
+    if logits.dim() != 2 or logits.shape != (x.shape[0], gate_up.num_experts) or logits.dtype not in _LOGITS or \
+            logits.device != x.device:
+        raise ValueError(f"logits must be fp32 / fp16 / bf16 [{x.shape[0]}, {gate_up.num_experts}] on x's device")
+    if _uses_few(gate_up, x.shape[0], topk) and gate_up.num_experts <= 1024:
+        ids = torch.empty((x.shape[0], topk), dtype=torch.int32, device=x.device)
+        w = torch.empty((x.shape[0], topk), dtype=torch.float32, device=x.device)
+        return _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2), ids, w
+    ids, w = route_topk(logits, topk, renormalize)
+    return moe_layer(gate_up, down, x, ids, w, w1, m1, w2, m2), ids, w
+
+
 def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
               w1: torch.Tensor, m1: torch.Tensor, w2: torch.Tensor, m2: torch.Tensor, x_scale=None,
               by_slot: Optional[bool] = None) -> torch.Tensor:
     """One MoE layer, y [t, n_down]: gate_up (SiLU * up, or with the fp8
     requant) then down with the top-k combine, on the by-slot path for
     decode-sized calls (moe_uses_by_slot) and the aligned path otherwise;
-    `by_slot` forces one.  x: [t, k] activations (fp8 codes with x_scale for
+    `by_slot` forces one.  w8a8_block plans take 16-bit x (quantised here, or
+    inside the two kernels that few tokens run in) or the codes and scales of
+    quantize_blocks, and always the aligned path beyond.  x: [t, k] activations (fp8 codes with x_scale for
     W4A8); topk_ids int32 / topk_w fp32 [t, topk] on the GPU."""
     t, topk = topk_ids.shape
     if down.epi != EPI_TOPK_COMBINE or gate_up.epi not in (EPI_SILU_MUL, EPI_SILU_MUL_QFP8):
@@ -860,6 +930,8 @@ def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: to
     if gate_up._block8:
         if by_slot:
             raise ValueError("w8a8_block layers have no by-slot path")
+        if x_scale is None and _uses_few(gate_up, t, topk):
+            return _moe_few(gate_up, down, x, topk, topk_ids, topk_w, None, False, w1, m1, w2, m2)
         by_slot = False
         if x_scale is None:
             x, x_scale = quantize_blocks(x)

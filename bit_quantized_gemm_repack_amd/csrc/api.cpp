@@ -1500,6 +1500,119 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* p, int64_t t, int topk, const void*
   }
 }
 
+static int logit_type_of(hq_dtype t) { return t == HQ_F32 ? 0 : (t == HQ_BF16 ? 1 : (t == HQ_F16 ? 2 : -1)); }
+
+hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, int renormalize,
+                        int32_t* topk_ids, float* topk_w, void* stream) {
+  const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
+  const int lt = logit_type_of(logit_type);
+  if (lt < 0) return fail(HQ_ERR_UNSUPPORTED, "logits must be fp32, fp16 or bf16");
+  if (t < 0 || t > (int64_t(1) << 24)) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, 2^24]");
+  if (num_experts < 1) return fail(HQ_ERR_INVALID_ARG, "num_experts must be >= 1");
+  if (num_experts > 1024) return fail(HQ_ERR_UNSUPPORTED, "routing covers up to 1024 experts");
+  if (topk < 1 || topk > 64 || topk > num_experts) return fail(HQ_ERR_INVALID_ARG, "topk must be 1..min(64, experts)");
+  if (renormalize != 0 && renormalize != 1) return fail(HQ_ERR_INVALID_ARG, "renormalize must be 0 or 1");
+  if (t == 0) return ok();
+  if (!logits || !topk_ids || !topk_w) return fail(HQ_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_w))
+    return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  hq::arm_timing(ev);
+  const int err = hq::launch_route(t, num_experts, topk, lt, logits, renormalize, topk_ids, topk_w, stream);
+  hq::arm_timing({nullptr, nullptr});
+  if (err != hipSuccess) return fail(HQ_ERR_HIP, "route launch: %s", hipGetErrorString((hipError_t)err));
+  return ok();
+}
+
+// The checks hq_moe_few_workspace_bytes and hq_moe_layer_few share.
+static hq_status few_check(const hq_plan* gu, const hq_plan* dn, int64_t t, int topk) {
+  if (!gu || !dn) return fail(HQ_ERR_INVALID_ARG, "null plan");
+  if (gu->fmt != hq::FMT_B8 || dn->fmt != hq::FMT_B8 || gu->compute.kind != HQ_GEMM_GROUPED ||
+      dn->compute.kind != HQ_GEMM_GROUPED)
+    return fail(HQ_ERR_UNSUPPORTED, "the two-kernel layer takes grouped plans of fp8 weights with block scales");
+  if (gu->compute.epi != HQ_EPI_SILU_MUL_QFP8 || dn->compute.epi != HQ_EPI_TOPK_COMBINE)
+    return fail(HQ_ERR_INVALID_ARG, "the layer takes a gate_up (SILU_MUL_QFP8) and a down (TOPK_COMBINE) plan");
+  if (gu->layer.num_experts != dn->layer.num_experts || gu->layer.n != 2 * dn->layer.k || gu->layer.k != dn->layer.n)
+    return fail(HQ_ERR_INVALID_ARG, "gate_up must be [2 I, H] and down [H, I] over the same experts");
+  if (t < 0 || t > gu->max_m || t > dn->max_m) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, max_m]");
+  if (topk < 1) return fail(HQ_ERR_INVALID_ARG, "topk must be at least 1");
+  if (t > hq::kB8FewMaxTokens || topk > hq::kB8FewMaxTopk)
+    return fail(HQ_ERR_UNSUPPORTED, "the two-kernel layer covers up to %d tokens and topk %d", hq::kB8FewMaxTokens,
+                hq::kB8FewMaxTopk);
+  const int64_t H = gu->layer.k, I = dn->layer.k;
+  if (gu->layer.num_experts > 4096) return fail(HQ_ERR_UNSUPPORTED, "more than 4096 experts");
+  if (H > 98304) return fail(HQ_ERR_UNSUPPORTED, "H above 98304 does not fit a workgroup's LDS");
+  if (t * topk * I * 4 >= (int64_t(1) << 31) || (int64_t)gu->w_bytes_per_expert >= (int64_t(1) << 31))
+    return fail(HQ_ERR_UNSUPPORTED, "the intermediate and one expert's weights must each stay below 2 GiB");
+  return HQ_OK;
+}
+
+hq_status hq_moe_few_workspace_bytes(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, size_t* bytes) {
+  if (!bytes) return fail(HQ_ERR_INVALID_ARG, "null argument");
+  hq_status s = few_check(gate_up, down, t, topk);
+  if (s != HQ_OK) return s;
+  *bytes = align256((size_t)t * (size_t)topk * (size_t)down->layer.k * 4);
+  return ok();
+}
+
+hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, hq_dtype x_type,
+                           const void* x, hq_dtype logit_type, const void* logits, int renormalize, int32_t* topk_ids,
+                           float* topk_w, const void* w1, const void* meta1, const void* w2, const void* meta2,
+                           void* out, void* ws, size_t ws_bytes, void* stream) {
+  const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
+  hq_status st = few_check(gate_up, down, t, topk);
+  if (st != HQ_OK) return st;
+  const int lt = logits ? logit_type_of(logit_type) : 0;
+  if (lt < 0) return fail(HQ_ERR_UNSUPPORTED, "logits must be fp32, fp16 or bf16");
+  if (x_type != HQ_F16 && x_type != HQ_BF16) return fail(HQ_ERR_UNSUPPORTED, "x must be fp16 or bf16");
+  if (renormalize != 0 && renormalize != 1) return fail(HQ_ERR_INVALID_ARG, "renormalize must be 0 or 1");
+  const int E = gate_up->layer.num_experts;
+  if (logits && E > 1024) return fail(HQ_ERR_UNSUPPORTED, "routing covers up to 1024 experts");
+  if (logits && topk > E) return fail(HQ_ERR_INVALID_ARG, "topk above the number of experts");
+  if (t == 0) return ok();
+  if (!x || !topk_ids || !topk_w || !w1 || !meta1 || !w2 || !meta2 || !out)
+    return fail(HQ_ERR_INVALID_ARG, "null device pointer");
+  for (const void* p : {x, (const void*)logits, (const void*)topk_ids, (const void*)topk_w, w1, meta1, w2, meta2, (const void*)out})
+    if (!aligned16(p)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  const int64_t H = gate_up->layer.k, I = down->layer.k;
+  const size_t need = (size_t)t * (size_t)topk * (size_t)I * 4;
+  if (!ws || ws_bytes < need) return fail(HQ_ERR_WORKSPACE, "this call needs %zu workspace bytes", need);
+  if (!aligned16(ws)) return fail(HQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  hq::B8FewArgs a{};
+  a.x = x;
+  a.logits = logits;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  a.w1 = static_cast<const uint8_t*>(w1);
+  a.s1 = static_cast<const float*>(meta1);
+  a.w2 = static_cast<const uint8_t*>(w2);
+  a.s2 = static_cast<const float*>(meta2);
+  a.act = static_cast<float*>(ws);
+  a.out = out;
+  a.w1_expert = (int64_t)gate_up->w_bytes_per_expert;
+  a.s1_expert = (int64_t)(gate_up->meta_bytes_per_expert / 4);
+  a.w2_expert = (int64_t)down->w_bytes_per_expert;
+  a.s2_expert = (int64_t)(down->meta_bytes_per_expert / 4);
+  a.t = (int)t;
+  a.topk = topk;
+  a.E = E;
+  a.H = (int)H;
+  a.I = (int)I;
+  a.x_bf16 = x_type == HQ_BF16;
+  a.out_bf16 = down->layer.q.out == HQ_BF16;
+  a.logit_type = lt;
+  a.renorm = renormalize;
+  a.rows = hq::b8_few_rows(t, H);
+  hq::arm_timing({ev.start, nullptr});
+  int err = hq::launch_few_gate_up(a, stream);
+  if (err == hipSuccess) {
+    hq::arm_timing({nullptr, ev.stop});
+    err = hq::launch_few_down(a, stream);
+  }
+  hq::arm_timing({nullptr, nullptr});
+  if (err != hipSuccess) return fail(HQ_ERR_HIP, "layer launch: %s", hipGetErrorString((hipError_t)err));
+  return ok();
+}
+
 hq_status hq_quantize_per_token(int64_t m, int64_t k, hq_dtype in, hq_dtype out, const void* x, void* codes,
                                 float* scales, void* stream) {
   const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens

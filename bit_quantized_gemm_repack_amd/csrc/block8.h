@@ -70,6 +70,35 @@ int launch_b8_repack(int64_t N, int64_t K, int64_t E, const void* codes, const v
 int launch_quantize_blocks(int64_t m, int64_t k, int in_bf16, int silu, const void* x, void* codes, float* scales,
                            void* stream);
 
+// Routing: softmax top-k of each row of logits [t][E] (logit_type 0 fp32, 1
+// bf16, 2 fp16), E <= 1024, topk <= 64.
+int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits, int renorm, int32_t* ids, float* w,
+                 void* stream);
+
+// An experts' layer for a few tokens in two kernels (block8_moe.hip).
+constexpr int kB8FewMaxTokens = 64;
+constexpr int kB8FewMaxTopk = 16;
+constexpr int kB8FewMaxSlots = kB8FewMaxTokens * kB8FewMaxTopk;
+struct B8FewArgs {
+  const void* x;        // [t][H]
+  const void* logits;   // [t][E], or null: topk_ids and topk_w are given
+  int32_t* topk_ids;    // [t][topk]
+  float* topk_w;
+  const uint8_t* w1;    // device layout, 2I x H per expert
+  const float* s1;
+  const uint8_t* w2;    // H x I per expert
+  const float* s2;
+  float* act;           // [t * topk][I]
+  void* out;            // [t][H]
+  int64_t w1_expert, s1_expert, w2_expert, s2_expert;
+  int t, topk, E, H, I;
+  int x_bf16, out_bf16, logit_type, renorm;
+  int rows;             // rows of x a gate_up workgroup holds (b8_few_rows)
+};
+int b8_few_rows(int64_t t, int64_t K);
+int launch_few_gate_up(const B8FewArgs& a, void* stream);
+int launch_few_down(const B8FewArgs& a, void* stream);
+
 // One 32-bit word of the device layout <- canonical uint8 [N][K].
 HQ_HD inline uint32_t repack_word_b8(const uint8_t* codes, int64_t K, int64_t widx) {
   const int64_t G = K / kFragK;

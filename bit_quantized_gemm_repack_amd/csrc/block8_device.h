@@ -13,19 +13,30 @@ __device__ inline f4_t b8_mfma(i8_t w, i8_t a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
+// The quotients v / s of one block: the reciprocal once, then a product and one
+// correction step per value, v r + r (v - s (v r)), which is the correctly
+// rounded quotient for every pair of 16-bit values behind v and s (checked
+// exhaustively), a third of the instructions of a division.  Scales near the
+// ends of the exponent range, where the reciprocal or the remainder would
+// leave it, divide.
+struct B8Div {
+  float s, r;
+  bool plain;
+  __device__ inline explicit B8Div(float scale) : s(scale), r(1.f / scale), plain(!(scale > 0x1p-90f && scale < 0x1p90f)) {}
+  __device__ inline float operator()(float v) const {
+    if (plain) return v / s;
+    const float q = v * r;
+    return fmaf(fmaf(-q, s, v), r, q);
+  }
+};
+
 // Four fp32 values over their block's scale -> e4m3 codes, little-endian:
-// the correctly rounded quotient, rounded to nearest even and saturated at
-// 448 (-0 gives code 0, as in the per-token quantiser); NaN gives NaN.
-__device__ inline uint32_t b8_codes(float v0, float v1, float v2, float v3, float s) {
-  auto q = [&](float v) {
-    const float x = v / s;
-    return x != x ? x : __builtin_amdgcn_fmed3f(x, 448.f, -448.f);
-  };
+// rounded to nearest even, at most 448 in size.
+__device__ inline uint32_t b8_codes(float v0, float v1, float v2, float v3, const B8Div& d) {
+  auto q = [&](float v) { return __builtin_amdgcn_fmed3f(d(v), 448.f, -448.f); };
   int t = __builtin_amdgcn_cvt_pk_fp8_f32(q(v0), q(v1), 0, false);
   t = __builtin_amdgcn_cvt_pk_fp8_f32(q(v2), q(v3), t, true);
-  const uint32_t u = (uint32_t)t;
-  const uint32_t nz = ((u & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u;
-  return u & (0x7F7F7F7Fu | nz);
+  return (uint32_t)t;
 }
 
 // The scale of a block from its largest magnitude: max / 448, 1 where that is
@@ -43,5 +54,23 @@ __device__ inline float b8_scale(uint32_t top_bits) {
 __device__ inline uint32_t b8_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 __device__ inline float b8_silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Maximum over the 16 lanes of a row, in every lane.
+__device__ inline uint32_t b8_row_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));  // row_ror:8
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
+  return v;
+}
+
+template <bool BF16>
+__device__ inline void b8_unpack(u4_t x, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = (j & 1) ? x[j >> 1] >> 16 : x[j >> 1] & 0xFFFFu;
+    v[j] = BF16 ? bf16_bits_to_float(b) : f16_bits_to_float(b);
+  }
+}
 
 }  // namespace hq

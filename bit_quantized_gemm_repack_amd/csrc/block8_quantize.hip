@@ -21,24 +21,6 @@ namespace hq {
 
 namespace {
 
-// Maximum over the 16 lanes of a row, in every lane.
-__device__ inline uint32_t row_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));  // row_ror:8
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
-  return v;
-}
-
-template <bool BF16>
-__device__ inline void unpack(u4_t x, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = (j & 1) ? x[j >> 1] >> 16 : x[j >> 1] & 0xFFFFu;
-    v[j] = BF16 ? bf16_bits_to_float(b) : f16_bits_to_float(b);
-  }
-}
-
 template <bool BF16, bool SILU>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const u4_t* __restrict__ x, uint32_t m, uint32_t k8,
                                                               uint32_t blocks, uint2* __restrict__ codes,
@@ -52,18 +34,19 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const u4_t* __rest
     const u4_t* r = x + (int64_t)row * 2 * k8 + c;
     const u4_t xg = __builtin_nontemporal_load(r), xu = __builtin_nontemporal_load(r + k8);
     float u[8];
-    unpack<BF16>(xg, v);
-    unpack<BF16>(xu, u);
+    b8_unpack<BF16>(xg, v);
+    b8_unpack<BF16>(xu, u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = b8_silu_mul(v[j], u[j]);
   } else {
-    unpack<BF16>(__builtin_nontemporal_load(x + (int64_t)row * k8 + c), v);
+    b8_unpack<BF16>(__builtin_nontemporal_load(x + (int64_t)row * k8 + c), v);
   }
   uint32_t top = 0u;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = max(top, b8_mag(v[j]));
-  const float s = b8_scale(row_max(top));
-  codes[(int64_t)row * k8 + c] = uint2{b8_codes(v[0], v[1], v[2], v[3], s), b8_codes(v[4], v[5], v[6], v[7], s)};
+  const float s = b8_scale(b8_row_max(top));
+  const B8Div d(s);
+  codes[(int64_t)row * k8 + c] = uint2{b8_codes(v[0], v[1], v[2], v[3], d), b8_codes(v[4], v[5], v[6], v[7], d)};
   if ((threadIdx.x & 15) == 0) scales[i] = s;
 }
 

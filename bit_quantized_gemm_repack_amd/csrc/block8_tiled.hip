@@ -250,10 +250,11 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
       const float s = b8_scale(max(max(red[rl], red[C::BM + rl]), max(red[2 * C::BM + rl], red[3 * C::BM + rl])));
       if (p.sorted_ids[m0 + rl] >= p.n_slots) continue;
       const int64_t row = m0 + rl;
+      const B8Div d(s);
 #pragma unroll
       for (int j = 0; j < NB / 2; ++j)
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * (N / 2) + nblk(j) * 16 + 4 * kq) =
-            b8_codes(acc[mb][j][0], acc[mb][j][1], acc[mb][j][2], acc[mb][j][3], s);
+            b8_codes(acc[mb][j][0], acc[mb][j][1], acc[mb][j][2], acc[mb][j][3], d);
       if (wn == 0 && kq == 0) p.out_scale[(int64_t)tn * p.out_rows + row] = s;
     }
   } else {
@@ -295,13 +296,9 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
 template <int MB, int NB, int WM, int ST, int MODE>
 hipError_t launch_t(const B8Args& a, dim3 grid, hipStream_t s) {
   using C = B8Cfg<MB, NB, WM, ST>;
-  auto kern = b8_tiled<MB, NB, WM, ST, MODE>;
-  if (C::LDS > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
-    if (e != hipSuccess) return e;
-  }
-  return launch_timed(kern, grid, dim3(C::THREADS), (size_t)C::LDS, s, a);
+  const hipError_t e = allow_lds<b8_tiled<MB, NB, WM, ST, MODE>>(C::LDS);
+  if (e != hipSuccess) return e;
+  return launch_timed(b8_tiled<MB, NB, WM, ST, MODE>, grid, dim3(C::THREADS), (size_t)C::LDS, s, a);
 }
 
 template <int MODE>

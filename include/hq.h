@@ -385,6 +385,12 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  *                             forms; after the call the first
  *                             max_padded * n/2 * 4 bytes of ws hold those
  *                             fp32 rows (rows of padding slots unspecified).
+ *                             W8A8-BLOCK plans requantise by row and 128
+ *                             columns inside the GEMM's tile (the rule of
+ *                             hq_quantize_blocks): out_scale = fp32 [n/256]
+ *                             [max_padded], no workspace; a_scale is fp32
+ *                             [k/128][t] for gate_up, [k/128][max_padded] for
+ *                             down.
  *   epi HQ_EPI_TOPK_COMBINE   down: row r of `a` [max_padded, k] is the
  *                             intermediate of slot sorted_ids[r];
  *                             out = y [t, n] (plan out dtype),
@@ -444,6 +450,43 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* plan, int64_t t, int topk, const vo
                               const int32_t* topk_ids, const float* topk_w, const void* w, const void* meta,
                               void* out, float* out_scale, void* ws, size_t ws_bytes, void* stream);
 
+/* Routing: the topk experts of largest logit of each row of logits [t,
+ * num_experts] (fp32, fp16 or bf16), in falling order, ties to the lowest
+ * index, with the weights softmax(logits)[expert], or (renormalize = 1) those
+ * over the chosen ones' sum.  Logits of -inf (experts shut off) and NaN are
+ * never chosen and add nothing to the softmax: a row with fewer than topk
+ * others ends in ids of -1 with weight 0.  A logit of +inf gives unspecified
+ * weights.  topk_ids int32 and topk_w fp32 [t, topk], fully overwritten, as
+ * hq_moe_align / hq_moe_gemm take them.  num_experts <= 1024, topk <= 64,
+ * t <= 2^24; t = 0 is a no-op.  Honours hq_time_next_launch (one kernel). */
+hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, int renormalize,
+                        int32_t* topk_ids, float* topk_w, void* stream);
+
+/* A whole experts' layer of fp8 weights with block scales (W8A8-BLOCK plans:
+ * gate_up [2 I, H] with SILU_MUL_QFP8, down [H, I] with TOPK_COMBINE, the same
+ * experts) for a few tokens, in two kernels: routing, the block quantisation
+ * of x, gate_up and SiLU * mul in the first; the block quantisation of the
+ * activation, down and the top-k sum in the second.
+ *   x         device [t, H] fp16 / bf16 (x_type)
+ *   logits    device [t, num_experts]: topk_ids and topk_w (device [t, topk])
+ *             are outputs, as hq_route_topk writes them; or NULL: they are
+ *             inputs (ids outside [0, num_experts) contribute zero, an id may
+ *             come twice in a row)
+ *   out       device [t, H] in the down plan's out dtype
+ *   ws        hq_moe_few_workspace_bytes bytes; holds the fp32 activations
+ *             [t * topk, I] between the kernels, no initialisation needed; two
+ *             calls that overlap in time must not share one
+ * The activations are rounded where hq_quantize_blocks and the grouped gate_up
+ * round them, and the sum over a token's experts is one fp32 accumulator
+ * rounded once.  Deterministic.  t <= 64, topk <= 16, num_experts <= 4096
+ * (1024 with logits), H <= 98304; t = 0 is a no-op.  Honours
+ * hq_time_next_launch (first kernel to last). */
+hq_status hq_moe_few_workspace_bytes(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, size_t* bytes);
+hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, hq_dtype x_type,
+                           const void* x, hq_dtype logit_type, const void* logits, int renormalize, int32_t* topk_ids,
+                           float* topk_w, const void* w1, const void* meta1, const void* w2, const void* meta2,
+                           void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Per-token activation quantiser: the step before a W4A8 GEMM, which takes
  * 8-bit activations with one fp32 scale per row (W4A8: INT8 or FP8
@@ -473,10 +516,11 @@ hq_status hq_quantize_per_token(int64_t m, int64_t k, hq_dtype in, hq_dtype out,
  *                      that is zero)
  *   codes[r, j]      = v / scale, the correctly rounded fp32 quotient, rounded
  *                      to the nearest e4m3fn value (ties to even), at most
- *                      448 in size (-0 gives code 0)
+ *                      448 in size
  * with v = x[r, j], or with silu_mul = 1 v = SiLU(x[r, j]) * x[r, k + j] formed
  * in fp32, x then being the [m, 2k] output of a gate_up GEMM.  A block that
- * holds an infinity or a NaN gets a NaN scale, so that the GEMM's row is NaN.
+ * holds an infinity or a NaN gets a NaN scale (and unspecified codes), so that
+ * the GEMM's row is NaN.
  *   x       device [m, k] or [m, 2k] fp16 / bf16 (in = HQ_F16 / HQ_BF16)
  *   codes   device [m, k] bytes, fully overwritten
  *   scales  device fp32 [k/128, m], fully overwritten
