@@ -282,7 +282,9 @@ def _dev(t: torch.Tensor, name: str):
 
 
 def _stream_ptr(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream of `device` (the raw handle: a Stream object costs
+    more than the rest of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
 
 
 _TORCH_OUT = {F16: torch.float16, BF16: torch.bfloat16}

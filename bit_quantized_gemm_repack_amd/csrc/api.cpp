@@ -1601,7 +1601,10 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
   a.out_bf16 = down->layer.q.out == HQ_BF16;
   a.logit_type = lt;
   a.renorm = renormalize;
-  a.rows = hq::b8_few_rows(t, H);
+  if (t > 8) {  // the wide gate_up writes codes, and scales behind them
+    a.act_codes = static_cast<uint8_t*>(ws);
+    a.act = reinterpret_cast<float*>(a.act_codes + t * topk * I);
+  }
   hq::arm_timing({ev.start, nullptr});
   int err = hq::launch_few_gate_up(a, stream);
   if (err == hipSuccess) {

@@ -88,14 +88,15 @@ struct B8FewArgs {
   const float* s1;
   const uint8_t* w2;    // H x I per expert
   const float* s2;
-  float* act;           // [t * topk][I]
+  float* act;           // fp32 rows [t * topk][I], or with act_codes their scales [t * topk][I/128]
+  uint8_t* act_codes;   // [t * topk][I], or null
   void* out;            // [t][H]
   int64_t w1_expert, s1_expert, w2_expert, s2_expert;
   int t, topk, E, H, I;
   int x_bf16, out_bf16, logit_type, renorm;
-  int rows;             // rows of x a gate_up workgroup holds (b8_few_rows)
+  int rows;             // rows of x a gate_up workgroup holds (set by its launcher)
+  int down_groups;      // 128-k groups a down workgroup holds (set by its launcher)
 };
-int b8_few_rows(int64_t t, int64_t K);
 int launch_few_gate_up(const B8FewArgs& a, void* stream);
 int launch_few_down(const B8FewArgs& a, void* stream);
 

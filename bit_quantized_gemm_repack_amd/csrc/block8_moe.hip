@@ -148,112 +148,99 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
 }
 
 // ---------------------------------------------------------------------------
-// gate_up: grid (16-column blocks of the outputs, slots); 8 waves over K
+// gate_up.  A workgroup row per slot; the first of the slots that share an
+// expert does the work for all of them.  Two shapes:
+//   narrow  16 outputs a workgroup, its waves share K (their sums meet in
+//           LDS); the fp32 rows are quantised by the down kernel.  For one or
+//           two tokens, whose few experts would leave most CUs idle otherwise.
+//   wide    128 outputs a workgroup, 16 a wave over all of K: no sums to join,
+//           and the workgroup holds a whole scale block, so that it writes
+//           codes and scales.  The routing above the stream is paid an eighth
+//           as often.
+// With logits one more block column writes the routing.
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8;
-constexpr int kFewLds = 128 * 1024;  // most dynamic LDS of a gate_up workgroup
+constexpr int kFewWaves = 8;  // of a down workgroup
+constexpr int kFewLds = 128 * 1024;  // most dynamic LDS of a workgroup
 
-template <int NPL, bool BF16>
-__global__ void __launch_bounds__(64 * kFewWaves) few_gate_up(B8FewArgs p) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ f4_t red[kFewWaves][2][64];
-  __shared__ int picks[kB8FewMaxSlots];  // slots that share this one's expert, in order
-  __shared__ int npicks;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c16 = lane & 15, kq = lane >> 4;
-  const int z = blockIdx.y, topk = p.topk, T = p.t, E = p.E, K = p.H, G = K / 128;
-  const int tok = z / topk;
-
-  // ---- the slot's expert -------------------------------------------------------
+// The routing of slot z, for the down kernel and the caller (one wave).
+template <int NPL>
+__device__ inline void few_write_routing(const B8FewArgs& p, int z, int lane) {
+  const int tok = z / p.topk;
+  Logits<NPL> r;
+  r.load(p.logits, tok, p.E, p.logit_type, lane);
+  uint32_t k0 = r.key[0];
+#pragma unroll
+  for (int i = 1; i < NPL; ++i) k0 = max(k0, r.key[i]);
+  const float top = key_logit(wave_max(k0));
+  float sum = p.renorm ? 0.f : r.exp_sum(top);
   int e = -1;
-  uint32_t ekey = 0u;
-  Logits<NPL> x;
+  float mine = 0.f;
+  for (int j = 0; j < p.topk; ++j) {
+    uint32_t k;
+    const int id = r.take(lane, &k);
+    if (id < 0) break;
+    const float v = expf(key_logit(k) - top);
+    if (p.renorm) sum += v;
+    if (j == z - tok * p.topk) {
+      e = id;
+      mine = v;
+      if (!p.renorm) break;
+    }
+  }
+  if (lane == 0) {
+    p.topk_ids[z] = e;
+    p.topk_w[z] = e < 0 ? 0.f : mine / sum;
+  }
+}
+
+// The expert of slot z, -1 for none.  Uniform over the workgroup.
+template <int NPL>
+__device__ inline int few_expert(const B8FewArgs& p, int z, int lane) {
+  int e = -1;
   if (p.logits) {
-    x.load(p.logits, tok, E, p.logit_type, lane);
-    for (int j = z - tok * topk; j >= 0; --j) {
-      e = x.take(lane, &ekey);
+    const int tok = z / p.topk;
+    Logits<NPL> x;
+    x.load(p.logits, tok, p.E, p.logit_type, lane);
+    for (int j = z - tok * p.topk; j >= 0; --j) {
+      uint32_t k;
+      e = x.take(lane, &k);
       if (e < 0) break;
     }
-    e = __builtin_amdgcn_readfirstlane(e);
   } else {
     e = p.topk_ids[z];
-    if (e < 0 || e >= E) e = -1;
+    if (e < 0 || e >= p.E) e = -1;
   }
-  if (p.logits && blockIdx.x == 0 && wave == kFewWaves - 1) {
-    // this slot's routing, for the down kernel and the caller
-    Logits<NPL> r;
-    r.load(p.logits, tok, E, p.logit_type, lane);
-    uint32_t k0 = r.key[0];
-#pragma unroll
-    for (int i = 1; i < NPL; ++i) k0 = max(k0, r.key[i]);
-    const float top = key_logit(wave_max(k0));
-    float sum = 0.f;
-    if (p.renorm) {
-      for (int j = 0; j < topk; ++j) {
-        uint32_t k;
-        if (r.take(lane, &k) < 0) break;
-        sum += expf(key_logit(k) - top);
-      }
-    } else {
-      sum = r.exp_sum(top);
-    }
-    if (lane == 0) {
-      p.topk_ids[z] = e;
-      p.topk_w[z] = e < 0 ? 0.f : expf(key_logit(ekey) - top) / sum;
-    }
-  }
-  if (e < 0) return;
+  return __builtin_amdgcn_readfirstlane(e);
+}
 
-  // ---- first weight loads (they need the expert only) ---------------------------
-  const int nbi = p.I / 16;
-  const uint8_t* wbase = p.w1 + (int64_t)e * p.w1_expert;
-  auto rsrc = [](const void* base, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-  };
-  const auto rw = rsrc(wbase, p.w1_expert);
-  const auto rws = rsrc(p.s1 + (int64_t)e * p.s1_expert, p.s1_expert * 4);
-  int woff[2], swoff[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int nb = u * nbi + blockIdx.x;
-    woff[u] = nb * G * 2048 + lane * 16;
-    swoff[u] = (nb / 8) * G * 4;
-  }
-  constexpr int ST = 4;
-  u4_t wr[ST][2][2];
-  uint32_t sw[ST][2];
-  auto issue = [&](int slot, int g) {
-    const int past = g < G ? 0 : (int)0x80000000u;
-    g = min(g, G - 1);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        wr[slot][u][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (woff[u] + 1024 * h) | past, g * 2048, 0));
-      sw[slot][u] = __builtin_amdgcn_raw_buffer_load_b32(rws, swoff[u] | past, g * 4, 0);
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < ST; ++s) issue(s, wave + s * kFewWaves);
-
-  // ---- the slots that share the expert ------------------------------------------
+// The slots that hold expert e, in order, into picks; returns how many.  Ends
+// with a barrier.
+template <int NPL>
+__device__ inline int few_slots(const B8FewArgs& p, int e, int* picks, int* npicks, int lane, int wave, int waves) {
+  const int T = p.t, topk = p.topk;
   if (p.logits) {
-    // slot of token t' that holds e: how many logits come before e's
-    for (int t = wave; t < T; t += kFewWaves) {
-      Logits<NPL> y;
-      y.load(p.logits, t, E, p.logit_type, lane);
-      const uint32_t k = logit_key(load_logit_rt(p.logits, (int64_t)t * E + e, p.logit_type));
-      const int rank = y.before(lane, e, k);
-      if (lane == 0) picks[t] = (k && rank < topk) ? t * topk + rank : -1;
+    // slot of token t that holds e: how many logits come before e's
+    for (int t0 = wave; t0 < T; t0 += 2 * waves) {
+      Logits<NPL> y[2];
+      uint32_t k[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = min(t0 + u * waves, T - 1);
+        y[u].load(p.logits, t, p.E, p.logit_type, lane);
+        k[u] = logit_key(load_logit_rt(p.logits, (int64_t)t * p.E + e, p.logit_type));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = t0 + u * waves, rank = y[u].before(lane, e, k[u]);
+        if (lane == 0 && t < T) picks[t] = (k[u] && rank < topk) ? t * topk + rank : -1;
+      }
     }
     __syncthreads();
     if (wave == 0) {
       const int s = lane < T ? picks[lane] : -1;  // T <= 64
       const uint64_t has = __ballot(s >= 0);
       if (s >= 0) picks[__popcll(has & ((1ull << lane) - 1))] = s;
-      if (lane == 0) npicks = __popcll(has);
+      if (lane == 0) *npicks = __popcll(has);
     }
   } else if (wave == 0) {
     int n = 0;
@@ -264,99 +251,208 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_gate_up(B8FewArgs p) {
       if (hit) picks[n + __popcll(has & ((1ull << lane) - 1))] = s;
       n += __popcll(has);
     }
-    if (lane == 0) npicks = n;
+    if (lane == 0) *npicks = n;
   }
   __syncthreads();
-  if (picks[0] != z) return;  // the first of them does the work
-  const int n = npicks;
+  return *npicks;
+}
+
+__device__ inline __amdgpu_buffer_rsrc_t few_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// One block of a row of x (16 lanes, 8 values each) -> codes and scale in LDS.
+template <bool BF16>
+__device__ inline void few_quantise(u4_t raw, uint8_t* codes, float* scale, int c16) {
+  float v[8];
+  b8_unpack<BF16>(raw, v);
+  uint32_t top = 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, b8_mag(v[j]));
+  const float s = b8_scale(b8_row_max(top));
+  const B8Div d(s);
+  *reinterpret_cast<uint2*>(codes + c16 * 8) =
+      uint2{b8_codes(v[0], v[1], v[2], v[3], d), b8_codes(v[4], v[5], v[6], v[7], d)};
+  if (c16 == 0) *scale = s;
+}
+
+template <int NPL, bool BF16, bool WIDE, int NW, int ST>
+__global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // rows: codes [R][pitch], scales [R][G]
+  __shared__ f4_t red[WIDE ? 1 : NW][2][64];
+  __shared__ uint32_t tops[NW][16];
+  __shared__ int picks[kB8FewMaxSlots];
+  __shared__ int npicks;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, kq = lane >> 4;
+  const int z = blockIdx.y, K = p.H, G = K / 128;
+  const int nbi = p.I / 16;
+  if (p.logits && blockIdx.x == gridDim.x - 1) {
+    if (wave == 0) few_write_routing<NPL>(p, z, lane);
+    return;
+  }
+  // the slot's own row of x is the first of the rows below: its loads (up to
+  // 64 blocks) start here, before the routing
+  constexpr int XP = 16 / NW;
+  u4_t xr[XP];
+#pragma unroll
+  for (int u = 0; u < XP; ++u) {
+    const int g = min((tid >> 4) + 4 * NW * u, G - 1);
+    xr[u] = static_cast<const u4_t*>(p.x)[(int64_t)(z / p.topk) * (K / 8) + g * 16 + c16];
+  }
+  const int e = few_expert<NPL>(p, z, lane);
+  if (e < 0) return;
+
+  // ---- weight stream: this wave's gate and up fragments of step i ----------------
+  const int nb0 = WIDE ? blockIdx.x * 8 + wave : blockIdx.x;
+  const int gs = WIDE ? 0 : wave, gd = WIDE ? 1 : NW;  // groups gs, gs + gd, ...
+  const auto rw = few_rsrc(p.w1 + (int64_t)e * p.w1_expert, p.w1_expert);
+  const auto rws = few_rsrc(p.s1 + (int64_t)e * p.s1_expert, p.s1_expert * 4);
+  u4_t wr[ST][2][2];
+  uint32_t sw[ST][2];
+  auto issue = [&](int slot, int g) {
+    const int past = g < G ? 0 : (int)0x80000000u;  // steps past the end read nothing and hold zeros
+    g = min(g, G - 1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int nb = u * nbi + nb0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        wr[slot][u][h] = __builtin_bit_cast(
+            u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (lane * 16 + 1024 * h) | past, (nb * G + g) * 2048, 0));
+      sw[slot][u] = __builtin_amdgcn_raw_buffer_load_b32(rws, past, ((nb / 8) * G + g) * 4, 0);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    issue(s, gs + s * gd);
+    __builtin_amdgcn_sched_barrier(0);  // step by step, as the waits of the loop below count them
+  }
+
+  int n = 1;
+  if (p.t == 1 && p.logits) {
+    if (tid == 0) picks[0] = z;
+  } else {
+    n = few_slots<NPL>(p, e, picks, &npicks, lane, wave, NW);
+    if (picks[0] != z) return;
+  }
 
   const int pitch = K + 16, R = p.rows;
-  float* sa = reinterpret_cast<float*>(lds + R * pitch);  // [R][G]
+  float* sa = reinterpret_cast<float*>(lds + R * pitch);
   for (int c0 = 0; c0 < n; c0 += R) {
     const int nr = min(n - c0, R);
     if (c0) {
       __syncthreads();  // the rows and sums of the chunk before are read
+    } else {
 #pragma unroll
-      for (int s = 0; s < ST; ++s) issue(s, wave + s * kFewWaves);
+      for (int u = 0; u < XP; ++u) {
+        const int g = (tid >> 4) + 4 * NW * u;
+        if (g < G) few_quantise<BF16>(xr[u], lds + g * 128, sa + g, c16);
+      }
     }
-    // ---- rows of x, quantised into LDS: 16 lanes a block ------------------------
-    for (int i = tid >> 4; i < nr * G; i += 4 * kFewWaves) {
+    // the rest of the rows' blocks: row i / G, block i % G
+    const int done = c0 ? 0 : min(G, 4 * NW * XP);
+#pragma unroll 1
+    for (int i = done + (tid >> 4); i < nr * G; i += 4 * NW) {
       const int r = i / G, g = i - r * G;
-      const int64_t row = picks[c0 + r] / topk;
-      float v[8];
-      b8_unpack<BF16>(static_cast<const u4_t*>(p.x)[row * (K / 8) + g * 16 + c16], v);
-      uint32_t top = 0u;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, b8_mag(v[j]));
-      const float s = b8_scale(b8_row_max(top));
-      const B8Div d(s);
-      *reinterpret_cast<uint2*>(lds + r * pitch + g * 128 + c16 * 8) =
-          uint2{b8_codes(v[0], v[1], v[2], v[3], d), b8_codes(v[4], v[5], v[6], v[7], d)};
-      if (c16 == 0) sa[r * G + g] = s;
+      const int64_t row = (!c0 && !r) ? z / p.topk : picks[c0 + r] / p.topk;
+      few_quantise<BF16>(static_cast<const u4_t*>(p.x)[row * (K / 8) + g * 16 + c16], lds + r * pitch + g * 128,
+                         sa + r * G + g, c16);
     }
     __syncthreads();
-    // ---- K over the waves -------------------------------------------------------
     const int rl = min(c16, nr - 1);
+    const uint8_t* ar = lds + rl * pitch + kq * 16;
     f4_t acc[2] = {f4_t{0.f, 0.f, 0.f, 0.f}, f4_t{0.f, 0.f, 0.f, 0.f}};
-    for (int g = wave; g < G; g += ST * kFewWaves) {
+#pragma unroll 1
+    for (int g = gs; g < G; g += ST * gd) {
 #pragma unroll
       for (int s = 0; s < ST; ++s) {
-        const int gg = min(g + s * kFewWaves, G - 1);  // past the end the weights and their scales are zero
-        const u4_t a0 = *reinterpret_cast<const u4_t*>(lds + rl * pitch + gg * 128 + kq * 16);
-        const u4_t a1 = *reinterpret_cast<const u4_t*>(lds + rl * pitch + gg * 128 + 64 + kq * 16);
-        const float f = sa[rl * G + gg];
-        const bool in = g + s * kFewWaves < G;
+        const int gg = min(g + s * gd, G - 1);
+        const i8_t av = cat8(*reinterpret_cast<const u4_t*>(ar + gg * 128), *reinterpret_cast<const u4_t*>(ar + gg * 128 + 64));
+        const float f = sa[rl * G + gg];  // past the end the weights and their scales are zero
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const f4_t P = b8_mfma(cat8(wr[s][u][0], wr[s][u][1]), cat8(a0, a1));
-          const float m = in ? f * __uint_as_float(sw[s][u]) : 0.f;
+          const f4_t P = b8_mfma(cat8(wr[s][u][0], wr[s][u][1]), av);
+          const float m = f * __uint_as_float(sw[s][u]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[u][q] = fmaf(m, P[q], acc[u][q]);
         }
-        issue(s, g + (s + ST) * kFewWaves);
+        // the ring goes on with the next groups, after the last ones with the
+        // first ones again if there are more rows
+        issue(s, g + ST * gd < G ? g + (s + ST) * gd : (c0 + R < n ? gs + s * gd : G));
+        __builtin_amdgcn_sched_barrier(0);  // one step's operands at a time: the ring fills the registers
       }
     }
-    red[wave][0][lane] = acc[0];
-    red[wave][1][lane] = acc[1];
-    __syncthreads();
-    if (tid < 64 && c16 < nr) {
-      f4_t h[2];
+    if constexpr (WIDE) {
+      uint32_t top = 0u;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        h[u] = red[0][u][lane];
-#pragma unroll
-        for (int w = 1; w < kFewWaves; ++w)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) h[u][q] += red[w][u][lane][q];
+      for (int q = 0; q < 4; ++q) {
+        acc[0][q] = b8_silu_mul(acc[0][q], acc[1][q]);
+        top = max(top, b8_mag(acc[0][q]));
       }
-      f4_t a;
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      if (kq == 0) tops[wave][c16] = top;
+      __syncthreads();
+      top = 0u;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) a[q] = b8_silu_mul(h[0][q], h[1][q]);
-      *reinterpret_cast<f4_t*>(p.act + (int64_t)picks[c0 + c16] * p.I + blockIdx.x * 16 + 4 * kq) = a;
+      for (int w = 0; w < NW; ++w) top = max(top, tops[w][c16]);
+      const float s = b8_scale(top);
+      const B8Div d(s);
+      if (c16 < nr) {
+        const int64_t slot = picks[c0 + c16];
+        *reinterpret_cast<uint32_t*>(p.act_codes + slot * p.I + nb0 * 16 + 4 * kq) =
+            b8_codes(acc[0][0], acc[0][1], acc[0][2], acc[0][3], d);
+        if (wave == 0 && kq == 0) p.act[slot * (p.I / 128) + blockIdx.x] = s;
+      }
+    } else {
+      red[wave][0][lane] = acc[0];
+      red[wave][1][lane] = acc[1];
+      __syncthreads();
+      if (tid < 64 && c16 < nr) {
+        f4_t h[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          h[u] = red[0][u][lane];
+#pragma unroll
+          for (int w = 1; w < NW; ++w)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[u][q] += red[w][u][lane][q];
+        }
+        f4_t a;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[q] = b8_silu_mul(h[0][q], h[1][q]);
+        *reinterpret_cast<f4_t*>(p.act + (int64_t)picks[c0 + c16] * p.I + nb0 * 16 + 4 * kq) = a;
+      }
     }
   }
 #endif
 }
 
 // ---------------------------------------------------------------------------
-// down + combine: grid (column blocks, tiles of 16 tokens); the waves take the
-// (expert, group) steps in turn
+// down + combine: grid (16-column blocks, tiles of 16 tokens).  The tile's
+// activation rows lie quantised in LDS (as many 128-k groups at a time as
+// fit); the waves take the (expert, group) steps in turn.
 // ---------------------------------------------------------------------------
-template <int NB>
-__global__ void __launch_bounds__(64 * kFewWaves) few_down(B8FewArgs p) {
+template <bool WIDE, int ST>
+__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(4))) few_down(B8FewArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kMaxTile = 16 * kB8FewMaxTopk;
-  __shared__ f4_t red[kFewWaves][NB][64];
-  __shared__ int key[kMaxTile];           // expert | occurrence << 16, -1: none
-  __shared__ int units[kMaxTile];         // first slot of each distinct key, in slot order
-  __shared__ short slot_of[kMaxTile][16]; // [first slot][token of the tile]: the slot with that key, -1 none
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // codes [ns][pitch], scales [ns][gmax]
+  __shared__ f4_t red[kFewWaves][64];
+  __shared__ int key[kMaxTile];            // expert | occurrence << 16, -1: none
+  __shared__ int unit_of[kMaxTile];        // index of a slot's unit, at the unit's first slot
+  __shared__ int unit_expert[kMaxTile];
+  __shared__ short slot_of[kMaxTile][16];  // [unit][token of the tile]: the slot with that key, -1 none
   __shared__ float wt[kMaxTile];
   __shared__ int wcount[4];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kq = lane >> 4;
   const int topk = p.topk, t0 = blockIdx.y * 16, nt = min(16, p.t - t0), ns = nt * topk;
-  const int G = p.I / 128, N = p.H;
+  const int G = p.I / 128, N = p.H, nb = blockIdx.x;
 
   // ---- the distinct experts of the tile's slots --------------------------------
   // A token may hold an expert more than once (given ids): each occurrence is
@@ -370,129 +466,162 @@ __global__ void __launch_bounds__(64 * kFewWaves) few_down(B8FewArgs p) {
     wt[tid] = p.topk_w[t0 * topk + tid];
   }
   __syncthreads();
-  const int my_tok = tid / topk;
-  int occ = 0;
-  if (tid < ns && id >= 0)
-    for (int s = my_tok * topk; s < tid; ++s) occ += key[s] == id;
-  __syncthreads();
-  if (tid < ns && id >= 0) key[tid] = id | (occ << 16);
-  __syncthreads();
-  int first = -1;
-  if (tid < ns && id >= 0) {
+  int first = -1, my_tok = 0;
+  if (nt == 1) {
+    first = id >= 0 ? tid : -1;  // every slot of one token is a unit
+  } else {
+    my_tok = tid / topk;
+    int occ = 0;
+    if (tid < ns && id >= 0)
+      for (int s = my_tok * topk; s < tid; ++s) occ += key[s] == id;
+    __syncthreads();
     const int k = id | (occ << 16);
-    for (first = 0; key[first] != k; ++first) {
-    }
-    slot_of[first][my_tok] = (short)tid;
+    if (tid < ns && id >= 0) key[tid] = k;
+    __syncthreads();
+    if (tid < ns && id >= 0)
+      for (first = 0; key[first] != k; ++first) {
+      }
   }
   const bool lead = first >= 0 && first == tid;
   const uint64_t leads = __ballot(lead);
   if (lane == 0 && wave < 4) wcount[wave] = __popcll(leads);
   __syncthreads();
+  const int nu = wcount[0] + wcount[1] + wcount[2] + wcount[3];
   if (lead) {
     int at = __popcll(leads & ((1ull << lane) - 1));
     for (int w = 0; w < wave; ++w) at += wcount[w];
-    units[at] = tid;
+    unit_of[tid] = at;
+    unit_expert[at] = id;
   }
   __syncthreads();
-  const int nu = wcount[0] + wcount[1] + wcount[2] + wcount[3];
-  const int steps = nu * G;
+  if (first >= 0) slot_of[unit_of[first]][my_tok] = (short)tid;
 
-  auto rsrc = [](const void* base, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-  };
-  const auto ract = rsrc(p.act, (int64_t)p.t * topk * p.I * 4);
-  const int nblocks = N / 16, nb0 = blockIdx.x * NB;
-  constexpr int ST = 2;
-  u4_t wr[ST][NB][2];
-  u4_t av[ST][8];
-  uint32_t sw[ST][NB];
-  float tw[ST];
-  bool has[ST];  // whether the lane's token holds the unit's expert
-  auto issue = [&](int slot, int i) {
-    const bool in = i < steps;
-    const int ii = in ? i : 0;
-    const int u = ii / G, g = ii - u * G;
-    const int s0 = __builtin_amdgcn_readfirstlane(steps ? units[u] : 0);
-    const int e = __builtin_amdgcn_readfirstlane(steps ? key[s0] & 0xFFFF : 0);
-    const auto rw = rsrc(p.w2 + (int64_t)e * p.w2_expert, in ? p.w2_expert : 0);
-    const auto rs = rsrc(p.s2 + (int64_t)e * p.s2_expert, in ? p.s2_expert * 4 : 0);
+  const int gmax = p.down_groups, pitch = gmax * 128 + 16;
+  float* sc = reinterpret_cast<float*>(lds + ns * pitch);  // [ns][gmax]
+  u4_t wr[ST][2];
+  uint32_t sw[ST];
+  f4_t acc = f4_t{0.f, 0.f, 0.f, 0.f};
+  // a lane keeps the experts of four units, so that a step finds its own
+  // without a trip to LDS
+  int ue[4];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int nb = min(nb0 + j, nblocks - 1);
+  for (int i = 0; i < 4; ++i) ue[i] = lane + 64 * i < nu ? unit_expert[lane + 64 * i] : 0;
+  for (int gc0 = 0; gc0 < G && nu; gc0 += gmax) {
+    const int gc = min(gmax, G - gc0), steps = nu * gc;
+    // step i is (unit i / gc, group i % gc), kept as a pair that the waves'
+    // stride moves on
+    const int du = kFewWaves / gc, dg = kFewWaves - du * gc;
+    struct Step {
+      int u, g;
+    };
+    auto next = [&](Step& t) {
+      t.u += du;
+      t.g += dg;
+      if (t.g >= gc) {
+        t.g -= gc;
+        ++t.u;
+      }
+    };
+    Step ahead{wave / gc, wave % gc}, now = ahead;
+    auto issue = [&](int slot) {
+      const bool in = ahead.u < nu;
+      const int u = in ? ahead.u : 0, g = gc0 + ahead.g;
+      int e = __builtin_amdgcn_readlane(ue[0], u & 63);
+      if (nu > 64) {
+        const int e1 = __builtin_amdgcn_readlane(ue[1], u & 63);
+        const int e2 = __builtin_amdgcn_readlane(ue[2], u & 63), e3 = __builtin_amdgcn_readlane(ue[3], u & 63);
+        e = u < 128 ? (u < 64 ? e : e1) : (u < 192 ? e2 : e3);
+      }
+      const auto rw = few_rsrc(p.w2 + (int64_t)e * p.w2_expert, in ? p.w2_expert : 0);
+      const auto rs = few_rsrc(p.s2 + (int64_t)e * p.s2_expert, in ? p.s2_expert * 4 : 0);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        wr[slot][j][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + 1024 * h, (nb * G + g) * 2048, 0));
-      sw[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(rs, 0, ((nb / 8) * G + g) * 4, 0);
+        wr[slot][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + 1024 * h, (nb * G + g) * 2048, 0));
+      sw[slot] = __builtin_amdgcn_raw_buffer_load_b32(rs, 0, ((nb / 8) * G + g) * 4, 0);
+      next(ahead);
+    };
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      issue(s);
+      __builtin_amdgcn_sched_barrier(0);  // step by step, as the waits of the loop below count them
     }
-    const int s = in ? slot_of[s0][c16] : -1;
-    has[slot] = s >= 0;
-    tw[slot] = wt[max(s, 0)];
-    const int off = s >= 0 ? ((t0 * topk + s) * p.I + g * 128 + 16 * kq) * 4 : (int)0x80000000u;
+    if (gc0) __syncthreads();  // the groups before are multiplied
+#pragma unroll 1
+    for (int i = tid >> 4; i < ns * gc; i += 4 * kFewWaves) {
+      const int s = i / gc, g = i - s * gc;
+      if (key[s] < 0) continue;  // its row was not written
+      const int64_t slot = t0 * topk + s;
+      float f;
+      uint2 q;
+      if constexpr (WIDE) {
+        q = *reinterpret_cast<const uint2*>(p.act_codes + slot * p.I + (gc0 + g) * 128 + c16 * 8);
+        f = p.act[slot * G + gc0 + g];
+      } else {
+        const f4_t* src = reinterpret_cast<const f4_t*>(p.act + slot * p.I + (gc0 + g) * 128 + c16 * 8);
+        const f4_t a = src[0], b = src[1];
+        uint32_t top = 0u;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      av[slot][q] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ract, off, (q & 3) * 16 + (q >> 2) * 256, 0));
-  };
-  f4_t acc[NB];
-#pragma unroll
-  for (int j = 0; j < NB; ++j) acc[j] = f4_t{0.f, 0.f, 0.f, 0.f};
-  if (steps) {
-#pragma unroll
-    for (int s = 0; s < ST; ++s) issue(s, wave + s * kFewWaves);
+        for (int v = 0; v < 4; ++v) top = max(top, max(b8_mag(a[v]), b8_mag(b[v])));
+        f = b8_scale(b8_row_max(top));
+        const B8Div d(f);
+        q = uint2{b8_codes(a[0], a[1], a[2], a[3], d), b8_codes(b[0], b[1], b[2], b[3], d)};
+      }
+      *reinterpret_cast<uint2*>(lds + s * pitch + g * 128 + c16 * 8) = q;
+      if (c16 == 0) sc[s * gmax + g] = f * wt[s];  // the top-k weight rides on the scale
+    }
+    __syncthreads();
+#pragma unroll 1
     for (int i = wave; i < steps; i += ST * kFewWaves) {
 #pragma unroll
       for (int s = 0; s < ST; ++s) {
-        // quantise the token's 128 values: 32 in this lane, four lanes a block
-        uint32_t top = 0u;
+        const bool in = now.u < nu;
+        const int sl = slot_of[in ? now.u : 0][c16];
+        const bool has = in && sl >= 0;  // lanes of other tokens take nothing
+        const int row = max(sl, 0);
+        const uint8_t* ar = lds + row * pitch + now.g * 128 + kq * 16;
+        const f4_t P = b8_mfma(cat8(wr[s][0], wr[s][1]),
+                               cat8(*reinterpret_cast<const u4_t*>(ar), *reinterpret_cast<const u4_t*>(ar + 64)));
+        const float f = sc[row * gmax + now.g] * __uint_as_float(sw[s]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) top = max(top, av[s][q][r] & 0x7FFFFFFFu);
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-        const float sc = b8_scale(top);
-        const B8Div d(sc);
-        i8_t a;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          a[q] = (int)b8_codes(__uint_as_float(av[s][q][0]), __uint_as_float(av[s][q][1]), __uint_as_float(av[s][q][2]),
-                               __uint_as_float(av[s][q][3]), d);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const f4_t P = b8_mfma(cat8(wr[s][j][0], wr[s][j][1]), a);
-          const float f = tw[s] * (sc * __uint_as_float(sw[s][j]));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[j][q] = has[s] ? fmaf(f, P[q], acc[j][q]) : acc[j][q];
-        }
-        issue(s, i + (s + ST) * kFewWaves);
+        for (int q = 0; q < 4; ++q) acc[q] = has ? fmaf(f, P[q], acc[q]) : acc[q];
+        next(now);
+        issue(s);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) red[wave][j][lane] = acc[j];
+  red[wave][lane] = acc;
   __syncthreads();
-  for (int i = tid; i < NB * 64; i += 64 * kFewWaves) {
-    const int j = i >> 6, l = i & 63;
-    f4_t v = red[0][j][l];
+  if (tid < 64 && c16 < nt) {
+    f4_t v = red[0][lane];
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += red[w][j][l][q];
-    const int t = l & 15, nb = nb0 + j;
-    if (t >= nt || nb >= nblocks) continue;
+      for (int q = 0; q < 4; ++q) v[q] += red[w][lane][q];
     auto cv = [&](float x) -> uint32_t { return p.out_bf16 ? float_to_bf16_bits(x) : float_to_f16_bits(x); };
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)(t0 + t) * N + nb * 16 + 4 * (l >> 4)) =
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)(t0 + c16) * N + nb * 16 + 4 * kq) =
         uint2{cv(v[0]) | (cv(v[1]) << 16), cv(v[2]) | (cv(v[3]) << 16)};
   }
 #endif
 }
 
+template <int NPL, bool BF16, bool WIDE, int NW, int ST>
+hipError_t gate_up_k(const B8FewArgs& a, dim3 grid, size_t lds, hipStream_t s) {
+  const hipError_t e = allow_lds<few_gate_up<NPL, BF16, WIDE, NW, ST>>(kFewLds);
+  if (e != hipSuccess) return e;
+  return launch_timed(few_gate_up<NPL, BF16, WIDE, NW, ST>, grid, dim3(64 * NW), lds, s, a);
+}
+
+template <int NPL, bool BF16>
+hipError_t gate_up_s(const B8FewArgs& a, dim3 grid, size_t lds, hipStream_t s) {
+  if (a.act_codes) return gate_up_k<NPL, BF16, true, 8, 6>(a, grid, lds, s);
+  if (a.t == 1) return gate_up_k<NPL, BF16, false, 8, 7>(a, grid, lds, s);
+  return gate_up_k<NPL, BF16, false, 4, 4>(a, grid, lds, s);
+}
+
 template <int NPL>
 hipError_t gate_up_t(const B8FewArgs& a, dim3 grid, size_t lds, hipStream_t s) {
-  const dim3 block(64 * kFewWaves);
-  const hipError_t e = a.x_bf16 ? allow_lds<few_gate_up<NPL, true>>(kFewLds) : allow_lds<few_gate_up<NPL, false>>(kFewLds);
-  if (e != hipSuccess) return e;
-  return a.x_bf16 ? launch_timed(few_gate_up<NPL, true>, grid, block, lds, s, a)
-                  : launch_timed(few_gate_up<NPL, false>, grid, block, lds, s, a);
+  return a.x_bf16 ? gate_up_s<NPL, true>(a, grid, lds, s) : gate_up_s<NPL, false>(a, grid, lds, s);
 }
 
 }  // namespace
@@ -509,29 +638,47 @@ int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits,
   return (int)launch_timed(route_kernel<16>, grid, block, 0, s, logits, logit_type, ti, E, topk, renorm, ids, w);
 }
 
-// Rows of x a workgroup keeps quantised at a time: four cover an expert's
-// tokens of a small batch nearly always (the weights are read again for each
-// further four), fewer where K is long.
-int b8_few_rows(int64_t t, int64_t K) {
-  const int64_t per = K + 16 + K / 128 * 4;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({t, 4, 96 * 1024 / per}));
+// Rows of x a gate_up workgroup keeps quantised at a time (the weights are
+// read again for each further so many): four cover an expert's tokens of a
+// small batch nearly always, eight where a CU holds one workgroup anyway.
+static int few_rows(const B8FewArgs& a) {
+  const int64_t per = a.H + 16 + a.H / 128 * 4;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)a.t, a.act_codes ? 8 : 4, 96 * 1024 / per}));
+}
+
+// 128-k groups of a tile's activation rows a down workgroup holds at a time:
+// two workgroups of a CU hold up to 48 KiB each.
+static int few_down_groups(const B8FewArgs& a) {
+  const int64_t ns = std::min(a.t, 16) * (int64_t)a.topk;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(a.I / 128, 48 * 1024 / (ns * 132)));
 }
 
 int launch_few_gate_up(const B8FewArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)(a.I / 16), (unsigned)(a.t * a.topk));
-  const size_t lds = (size_t)a.rows * (a.H + 16 + a.H / 128 * 4);
+  B8FewArgs b = a;
+  b.rows = few_rows(a);
+  const dim3 grid((unsigned)(a.I / (a.act_codes ? 128 : 16) + (a.logits ? 1 : 0)), (unsigned)(a.t * a.topk));
+  const size_t lds = (size_t)b.rows * (a.H + 16 + a.H / 128 * 4);
   if (lds > kFewLds) return (int)hipErrorInvalidValue;
-  if (!a.logits || a.E <= 64) return (int)gate_up_t<1>(a, grid, lds, s);
-  if (a.E <= 256) return (int)gate_up_t<4>(a, grid, lds, s);
-  return (int)gate_up_t<16>(a, grid, lds, s);
+  if (!a.logits || a.E <= 64) return (int)gate_up_t<1>(b, grid, lds, s);
+  if (a.E <= 256) return (int)gate_up_t<4>(b, grid, lds, s);
+  return (int)gate_up_t<16>(b, grid, lds, s);
 }
 
 int launch_few_down(const B8FewArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const unsigned tiles = (unsigned)((a.t + 15) / 16);
-  const int nblocks = a.H / 16;
-  return (int)launch_timed(few_down<1>, dim3((unsigned)nblocks, tiles), dim3(64 * kFewWaves), 0, s, a);
+  B8FewArgs b = a;
+  b.down_groups = few_down_groups(a);
+  const size_t lds = (size_t)std::min(a.t, 16) * a.topk * (b.down_groups * 132 + 16);
+  const dim3 grid((unsigned)(a.H / 16), (unsigned)((a.t + 15) / 16)), block(64 * kFewWaves);
+  auto go = [&]<bool WIDE, int ST>() -> int {
+    const hipError_t e = allow_lds<few_down<WIDE, ST>>(kFewLds);
+    return e != hipSuccess ? (int)e : (int)launch_timed(few_down<WIDE, ST>, grid, block, lds, s, b);
+  };
+  // up to two steps a wave need no deeper ring
+  if (std::min(a.t, 16) * a.topk * b.down_groups <= 2 * kFewWaves)
+    return a.act_codes ? go.template operator()<true, 2>() : go.template operator()<false, 2>();
+  return a.act_codes ? go.template operator()<true, 6>() : go.template operator()<false, 6>();
 }
 
 }  // namespace hq

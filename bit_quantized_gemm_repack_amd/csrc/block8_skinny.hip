@@ -83,7 +83,10 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
     for (int j = 0; j < NB; ++j) acc[b][j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll
-  for (int s = 0; s < ST; ++s) issue(s, g0 + wave + s * waves);
+  for (int s = 0; s < ST; ++s) {
+    issue(s, g0 + wave + s * waves);
+    __builtin_amdgcn_sched_barrier(0);  // step by step, as the waits of the loop below count them
+  }
   for (int g = g0 + wave; g < g1; g += ST * waves) {
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
@@ -98,6 +101,7 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
           for (int q = 0; q < 4; ++q) acc[b][j][q] = fmaf(f, P[q], acc[b][j][q]);
         }
       issue(s, g + (s + ST) * waves);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll

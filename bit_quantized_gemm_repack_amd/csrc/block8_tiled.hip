@@ -129,14 +129,17 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
   }
   const int sseg = __builtin_amdgcn_readfirstlane(wave % (C::SROWS / 64));
   const int soff = row_of(min(sseg * 64 + lane, C::BM - 1)) * 4;
-  // columns past N read the last block (their results are not stored)
-  int woff[NB];
+  // Weight fragments: lane offset 16 l, the fragment's place in a scalar
+  // offset.  Columns past N read the last block (their results are not stored).
+  const int woff = lane * 16;
+  int wsc_off[NB];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) woff[j] = min(nblk(j), nblocks - 1) * G * 2048 + lane * 16;
+  for (int j = 0; j < NB; ++j) wsc_off[j] = __builtin_amdgcn_readfirstlane(min(nblk(j), nblocks - 1) * G * 2048);
   constexpr int NSW = MODE == B8_GATE_UP ? 2 : 1;  // weight scales a wave needs per step
   int swoff[NSW];
 #pragma unroll
-  for (int u = 0; u < NSW; ++u) swoff[u] = (min(nblk(u * (NB / 2)), nblocks - 1) * 16 / 128) * G * 4;
+  for (int u = 0; u < NSW; ++u)
+    swoff[u] = __builtin_amdgcn_readfirstlane((min(nblk(u * (NB / 2)), nblocks - 1) * 16 / 128) * G * 4);
 
   u4_t braw[ST][NB][2];
   uint32_t sraw[ST][NSW];
@@ -156,9 +159,9 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         braw[slot][j][h] =
-            __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, woff[j] + 1024 * h, gg * 2048, 0));
+            __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, woff + 1024 * h, wsc_off[j] + gg * 2048, 0));
 #pragma unroll
-    for (int u = 0; u < NSW; ++u) sraw[slot][u] = __builtin_amdgcn_raw_buffer_load_b32(rws, swoff[u], gg * 4, 0);
+    for (int u = 0; u < NSW; ++u) sraw[slot][u] = __builtin_amdgcn_raw_buffer_load_b32(rws, 0, swoff[u] + gg * 4, 0);
   };
 
   f4_t acc[MB][NB];
@@ -167,30 +170,50 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[mb][j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
+  // The step's MB x NB matrix instructions, row block by row block, as one
+  // pipeline: the operand of the next row block is read while the current
+  // one multiplies, and the four multiply-adds that promote a product follow
+  // two instructions behind it, so that they issue in the shadow of the matrix
+  // instruction then running (32 cycles against 16) instead of waiting for
+  // their own.
   auto compute = [&](auto slot_c) {
     constexpr int slot = decltype(slot_c)::value;
-    const uint8_t* at = lds + slot * C::STAGE + wm * (16 * MB) * 128;
-    const float* st = reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + wm * 16 * MB;
+    const uint8_t* at = lds + slot * C::STAGE + wm * (16 * MB) * 128 + c16 * 128;
+    const float* st = reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + wm * 16 * MB + c16;
     float sw[NSW];
 #pragma unroll
     for (int u = 0; u < NSW; ++u) sw[u] = __uint_as_float(sraw[slot][u]);
+    i8_t a[2];
+    float sa[2];
+    auto read = [&](int mb) {  // the row blocks start at multiples of 16: the swizzle sees c16 alone
+      a[mb & 1] = cat8(*reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, kq) * 16),
+                       *reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, 4 + kq) * 16));
+      sa[mb & 1] = st[16 * mb];
+    };
+    constexpr int D = NB == 4 && MB > 1 ? 3 : (MB * NB > 2 ? 2 : 1);  // products in flight ahead of their promotion (fewer than NB, or both of two)
+    f4_t P[D + 1];
+    float f[2][NSW];
+    auto promote = [&](int i) {
+      const int mb = i / NB, j = i - mb * NB;
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const int r = 16 * mb + c16;  // the wave's rows start at a multiple of 16: the swizzle sees the same r
-      const u4_t a0 = *reinterpret_cast<const u4_t*>(at + r * 128 + swz<8>(r, kq) * 16);
-      const u4_t a1 = *reinterpret_cast<const u4_t*>(at + r * 128 + swz<8>(r, 4 + kq) * 16);
-      const float sa = st[r];
-      const i8_t av = cat8(a0, a1);
-      f4_t P[NB];
+      for (int q = 0; q < 4; ++q)
+        acc[mb][j][q] = fmaf(f[mb & 1][NSW == 2 ? j / (NB / 2) : 0], P[i % (D + 1)][q], acc[mb][j][q]);
+    };
+    read(0);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) P[j] = b8_mfma(cat8(braw[slot][j][0], braw[slot][j][1]), av);
+    for (int i = 0; i < MB * NB; ++i) {
+      const int mb = i / NB, j = i - mb * NB;
+      if (j == 0 && mb + 1 < MB) read(mb + 1);
+      P[i % (D + 1)] = b8_mfma(cat8(braw[slot][j][0], braw[slot][j][1]), a[mb & 1]);
+      if (j == (NB > D ? D - 1 : 0)) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const float s = sa * sw[NSW == 2 ? j / (NB / 2) : 0];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[mb][j][q] = fmaf(s, P[j][q], acc[mb][j][q]);
+        for (int u = 0; u < NSW; ++u) f[mb & 1][u] = sa[mb & 1] * sw[u];
       }
+      if (i >= D) promote(i - D);
+      __builtin_amdgcn_sched_barrier(0);  // keeps this order: left to itself the scheduler puts each product's promotion right behind it
     }
+#pragma unroll
+    for (int i = MB * NB - D; i < MB * NB; ++i) promote(i);
   };
 
   auto gclamp = [&](int g) { return g < Gl ? g : Gl - 1; };
