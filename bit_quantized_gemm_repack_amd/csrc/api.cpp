@@ -424,7 +424,7 @@ hq_status check_exec(const hq_plan* p, const hq::Exec& e) {
   if (p->user.split_k < 0 || p->user.split_k > 64) return fail(HQ_ERR_INVALID_ARG, "split_k must be 1..64");
   if (p->fmt == hq::FMT_B8) {
     if (e.kernel == hq::KER_TILED) {
-      if (!hq::b8_tile_ok(hq::B8_DENSE, {e.tl.bm, 64 * e.tl.nbw, e.tl.split, e.tl.stages}))
+      if (!hq::b8_tile_ok({e.tl.bm, 64 * e.tl.nbw, e.tl.split, e.tl.stages}))
         return fail(HQ_ERR_INVALID_ARG, "no fp8 block tile of %d x %d with %d stages", e.tl.bm, 64 * e.tl.nbw, e.tl.stages);
       if (e.tl.gm < 1 || e.tl.gm > 64) return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_group must be 1..64");
       if (e.tiles_m * e.tiles_n > (int64_t(1) << 31) - 1) return fail(HQ_ERR_UNSUPPORTED, "too many tiles");
@@ -830,7 +830,7 @@ hq_status dense_run(const hq_plan* p, const hq::Exec& e, int64_t m, const void* 
       b.tiles_n = (int)e.tiles_n;
       b.group_m = (int)std::min<int64_t>(e.tl.gm, std::max<int64_t>(1, e.tiles_m));
       hq::arm_timing({ev.start, split > 1 ? nullptr : ev.stop});
-      int err = tiled ? hq::launch_b8_tiled(hq::B8_DENSE, {e.tl.bm, 64 * e.tl.nbw, split, e.tl.stages}, b, 0, stream)
+      int err = tiled ? hq::launch_b8_dense({e.tl.bm, 64 * e.tl.nbw, split, e.tl.stages}, b, stream)
                       : hq::launch_b8_skinny({e.sk.mb, e.sk.nb, e.sk.waves, split}, b, stream);
       if (err == hipSuccess && split > 1) {
         hq::arm_timing({nullptr, ev.stop});
@@ -1117,6 +1117,17 @@ static int64_t moe_down_cols(const hq_plan* p, int64_t t, int topk, int bm) {
   return std::min(c, N);
 }
 
+// Columns of a down launch of fp8 block layers: windows whose slot rows fit the
+// last-level cache, so that the sum reads them from there.
+static constexpr int64_t kB8WindowBytes = int64_t(96) << 20;
+
+static int64_t b8_window(const hq_plan* p, int64_t t, int topk) {
+  const int64_t N = p->layer.n, per = std::max<int64_t>(1, t * topk * 2);
+  if (N * per <= kB8WindowBytes) return N;
+  const int64_t n = cdiv(N, std::max<int64_t>(256, kB8WindowBytes / per / 256 * 256));  // windows
+  return cdiv(cdiv(N, n), 256) * 256;
+}
+
 struct MoeWs {
   size_t act32, rows, total;
 };
@@ -1126,7 +1137,10 @@ static MoeWs moe_ws(const hq_plan* p, int64_t t, int topk) {
   const int64_t mp = moe_max_padded(t, topk, p->layer.num_experts, moe_choice(p, t, topk).bm);
   // (the fp8 block gate_up requantises inside its tile: no fp32 rows)
   if (p->compute.epi == HQ_EPI_SILU_MUL_QFP8 && p->fmt != hq::FMT_B8) w.act32 = align256((size_t)mp * (size_t)(p->layer.n / 2) * 4);
-  if (p->compute.epi == HQ_EPI_TOPK_COMBINE)
+  if (p->compute.epi == HQ_EPI_TOPK_COMBINE && p->fmt == hq::FMT_B8) {
+    const int64_t win = b8_window(p, t, topk);
+    w.rows = align256((size_t)(t * topk * win) * 2) + align256((size_t)(t * topk * (win / 64)) * 4);
+  } else if (p->compute.epi == HQ_EPI_TOPK_COMBINE)
     w.rows = align256((size_t)t * topk * (size_t)moe_down_cols(p, t, topk, moe_choice(p, t, topk).bm) * 2);
   w.total = w.act32 + w.rows;
   return w;
@@ -1221,7 +1235,6 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.G = (int)G;
       b.a_rows = (int)(down ? mp : t);
       b.gps = (int)G;
-      b.tiles_n = (int)cdiv(N, 256);
       b.sorted_ids = sorted_ids;
       b.block_expert = block_expert;
       b.num_padded = num_padded;
@@ -1232,12 +1245,24 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.s_expert = (int64_t)(p->meta_bytes_per_expert / 4);
       b.out_scale = out_scale;
       b.out_rows = (int)mp;
-      b.rows16 = rows16;
-      hq::arm_timing({ev.start, down ? nullptr : ev.stop});
-      err = hq::launch_b8_tiled(down ? hq::B8_DOWN : hq::B8_GATE_UP, {bm, 256, 1, mc.tl.stages}, b, blocks, stream);
-      if (err == hipSuccess && down) {
-        hq::arm_timing({nullptr, ev.stop});
-        err = hq::launch_moe_combine(rows16, topk, t, N, 0, N, out, p->layer.q.out == HQ_BF16, stream);
+      err = hipSuccess;
+      if (!down) {
+        hq::arm_timing(ev);
+        err = hq::launch_b8_grouped(hq::B8_GATE_UP, bm, b, blocks, stream);
+      }
+      // down: column windows, each the GEMM and then the sum of its rows
+      const int64_t win = down ? b8_window(p, t, topk) : 1;
+      b.rows16 = reinterpret_cast<int16_t*>(rows16);
+      b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win) * 2));
+      b.out_bf16 = p->layer.q.out == HQ_BF16;
+      for (int64_t c = 0; down && c < N && err == hipSuccess; c += win) {
+        b.col0 = (int)c;
+        b.ncol = (int)std::min(win, N - c);
+        hq::arm_timing({c == 0 ? ev.start : nullptr, nullptr});
+        err = hq::launch_b8_grouped(hq::B8_DOWN, bm, b, blocks, stream);
+        if (err != hipSuccess) break;
+        hq::arm_timing({nullptr, c + win >= N ? ev.stop : nullptr});
+        err = hq::launch_b8_combine(b, t, stream);
       }
       hq::arm_timing({nullptr, nullptr});
       if (err != hipSuccess) return fail(HQ_ERR_HIP, "grouped gemm launch: %s", hipGetErrorString((hipError_t)err));

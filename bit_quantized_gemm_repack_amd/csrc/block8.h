@@ -41,18 +41,27 @@ struct B8Args {
   int64_t s_expert;        // weight scales per expert
   float* out_scale;        // gate_up: scales of the requantised rows [N/256][out_rows]
   int out_rows;
-  uint16_t* rows16;        // down: weighted slot rows, bf16 [n_slots][N]
+  // down: this launch's columns [col0, col0 + ncol) of N, col0 a multiple of
+  // 256; the slots' rows as 16-bit integers with a scale per 64 columns
+  int col0, ncol;
+  int16_t* rows16;         // [n_slots][ncol]
+  float* row_scale;        // [n_slots][ncol / 64]
+  int cols_wg;             // short K: columns a workgroup walks
 };
 
 enum B8Mode : int { B8_DENSE = 0, B8_GATE_UP = 1, B8_DOWN = 2 };
 
-// The 16-byte load of a dense or grouped tile: bm rows (16, 32, 64, 128, 256)
-// by bn columns (128, 256).
+// A dense tile: bm rows (16 .. 256) by bn columns (128, 256), K over `split`
+// workgroups, groups in the load ring.
 struct B8Tile {
   int bm, bn, split, stages;
 };
-bool b8_tile_ok(int mode, const B8Tile& t);
-int launch_b8_tiled(int mode, const B8Tile& t, const B8Args& a, int64_t blocks, void* stream);
+bool b8_tile_ok(const B8Tile& t);
+int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream);
+// Grouped: aligned blocks of bm rows (16, 32, 64, 128) by 256 columns.
+int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* stream);
+// y = the sum of a token's slot rows over the columns of a's window.
+int launch_b8_combine(const B8Args& a, int64_t t, void* stream);
 
 // Few rows: 16-column blocks, K over the waves of a workgroup and over `split`
 // workgroups.  rb: 16-row blocks per workgroup (1, 2, 4).

@@ -21,6 +21,146 @@ namespace hq {
 
 namespace {
 
+// One 128-k step of a wave's 16 MB rows by 16 NB columns as one pipeline: the
+// operand of the next row block is read while the current one multiplies, and
+// the four multiply-adds that promote a product follow up to three matrix
+// instructions behind it, so that they issue in the shadow of the one then
+// running (32 cycles against 16) instead of waiting for their own.
+//   at, st  the step's activation rows and row scales in LDS, this lane's row
+//           (c16) of the first row block
+//   b, sw   weight operands and scales (NSW = 2: gate columns, up columns)
+template <int MB, int NB, int NSW>
+__device__ __forceinline__ void b8_step(const uint8_t* at, const float* st, int c16, int kq, const u4_t (&b)[NB][2],
+                                        const float (&sw)[NSW], f4_t (&acc)[MB][NB]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  i8_t a[2];
+  float sa[2];
+  auto read = [&](int mb) {  // row blocks start at multiples of 16: the swizzle sees c16 alone
+    a[mb & 1] = cat8(*reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, kq) * 16),
+                     *reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, 4 + kq) * 16));
+    sa[mb & 1] = st[16 * mb];
+  };
+  // products in flight ahead of their promotion (fewer than NB, or both of two)
+  constexpr int D = NB == 4 && MB > 1 ? 3 : (MB * NB > 2 ? 2 : 1);
+  f4_t P[D + 1];
+  float f[2][NSW];
+  auto promote = [&](int i) {
+    const int mb = i / NB, j = i - mb * NB;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      acc[mb][j][q] = fmaf(f[mb & 1][NSW == 2 ? j / (NB / 2) : 0], P[i % (D + 1)][q], acc[mb][j][q]);
+  };
+  read(0);
+#pragma unroll
+  for (int i = 0; i < MB * NB; ++i) {
+    const int mb = i / NB, j = i - mb * NB;
+    if (j == 0 && mb + 1 < MB) read(mb + 1);
+    P[i % (D + 1)] = b8_mfma(cat8(b[j][0], b[j][1]), a[mb & 1]);
+    if (j == (NB > D ? D - 1 : 0)) {
+#pragma unroll
+      for (int u = 0; u < NSW; ++u) f[mb & 1][u] = sa[mb & 1] * sw[u];
+    }
+    if (i >= D) promote(i - D);
+    // keeps this order: left to itself the scheduler puts each product's promotion right behind it
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = MB * NB - D; i < MB * NB; ++i) promote(i);
+#endif
+}
+
+// Sixteen rows of 16 NB 16-bit values from the operand layout (lane (c16, kq),
+// fragment j: columns 16 j + 4 kq .. + 3 of row c16) to 16 bytes a lane, so
+// that a store instruction covers whole 64-byte runs of its rows; through the
+// wave's own 16 x (32 NB + 16) bytes of LDS.  Stored 8 bytes a lane straight
+// from the operand layout, the rows of the down GEMM took 129 us of 4096
+// tokens' 340.
+constexpr int b8_rows_lds(int NB) { return 16 * (32 * NB + 16); }
+
+template <int NB, typename V, typename S>
+__device__ __forceinline__ void b8_rows16(uint8_t* buf, int lane, V&& value, S&& store) {
+  const int c16 = lane & 15, kq = lane >> 4;
+  constexpr int PITCH = 32 * NB + 16;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) *reinterpret_cast<uint2*>(buf + c16 * PITCH + 32 * j + 8 * kq) = value(j);
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int h = 0; h < NB / 2; ++h)
+    store(64 * h + 16 * kq, *reinterpret_cast<const uint4*>(buf + c16 * PITCH + 64 * h + 16 * kq));
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A slot's weighted row of the down GEMM, 64 columns a wave: the fp32 sums o
+// as 16-bit integers q = o / 2^e with the one 2^e that brings the largest to
+// 15 bits, and topk_w * 2^e as their scale.  Half the bytes of fp32 rows at an
+// error of 2^-16 of the 64 columns' largest (bf16 rows: 2^-9 of each).  A
+// value that is not finite makes the scale NaN, and so the 64 columns.
+template <int MB>
+__device__ __forceinline__ void b8_store_rows(const B8Args& p, const int32_t* ids, const float* tw, uint8_t* buf, int col,
+                                              int lane, const f4_t (&acc)[MB][4]) {
+  const int c16 = lane & 15;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) top = max(top, b8_mag(acc[mb][j][q]));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    const int e = max((int)(top >> 23) - 127 - 14, -126);  // the largest is below 2^(e + 15)
+    const float inv = __builtin_amdgcn_ldexpf(1.f, -e);    // (exact: e is at most 113)
+    const int id = ids[16 * mb + c16];
+    const bool live = id < p.n_slots;
+    char* o = reinterpret_cast<char*>(p.rows16 + (int64_t)(live ? id : 0) * p.ncol + (col - p.col0));
+    b8_rows16<4>(
+        buf, lane,
+        [&](int j) {
+          int v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v[q] = (int)__builtin_amdgcn_fmed3f(__builtin_rintf(acc[mb][j][q] * inv), 32767.f, -32767.f);
+          return uint2{((uint32_t)v[0] & 0xFFFFu) | ((uint32_t)v[1] << 16), ((uint32_t)v[2] & 0xFFFFu) | ((uint32_t)v[3] << 16)};
+        },
+        [&](int byte, uint4 v) {
+          if (live) *reinterpret_cast<uint4*>(o + byte) = v;
+        });
+    if (live && lane < 16)
+      p.row_scale[(int64_t)id * (p.ncol / 64) + (col - p.col0) / 64] =
+          top < 0x7F800000u ? tw[16 * mb + c16] * __builtin_amdgcn_ldexpf(1.f, e) : __builtin_nanf("");
+  }
+}
+
+// Slots and top-k weights of a block's rows, into LDS.
+__device__ inline void b8_load_slots(const B8Args& p, int m0, int rows, int32_t* ids, float* tw, int tid, int threads) {
+  for (int i = tid; i < rows; i += threads) {
+    const int id = p.sorted_ids[m0 + i];
+    ids[i] = id;
+    tw[i] = id < p.n_slots ? p.topk_w[id] : 0.f;
+  }
+}
+
+// The rows of slots whose expert id is out of range: zeros, columns [c0, c1).
+__device__ inline void b8_zero_rows(const B8Args& p, int m0, int rows, int c0, int c1, int tid, int threads) {
+  const int n = (c1 - c0) / 64;  // strips
+  for (int i = tid; i < rows * n * 16; i += threads) {
+    const int s = i >> 4, r = s / n, strip = s - r * n;
+    const int id = p.sorted_ids[m0 + r];
+    if (id >= p.n_slots) continue;
+    const int col = c0 + 64 * strip - p.col0;
+    *reinterpret_cast<uint2*>(p.rows16 + (int64_t)id * p.ncol + col + 4 * (i & 15)) = uint2{0u, 0u};
+    if ((i & 15) == 0) p.row_scale[(int64_t)id * (p.ncol / 64) + col / 64] = 0.f;
+  }
+}
+
+// Rows of the aligned block from m0 on that hold a slot: a prefix of it.
+__device__ inline int b8_block_rows(const B8Args& p, int m0, int bm, int lane) {
+  int n = 0;
+  for (int b = 0; b < bm; b += 64)
+    n += __popcll(__ballot(b + lane < bm && p.sorted_ids[m0 + min(b + lane, bm - 1)] < p.n_slots));
+  return n;
+}
+
 // A workgroup of WM x 4 waves computes BM = 16 MB WM rows by BN = 64 NB
 // columns: wave (wm, wn) owns rows [16 MB wm, + 16 MB) and 16 NB columns.
 template <int MB, int NB, int WM, int ST>
@@ -33,60 +173,26 @@ struct B8Cfg {
   static constexpr int SEGW = NSEG > WAVES ? NSEG / WAVES : 1;
   static constexpr int SROWS = BM < 64 ? 64 : BM;  // row scales per step (whole 64-lane loads)
   static constexpr int STAGE = BM * 128 + SROWS * 4;
-  static constexpr int LDS = ST * STAGE > 4 * BM * 4 ? ST * STAGE : 4 * BM * 4;
+  // the ring, or what the epilogues keep in its place
+  static constexpr int EPI = BM * 16 + WAVES * b8_rows_lds(4);
+  static constexpr int LDS = ST * STAGE > EPI ? ST * STAGE : EPI;
 };
 
+// One tile: rows m0 .. m0 + C::BM - 1, column tile tn.
 template <int MB, int NB, int WM, int ST, int MODE>
-__global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2))) b8_tiled(B8Args p) {
+__device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = B8Cfg<MB, NB, WM, ST>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c16 = lane & 15, kq = lane >> 4;
   const int wn = wave & 3, wm = wave >> 2;
   const int N = p.N, K = p.K, G = p.G;
 
-  int tm, tn;
-  if constexpr (MODE == B8_DENSE) {
-    // ids dealt round-robin to the 8 XCDs get consecutive logical tiles on
-    // each; logical tiles run in groups of group_m row tiles, column by column
-    const int nwg = gridDim.x;
-    int lid = blockIdx.x;
-    if ((nwg & 7) == 0) lid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
-    const int per = p.group_m * p.tiles_n;
-    const int grp = lid / per, first = grp * p.group_m;
-    const int gsz = min(p.tiles_m - first, p.group_m);
-    const int r = lid - grp * per;
-    tm = first + r % gsz;
-    tn = r / gsz;
-  } else {
-    tm = blockIdx.x / p.tiles_n;
-    tn = blockIdx.x - tm * p.tiles_n;
-  }
-  const int m0 = tm * C::BM;
   const int split = MODE == B8_DENSE ? (int)blockIdx.y : 0;
   const int gb = split * p.gps;
   const int Gl = min(G - gb, p.gps);
-
-  const uint8_t* wbytes = p.w;
-  const float* wsc = p.w_scale;
-  if constexpr (MODE != B8_DENSE) {
-    if (m0 >= *p.num_padded) return;
-    const int64_t ex = p.block_expert[tm];
-    if (ex < 0) {
-      // slots whose expert id is out of range: the down GEMM's rows are zero
-      if constexpr (MODE == B8_DOWN) {
-        for (int e = tid; e < C::BM * C::BN; e += C::THREADS) {
-          const int id = p.sorted_ids[m0 + e / C::BN];
-          const int n = tn * C::BN + e % C::BN;
-          if (id < p.n_slots && n < N) p.rows16[(int64_t)id * N + n] = 0;
-        }
-      }
-      return;
-    }
-    wbytes += ex * p.w_expert;
-    wsc += ex * p.s_expert;
-  }
+  const uint8_t* wbytes = p.w + (MODE == B8_DENSE ? 0 : ex * p.w_expert);
+  const float* wsc = p.w_scale + (MODE == B8_DENSE ? 0 : ex * p.s_expert);
 
   // 16-column block of this wave's fragment j.  gate_up: the wave's first
   // NB / 2 fragments are gate columns, the others the up columns of the same
@@ -97,7 +203,7 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
       const int b = tn * (C::BN / 32) + wn * (NB / 2) + (j % (NB / 2));
       return j < NB / 2 ? b : nblocks / 2 + b;
     }
-    return tn * (C::BN / 16) + wn * NB + j;
+    return (MODE == B8_DOWN ? p.col0 / 16 : 0) + tn * (C::BN / 16) + wn * NB + j;
   };
 
   auto rsrc = [](const void* base, int64_t bytes) {
@@ -170,50 +276,14 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[mb][j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
-  // The step's MB x NB matrix instructions, row block by row block, as one
-  // pipeline: the operand of the next row block is read while the current
-  // one multiplies, and the four multiply-adds that promote a product follow
-  // two instructions behind it, so that they issue in the shadow of the matrix
-  // instruction then running (32 cycles against 16) instead of waiting for
-  // their own.
   auto compute = [&](auto slot_c) {
     constexpr int slot = decltype(slot_c)::value;
-    const uint8_t* at = lds + slot * C::STAGE + wm * (16 * MB) * 128 + c16 * 128;
-    const float* st = reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + wm * 16 * MB + c16;
     float sw[NSW];
 #pragma unroll
     for (int u = 0; u < NSW; ++u) sw[u] = __uint_as_float(sraw[slot][u]);
-    i8_t a[2];
-    float sa[2];
-    auto read = [&](int mb) {  // the row blocks start at multiples of 16: the swizzle sees c16 alone
-      a[mb & 1] = cat8(*reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, kq) * 16),
-                       *reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, 4 + kq) * 16));
-      sa[mb & 1] = st[16 * mb];
-    };
-    constexpr int D = NB == 4 && MB > 1 ? 3 : (MB * NB > 2 ? 2 : 1);  // products in flight ahead of their promotion (fewer than NB, or both of two)
-    f4_t P[D + 1];
-    float f[2][NSW];
-    auto promote = [&](int i) {
-      const int mb = i / NB, j = i - mb * NB;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        acc[mb][j][q] = fmaf(f[mb & 1][NSW == 2 ? j / (NB / 2) : 0], P[i % (D + 1)][q], acc[mb][j][q]);
-    };
-    read(0);
-#pragma unroll
-    for (int i = 0; i < MB * NB; ++i) {
-      const int mb = i / NB, j = i - mb * NB;
-      if (j == 0 && mb + 1 < MB) read(mb + 1);
-      P[i % (D + 1)] = b8_mfma(cat8(braw[slot][j][0], braw[slot][j][1]), a[mb & 1]);
-      if (j == (NB > D ? D - 1 : 0)) {
-#pragma unroll
-        for (int u = 0; u < NSW; ++u) f[mb & 1][u] = sa[mb & 1] * sw[u];
-      }
-      if (i >= D) promote(i - D);
-      __builtin_amdgcn_sched_barrier(0);  // keeps this order: left to itself the scheduler puts each product's promotion right behind it
-    }
-#pragma unroll
-    for (int i = MB * NB - D; i < MB * NB; ++i) promote(i);
+    b8_step<MB, NB, NSW>(lds + slot * C::STAGE + wm * (16 * MB) * 128 + c16 * 128,
+                         reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + wm * 16 * MB + c16, c16, kq,
+                         braw[slot], sw, acc);
   };
 
   auto gclamp = [&](int g) { return g < Gl ? g : Gl - 1; };
@@ -280,99 +350,340 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
             b8_codes(acc[mb][j][0], acc[mb][j][1], acc[mb][j][2], acc[mb][j][3], d);
       if (wn == 0 && kq == 0) p.out_scale[(int64_t)tn * p.out_rows + row] = s;
     }
-  } else {
+  } else if constexpr (MODE == B8_DOWN) {
+    const int col = nblk(0) * 16;
+    // the rows' slots and weights, into LDS first: a load per row block between
+    // the stores would wait for each in turn
+    int32_t* lid = reinterpret_cast<int32_t*>(lds);
+    float* ltw = reinterpret_cast<float*>(lid + C::BM);
+    __syncthreads();  // every wave is done with the stage ring
+    b8_load_slots(p, m0, C::BM, lid, ltw, tid, C::THREADS);
+    __syncthreads();
+    uint8_t* buf = lds + C::BM * 8 + wave * b8_rows_lds(4);
+    if (col < p.col0 + p.ncol) b8_store_rows<MB>(p, lid + (mw - m0), ltw + (mw - m0), buf, col, lane, acc);
+  } else if (p.part) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       const int m = mw + 16 * mb + c16;
-      float f = 1.f;
-      int64_t orow = m;
-      if constexpr (MODE == B8_DENSE) {
-        if (m >= p.M) continue;
-      } else {
-        const int id = p.sorted_ids[m];
-        if (id >= p.n_slots) continue;
-        f = p.topk_w[id];
-        orow = id;
-      }
+      if (m >= p.M) continue;
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int b = nblk(j);
-        if (b >= nblocks) continue;
-        const f4_t v = acc[mb][j];
-        const int n = b * 16 + 4 * kq;
-        if constexpr (MODE == B8_DENSE) {
-          if (p.part) {
-            *reinterpret_cast<f4_t*>(p.part + ((int64_t)split * p.M + orow) * N + n) = v;
-            continue;
-          }
-        }
-        const int bf16 = MODE == B8_DOWN ? 1 : p.out_bf16;
-        uint16_t* o = (MODE == B8_DOWN ? p.rows16 : static_cast<uint16_t*>(p.out)) + orow * N + n;
-        auto cv = [&](float x) -> uint32_t { return bf16 ? float_to_bf16_bits(x * f) : float_to_f16_bits(x * f); };
-        *reinterpret_cast<uint2*>(o) = uint2{cv(v[0]) | (cv(v[1]) << 16), cv(v[2]) | (cv(v[3]) << 16)};
-      }
+      for (int j = 0; j < NB; ++j)
+        if (nblk(j) < nblocks)
+          *reinterpret_cast<f4_t*>(p.part + ((int64_t)split * p.M + m) * N + nblk(j) * 16 + 4 * kq) = acc[mb][j];
+    }
+  } else {
+    __syncthreads();  // every wave is done with the stage ring
+    uint8_t* buf = lds + wave * b8_rows_lds(NB);
+    const int col = nblk(0) * 16, cols = min(16 * NB, N - col);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int m = mw + 16 * mb + c16;
+      char* o = reinterpret_cast<char*>(static_cast<uint16_t*>(p.out) + (int64_t)m * N + col);
+      b8_rows16<NB>(
+          buf, lane,
+          [&](int j) {
+            auto cv = [&](float x) -> uint32_t { return p.out_bf16 ? float_to_bf16_bits(x) : float_to_f16_bits(x); };
+            const f4_t v = acc[mb][j];
+            return uint2{cv(v[0]) | (cv(v[1]) << 16), cv(v[2]) | (cv(v[3]) << 16)};
+          },
+          [&](int byte, uint4 v) {
+            if (m < p.M && byte < 2 * cols) *reinterpret_cast<uint4*>(o + byte) = v;
+          });
     }
   }
 #endif
 }
 
-template <int MB, int NB, int WM, int ST, int MODE>
-hipError_t launch_t(const B8Args& a, dim3 grid, hipStream_t s) {
-  using C = B8Cfg<MB, NB, WM, ST>;
-  const hipError_t e = allow_lds<b8_tiled<MB, NB, WM, ST, MODE>>(C::LDS);
-  if (e != hipSuccess) return e;
-  return launch_timed(b8_tiled<MB, NB, WM, ST, MODE>, grid, dim3(C::THREADS), (size_t)C::LDS, s, a);
+template <int MB, int NB, int WM, int ST>
+__global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2))) b8_dense(B8Args p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  // ids dealt round-robin to the 8 XCDs get consecutive logical tiles on
+  // each; logical tiles run in groups of group_m row tiles, column by column
+  const int nwg = gridDim.x;
+  int lid = blockIdx.x;
+  if ((nwg & 7) == 0) lid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
+  const int per = p.group_m * p.tiles_n;
+  const int grp = lid / per, first = grp * p.group_m;
+  const int gsz = min(p.tiles_m - first, p.group_m);
+  const int r = lid - grp * per;
+  b8_tile<MB, NB, WM, ST, B8_DENSE>(p, lds, (first + r % gsz) * B8Cfg<MB, NB, WM, ST>::BM, 0, r / gsz);
+#endif
 }
 
-template <int MODE>
-hipError_t dispatch(const B8Tile& t, const B8Args& a, dim3 grid, hipStream_t s) {
+// A grouped tile of up to 16 MB rows: an aligned block is run with as many row
+// blocks (a power of two) as hold slots, so that the half-empty blocks that end
+// each expert's segment cost what they hold.
+template <int MB, int MODE>
+__device__ __forceinline__ void b8_grouped_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn, int rows) {
+  if constexpr (MB > 1) {
+    if (rows <= 8 * MB) {
+      b8_grouped_tile<MB / 2, MODE>(p, lds, m0, ex, tn, rows);
+      return;
+    }
+  }
+  b8_tile<MB, 4, 1, (MB <= 4 ? 3 : 2), MODE>(p, lds, m0, ex, tn);
+}
+
+template <int MB, int MODE>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_grouped(B8Args p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
+  const int m0 = tm * 16 * MB;
+  if (m0 >= *p.num_padded) return;
+  const int64_t ex = p.block_expert[tm];
+  if (ex < 0) {
+    if constexpr (MODE == B8_DOWN)
+      b8_zero_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
+    return;
+  }
+  b8_grouped_tile<MB, MODE>(p, lds, m0, ex, tn, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+#endif
+}
+
+// The down GEMM with short K: the block's activation rows lie in LDS whole, and
+// the workgroup walks its column tiles in one stream of weight loads, with no
+// barrier and no refill between tiles (with two or four groups of K per tile
+// the loads' latency at each tile's start would cost as much as its math).
+template <int MB>
+__device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int c0, int c1) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, kq = lane >> 4;
+  const int K = p.K, G = p.G;
+  constexpr int ROWS = 16 * MB;
+  auto rsrc = [](const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+  };
+  const auto ra = rsrc(p.a, (int64_t)p.a_rows * K);
+  const auto rw = rsrc(p.w + ex * p.w_expert, p.w_expert);
+  const auto rws = rsrc(p.w_scale + ex * p.s_expert, p.s_expert * 4);
+  // rows: group g at g * ROWS * 128, chunks swizzled; scales [G][ROWS] behind
+  float* ls = reinterpret_cast<float*>(lds + G * ROWS * 128);
+  for (int s = wave; s < G * ROWS / 8; s += 4) {
+    const int g = s / (ROWS / 8), seg = s - g * (ROWS / 8);
+    const int r = seg * 8 + (lane >> 3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(lds + s * 1024), 16, (m0 + r) * K + swz<8>(r, lane & 7) * 16,
+                                             g * 128, 0, 0);
+  }
+  for (int i = tid; i < G * ROWS; i += 256) {
+    const int g = i / ROWS;
+    ls[i] = p.a_scale[(int64_t)g * p.a_rows + m0 + i - g * ROWS];
+  }
+  int32_t* lid = reinterpret_cast<int32_t*>(ls + G * ROWS);
+  float* ltw = reinterpret_cast<float*>(lid + ROWS);
+  b8_load_slots(p, m0, ROWS, lid, ltw, tid, 256);
+  uint8_t* buf = reinterpret_cast<uint8_t*>(ltw + ROWS) + wave * b8_rows_lds(4);
+
+  u4_t braw[2][4][2];
+  float sw[2][1];
+  int col = c0 + 64 * wave, g = 0;      // of the step being multiplied
+  int acol = col, ag = 0;               // of the step being loaded
+  auto issue = [&](auto slot_c) {
+    constexpr int slot = decltype(slot_c)::value;
+    const int cc = min(acol, c1 - 64);  // past the end: loaded again, not stored
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        braw[slot][j][h] = __builtin_bit_cast(
+            u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + 1024 * h, ((cc / 16 + j) * G + ag) * 2048, 0));
+    sw[slot][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, 0, ((cc / 128) * G + ag) * 4, 0));
+    if (++ag == G) {
+      ag = 0;
+      acol += 256;
+    }
+  };
+  f4_t acc[MB][4];
+  auto zero = [&] {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[mb][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  zero();
+  issue(std::integral_constant<int, 0>{});
+  __builtin_amdgcn_s_waitcnt(0);  // this wave's loads into LDS have landed
+  __syncthreads();
+  auto step = [&](auto slot_c) {
+    constexpr int slot = decltype(slot_c)::value;
+    issue(std::integral_constant<int, slot ^ 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+    b8_step<MB, 4, 1>(lds + g * ROWS * 128 + c16 * 128, ls + g * ROWS + c16, c16, kq, braw[slot], sw[slot], acc);
+    if (++g == G) {
+      if (col < c1) b8_store_rows<MB>(p, lid, ltw, buf, col, lane, acc);
+      zero();
+      g = 0;
+      col += 256;
+    }
+  };
+  const int steps = (c1 - c0 + 255) / 256 * G;
+  for (int s = 0; s < steps; s += 2) {
+    step(std::integral_constant<int, 0>{});
+    if (s + 1 < steps) step(std::integral_constant<int, 1>{});
+  }
+#endif
+}
+
+template <int MB>
+__device__ __forceinline__ void b8_down_dispatch(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int c0, int c1, int rows) {
+  if constexpr (MB > 1) {
+    if (rows <= 8 * MB) {
+      b8_down_dispatch<MB / 2>(p, lds, m0, ex, c0, c1, rows);
+      return;
+    }
+  }
+  b8_down_tiles<MB>(p, lds, m0, ex, c0, c1);
+}
+
+template <int MB>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_down_short(B8Args p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
+  const int m0 = tm * 16 * MB;
+  if (m0 >= *p.num_padded) return;
+  const int64_t ex = p.block_expert[tm];
+  const int c0 = p.col0 + tn * p.cols_wg, c1 = min(c0 + p.cols_wg, p.col0 + p.ncol);
+  if (ex < 0) {
+    b8_zero_rows(p, m0, 16 * MB, c0, c1, threadIdx.x, 256);
+    return;
+  }
+  b8_down_dispatch<MB>(p, lds, m0, ex, c0, c1, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+#endif
+}
+
+// y[t][col0 + c] = RNE(sum over the token's topk slots of q * scale), in slot
+// order; eight columns a thread.
+__global__ void __launch_bounds__(256) b8_combine_kernel(const uint4* __restrict__ rows, const float* __restrict__ scale,
+                                                         int topk, int n, int col0, int ncol, int64_t elems,
+                                                         uint4* __restrict__ y, int out_bf16) {
+  const int ncol8 = ncol / 8, strips = ncol / 64;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < elems; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / ncol8;
+    const int c = (int)(i - t * ncol8);
+    float v[8] = {};
+    for (int j = 0; j < topk; ++j) {
+      const uint4 w = rows[(t * topk + j) * ncol8 + c];
+      const float f = scale[(t * topk + j) * strips + c / 8];
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = fmaf((float)(int16_t)(u[q >> 1] >> (16 * (q & 1))), f, v[q]);
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      o[q] = out_bf16 ? (uint32_t)float_to_bf16_bits(v[2 * q]) | ((uint32_t)float_to_bf16_bits(v[2 * q + 1]) << 16)
+                      : (uint32_t)float_to_f16_bits(v[2 * q]) | ((uint32_t)float_to_f16_bits(v[2 * q + 1]) << 16);
+    y[t * (n / 8) + col0 / 8 + c] = uint4{o[0], o[1], o[2], o[3]};
+  }
+}
+
+template <int MB, int NB, int WM, int ST>
+hipError_t launch_dense(const B8Args& a, dim3 grid, hipStream_t s) {
+  using C = B8Cfg<MB, NB, WM, ST>;
+  const hipError_t e = allow_lds<b8_dense<MB, NB, WM, ST>>(C::LDS);
+  if (e != hipSuccess) return e;
+  return launch_timed(b8_dense<MB, NB, WM, ST>, grid, dim3(C::THREADS), (size_t)C::LDS, s, a);
+}
+
+hipError_t dispatch_dense(const B8Tile& t, const B8Args& a, dim3 grid, hipStream_t s) {
 #define HQ_B8(bm_, bn_, st_, MB, NB, WM) \
-  if (t.bm == bm_ && t.bn == bn_ && t.stages == st_) return launch_t<MB, NB, WM, st_, MODE>(a, grid, s);
+  if (t.bm == bm_ && t.bn == bn_ && t.stages == st_) return launch_dense<MB, NB, WM, st_>(a, grid, s);
   HQ_B8(16, 256, 3, 1, 4, 1)
   HQ_B8(32, 256, 3, 2, 4, 1)
   HQ_B8(64, 256, 2, 4, 4, 1)
   HQ_B8(64, 256, 3, 4, 4, 1)
   HQ_B8(128, 256, 2, 8, 4, 1)
-  if constexpr (MODE == B8_DENSE) {
-    HQ_B8(256, 256, 2, 8, 4, 2)
-    HQ_B8(128, 128, 2, 8, 2, 1)
-    HQ_B8(128, 128, 3, 8, 2, 1)
-    HQ_B8(64, 128, 3, 4, 2, 1)
-    HQ_B8(64, 128, 4, 4, 2, 1)
-    HQ_B8(32, 128, 4, 2, 2, 1)
-    HQ_B8(16, 128, 4, 1, 2, 1)
-  }
+  HQ_B8(256, 256, 2, 8, 4, 2)
+  HQ_B8(128, 128, 2, 8, 2, 1)
+  HQ_B8(128, 128, 3, 8, 2, 1)
+  HQ_B8(64, 128, 3, 4, 2, 1)
+  HQ_B8(64, 128, 4, 4, 2, 1)
+  HQ_B8(32, 128, 4, 2, 2, 1)
+  HQ_B8(16, 128, 4, 1, 2, 1)
 #undef HQ_B8
   return hipErrorInvalidValue;
 }
 
+template <int MB>
+hipError_t launch_grouped(int mode, const B8Args& a, dim3 grid, hipStream_t s) {
+  // the largest ring of the row counts a block may run with
+  constexpr size_t lds = std::max<size_t>({(size_t)B8Cfg<1, 4, 1, 3>::LDS, (size_t)B8Cfg<(MB >= 2 ? 2 : 1), 4, 1, 3>::LDS,
+                                           (size_t)B8Cfg<(MB >= 4 ? 4 : 1), 4, 1, 3>::LDS,
+                                           (size_t)B8Cfg<MB, 4, 1, (MB <= 4 ? 3 : 2)>::LDS});
+  if (mode == B8_GATE_UP) {
+    const hipError_t e = allow_lds<b8_grouped<MB, B8_GATE_UP>>(lds);
+    return e != hipSuccess ? e : launch_timed(b8_grouped<MB, B8_GATE_UP>, grid, dim3(256), lds, s, a);
+  }
+  const hipError_t e = allow_lds<b8_grouped<MB, B8_DOWN>>(lds);
+  return e != hipSuccess ? e : launch_timed(b8_grouped<MB, B8_DOWN>, grid, dim3(256), lds, s, a);
+}
+
+constexpr int kShortLds = 72 * 1024;  // two workgroups a CU
+
+template <int MB>
+hipError_t launch_short(const B8Args& a, dim3 grid, hipStream_t s) {
+  const hipError_t e = allow_lds<b8_down_short<MB>>(kShortLds);
+  return e != hipSuccess ? e : launch_timed(b8_down_short<MB>, grid, dim3(256), (size_t)(16 * MB * (a.G * 132 + 8) + 4 * b8_rows_lds(4)), s, a);
+}
+
 }  // namespace
 
-bool b8_tile_ok(int mode, const B8Tile& t) {
+bool b8_tile_ok(const B8Tile& t) {
   if (t.bn == 256) {
     if (t.bm == 16 || t.bm == 32) return t.stages == 3;
     if (t.bm == 64) return t.stages == 2 || t.stages == 3;
-    return (t.bm == 128 || (t.bm == 256 && mode == B8_DENSE)) && t.stages == 2;
+    return (t.bm == 128 || t.bm == 256) && t.stages == 2;
   }
-  if (t.bn != 128 || mode != B8_DENSE) return false;
+  if (t.bn != 128) return false;
   if (t.bm == 128) return t.stages == 2 || t.stages == 3;
   if (t.bm == 64) return t.stages == 3 || t.stages == 4;
   return (t.bm == 16 || t.bm == 32) && t.stages == 4;
 }
 
-int launch_b8_tiled(int mode, const B8Tile& t, const B8Args& a, int64_t blocks, void* stream) {
-  if (!b8_tile_ok(mode, t) || a.G < 1 || a.gps < 1) return (int)hipErrorInvalidValue;
+int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream) {
+  if (!b8_tile_ok(t) || a.G < 1 || a.gps < 1) return (int)hipErrorInvalidValue;
+  // every split holds at least one group and together they cover K
+  if ((int64_t)(t.split - 1) * a.gps >= a.G || (int64_t)t.split * a.gps < a.G) return (int)hipErrorInvalidValue;
+  return (int)dispatch_dense(t, a, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)t.split), static_cast<hipStream_t>(stream));
+}
+
+int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.G < 1 || a.gps != a.G || a.N % (mode == B8_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
+  if (mode == B8_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
   B8Args b = a;
-  if (mode == B8_DENSE) {
-    // every split holds at least one group and together they cover K
-    if ((int64_t)(t.split - 1) * a.gps >= a.G || (int64_t)t.split * a.gps < a.G) return (int)hipErrorInvalidValue;
-    return (int)dispatch<B8_DENSE>(t, b, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)t.split), s);
+  const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) + 4 * b8_rows_lds(4) <= kShortLds;
+  if (whole) {
+    // columns a workgroup walks: at least four tiles' worth where that leaves
+    // the chip four workgroups a CU, and never more than the window
+    const int64_t tiles = (a.ncol + 255) / 256;
+    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(tiles, tiles * blocks / 1024));
+    b.cols_wg = (int)(256 * per);
+    b.tiles_n = (int)((tiles + per - 1) / per);
+  } else {
+    b.tiles_n = (int)((mode == B8_DOWN ? a.ncol : a.N) + 255) / 256;
   }
-  if (a.gps != a.G || a.N % (mode == B8_GATE_UP ? 256 : 16) || blocks < 1 || blocks * a.tiles_n > INT32_MAX)
-    return (int)hipErrorInvalidValue;
-  const dim3 grid((unsigned)(blocks * a.tiles_n));
-  return mode == B8_GATE_UP ? (int)dispatch<B8_GATE_UP>(t, b, grid, s) : (int)dispatch<B8_DOWN>(t, b, grid, s);
+  if (blocks * b.tiles_n > INT32_MAX) return (int)hipErrorInvalidValue;
+  const dim3 grid((unsigned)(blocks * b.tiles_n));
+  switch (bm) {
+    case 16: return whole ? (int)launch_short<1>(b, grid, s) : (int)launch_grouped<1>(mode, b, grid, s);
+    case 32: return whole ? (int)launch_short<2>(b, grid, s) : (int)launch_grouped<2>(mode, b, grid, s);
+    case 64: return whole ? (int)launch_short<4>(b, grid, s) : (int)launch_grouped<4>(mode, b, grid, s);
+    case 128: return whole ? (int)launch_short<8>(b, grid, s) : (int)launch_grouped<8>(mode, b, grid, s);
+  }
+  return (int)hipErrorInvalidValue;
+}
+
+int launch_b8_combine(const B8Args& a, int64_t t, void* stream) {
+  const int64_t elems = t * a.ncol / 8;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((elems + 255) / 256, 16384));
+  return (int)launch_timed(b8_combine_kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+                           reinterpret_cast<const uint4*>(a.rows16), a.row_scale, a.topk, a.N, a.col0, a.ncol, elems,
+                           static_cast<uint4*>(a.out), a.out_bf16);
 }
 
 }  // namespace hq
