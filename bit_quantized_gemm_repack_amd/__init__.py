@@ -287,6 +287,24 @@ def _stream_ptr(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
 
 
+class _on:
+    """Makes `device` current where it is not (a launch goes to the current
+    device, its stream to the tensors')."""
+    __slots__ = ("index", "was")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.was != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.was != self.index:
+            torch.cuda.set_device(self.was)
+
+
 _TORCH_OUT = {F16: torch.float16, BF16: torch.bfloat16}
 _LOGITS = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _DT_NAME = {F16: "f16", BF16: "bf16", FP8_E4M3: "fp8", INT8: "int8", FP4_E2M1: "mxfp4"}
@@ -350,6 +368,8 @@ class Plan:
             self.fallback = (f"{_DT_NAME.get(quant.act, quant.act)} activations requested: {e}; running "
                              f"{_DT_NAME[q16.act]} activations")
         self._h = handle
+        self._block8 = self.quant.act_scale == ASCALE_BLOCK_F32
+        self._ws_need = {}  # rows -> workspace bytes of a block-scaled GEMM
         self._ws = {}
         self._act_buf = {}
 
@@ -388,10 +408,6 @@ class Plan:
             ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
             self._ws[dev] = ws
         return ws
-
-    @property
-    def _block8(self) -> bool:
-        return self.quant.act_scale == ASCALE_BLOCK_F32
 
     # -- repack ---------------------------------------------------------
     def _check_block_weight(self, codes, scales):
@@ -441,6 +457,8 @@ class Plan:
     def gemm(self, a: torch.Tensor, w: torch.Tensor, meta: torch.Tensor, a_scale: Optional[torch.Tensor] = None,
              out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
         """out[m, n] = A . W_deq^T (see include/hq.h, hq_gemm)."""
+        if self._block8:
+            return self._gemm_block(a, w, meta, a_scale, out, ws)
         _dev(a, "a"), _dev(w, "w"), _dev(meta, "meta")
         act4 = self.quant.act == FP4_E2M1
         if a_scale is not None:
@@ -448,11 +466,6 @@ class Plan:
             if a_scale.dtype != (torch.uint8 if act4 else torch.float32):
                 raise ValueError("a_scale must be uint8 E8M0 [m, k/32] (MXFP4 activations) or float32 [m]")
         m = a.shape[0]
-        if self._block8:
-            if a_scale is None or a_scale.numel() != m * (self.k // 128):
-                raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
-            if a.element_size() != 1:
-                raise ValueError("a must hold one-byte fp8 codes")
         if act4:  # MXFP4 codes two per byte: [m, k/2] bytes (or [m, k/8] int32 words)
             if a.dim() != 2 or a.shape[1] * a.element_size() != self.k // 2:
                 raise ValueError(f"a must hold [m, {self.k // 2}] bytes of packed MXFP4 codes")
@@ -471,6 +484,39 @@ class Plan:
                              ws_bytes, _stream_ptr(a.device)))
         return out
 
+
+    def _gemm_block(self, a, w, meta, a_scale, out, ws):
+        """gemm of a w8a8_block plan.  Split-K partials live in a workspace of
+        the call's own unless one is given, so that calls on several streams, or
+        captured into several graphs, do not share one."""
+        dev = a.device
+        for t, name in ((a, "a"), (w, "w"), (meta, "meta"), (a_scale, "a_scale")):
+            if _dev(t, name).device != dev:
+                raise ValueError(f"{name} must be on a's device")
+        if a.dim() != 2 or a.shape[1] != self.k or a.element_size() != 1:
+            raise ValueError(f"a must hold one-byte fp8 codes [m, {self.k}]")
+        m = a.shape[0]
+        if a_scale.dtype != torch.float32 or a_scale.numel() != m * (self.k // 128):
+            raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
+        self._check_block_layout(w, meta)
+        if out is None:
+            out = torch.empty((m, self.n), dtype=_TORCH_OUT[self.quant.out], device=dev)
+        elif _dev(out, "out").shape != (m, self.n) or out.dtype != _TORCH_OUT[self.quant.out] or out.device != dev:
+            raise ValueError(f"out must be {_TORCH_OUT[self.quant.out]} [m, {self.n}] on a's device")
+        need = self._ws_need.get(m)
+        if need is None:
+            need = self._ws_need[m] = self.workspace_bytes(m)
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        with _on(dev):
+            _check(lib().hq_gemm(self._h, m, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), meta.data_ptr(), out.data_ptr(),
+                                 _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_ptr(dev)))
+        return out
+
+    def _check_block_layout(self, w, meta):
+        if w.numel() * w.element_size() < self.num_experts * self.n * self.k or \
+                meta.numel() * meta.element_size() < self.num_experts * (-(-self.n // 128)) * (self.k // 128) * 4:
+            raise ValueError("w and meta must be what repack returned for this plan")
 
     def linear(self, x: torch.Tensor, w: torch.Tensor, meta: torch.Tensor, out: Optional[torch.Tensor] = None,
                ws: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -520,6 +566,7 @@ class Plan:
         if a_scale is not None:
             _dev(a_scale, "a_scale")
         m = a.shape[0]
+        self._ws_need.pop(m, None)
         out = torch.empty((m, self.n), dtype=_TORCH_OUT.get(self.quant.out, torch.float16), device=a.device)
         if self.epi == EPI_I32_ACC:
             out = torch.empty((m, self.n, self.k // 128), dtype=torch.int32, device=a.device)
@@ -553,6 +600,7 @@ class Plan:
 
     def set_tuning(self, m: int, tuning: Optional[dict]):
         """Install a tuning for exactly m rows (None removes m's entry)."""
+        self._ws_need.pop(int(m), None)
         t = None if tuning is None else Tuning(**{f: int(tuning.get(f, 0)) for f in _TUNING_FIELDS})
         _check(lib().hq_plan_set_tuning(self._h, int(m), None if t is None else ctypes.byref(t)))
 
@@ -669,16 +717,18 @@ def quantize_blocks(x: torch.Tensor, silu_mul: bool = False, codes: Optional[tor
         if k % 2:
             raise ValueError("x must be [m, 2k] with silu_mul")
         k //= 2
+    dev = x.device
     if codes is None:
-        codes = torch.empty((m, k), dtype=torch.uint8, device=x.device)
-    elif _dev(codes, "codes").shape != (m, k) or codes.element_size() != 1 or codes.device != x.device:
+        codes = torch.empty((m, k), dtype=torch.uint8, device=dev)
+    elif _dev(codes, "codes").shape != (m, k) or codes.element_size() != 1 or codes.device != dev:
         raise ValueError("codes must be 1-byte [m, k] on x's device")
     if scales is None:
-        scales = torch.empty((k // 128, m), dtype=torch.float32, device=x.device)
-    elif _dev(scales, "scales").shape != (k // 128, m) or scales.dtype != torch.float32 or scales.device != x.device:
+        scales = torch.empty((k // 128, m), dtype=torch.float32, device=dev)
+    elif _dev(scales, "scales").shape != (k // 128, m) or scales.dtype != torch.float32 or scales.device != dev:
         raise ValueError("scales must be float32 [k/128, m] on x's device")
-    _check(lib().hq_quantize_blocks(m, k, BF16 if x.dtype == torch.bfloat16 else F16, 1 if silu_mul else 0,
-                                    x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream_ptr(x.device)))
+    with _on(dev):
+        _check(lib().hq_quantize_blocks(m, k, BF16 if x.dtype == torch.bfloat16 else F16, 1 if silu_mul else 0,
+                                        x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream_ptr(dev)))
     return codes, scales
 
 
@@ -796,7 +846,12 @@ class MoePlan(Plan):
             if a_scale is None or a_scale.dtype != torch.float32 or a_scale.numel() != rows * (self.k // 128) or \
                     a.element_size() != 1 or a.numel() != rows * self.k:
                 raise ValueError(f"a must hold [{rows}, {self.k}] one-byte codes and a_scale float32 [{self.k // 128}, {rows}]")
-        if ws is None:
+            self._check_block_layout(w, meta)
+            if ws is None and self.epi == EPI_TOPK_COMBINE:  # of the call's own, as in gemm
+                b = ctypes.c_size_t()
+                _check(lib().hq_moe_workspace_bytes(self._h, int(t), int(topk), ctypes.byref(b)))
+                ws = torch.empty(b.value, dtype=torch.uint8, device=dev)
+        if ws is None and not self._block8:
             ws = self.moe_workspace(t, topk, dev)
         ws_bytes = 0 if ws is None else ws.numel()
         _check(lib().hq_moe_gemm(self._h, int(t), int(topk), _ptr(a), _ptr(a_scale), _ptr(sorted_ids),
@@ -865,8 +920,9 @@ def route_topk(logits: torch.Tensor, topk: int, renormalize: bool = True):
     t, experts = logits.shape
     ids = torch.empty((t, int(topk)), dtype=torch.int32, device=logits.device)
     w = torch.empty((t, int(topk)), dtype=torch.float32, device=logits.device)
-    _check(lib().hq_route_topk(t, experts, int(topk), _LOGITS[logits.dtype], logits.data_ptr(), 1 if renormalize else 0,
-                               ids.data_ptr(), w.data_ptr(), _stream_ptr(logits.device)))
+    with _on(logits.device):
+        _check(lib().hq_route_topk(t, experts, int(topk), _LOGITS[logits.dtype], logits.data_ptr(), 1 if renormalize else 0,
+                                   ids.data_ptr(), w.data_ptr(), _stream_ptr(logits.device)))
     return ids, w
 
 
@@ -889,11 +945,13 @@ def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2
         raise ValueError(f"topk_ids / topk_w must be int32 / float32 [{t}, {topk}]")
     ws = torch.empty(t * topk * down.k, dtype=torch.float32, device=x.device)
     out = torch.empty((t, down.n), dtype=_TORCH_OUT[down.quant.out], device=x.device)
-    _check(lib().hq_moe_layer_few(gate_up._h, down._h, t, topk, BF16 if x.dtype == torch.bfloat16 else F16,
-                                  x.data_ptr(), F32 if logits is None else _LOGITS[logits.dtype], _ptr(logits),
-                                  1 if renormalize else 0, ids.data_ptr(), w.data_ptr(), w1.data_ptr(), m1.data_ptr(),
-                                  w2.data_ptr(), m2.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel() * 4,
-                                  _stream_ptr(x.device)))
+    gate_up._check_block_layout(w1, m1), down._check_block_layout(w2, m2)
+    with _on(x.device):
+        _check(lib().hq_moe_layer_few(gate_up._h, down._h, t, topk, BF16 if x.dtype == torch.bfloat16 else F16,
+                                      x.data_ptr(), F32 if logits is None else _LOGITS[logits.dtype], _ptr(logits),
+                                      1 if renormalize else 0, ids.data_ptr(), w.data_ptr(), w1.data_ptr(),
+                                      m1.data_ptr(), w2.data_ptr(), m2.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                                      ws.numel() * 4, _stream_ptr(x.device)))
     return out
 
 

@@ -224,39 +224,70 @@ static const hq_tuning* tuned_for(const hq_plan* p, int64_t m) {
   return &p->user;
 }
 
-// fp8 x fp8 with 128-block scales (block8.h): the weight-streaming kernel for
-// few rows, the tiled one beyond.
+// fp8 x fp8 with 128-block scales (block8.h).  The rules follow a sweep on
+// MI355X of every shape and K split over 1 .. 2048 rows and (N, K) = (576,
+// 7168), (2112, 7168), (4096, 7168), (7168, 2048), (14336, 4096), (4096, 14336),
+// (24576, 1536), (1024, 1024), weights from memory: their choice took 1.2 %
+// more than the best one on the geometric mean, 19 % at most.
 static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
   Exec e{};
   const int64_t N = p->layer.n, G = p->layer.k / kFragK, mm = m > 0 ? m : 1;
-  const bool skinny = u.kernel ? u.kernel == KER_SKINNY : mm <= 64;
+  const int64_t n16 = cdiv(N, 16), n128 = cdiv(N, 128), blocks = n16 * cdiv(mm, 16);
+  // Few rows: 16-row x 16-column blocks (32 where there are many), up to 16
+  // rows unless whole 128-column tiles fill the chip (N = 24576, K = 1536, one
+  // row: 9.7 against 12.3 us), beyond while the blocks are few (33 rows of N =
+  // 576: 8.2 us against 10 for the best tile).
+  bool skinny = mm <= 16 ? n128 < 160 : (mm <= 128 && blocks <= 512);
+  if (u.kernel) skinny = u.kernel == KER_SKINNY;
   int64_t split = 1;
   if (skinny) {
     e.kernel = KER_SKINNY;
     SkinnyCfg& c = e.sk;
-    c.mb = mm <= 16 ? 1 : (mm <= 32 ? 2 : 4);
-    c.nb = 1;
-    c.waves = 8;
+    c.mb = 1;
+    // one column block a workgroup while that leaves under a workgroup and a
+    // half a CU and K is long (N = 4096, one row: 9.0 against 9.5 us; N = 14336:
+    // two 14.0, one 25)
+    c.nb = (mm <= 16 ? n16 < 384 && G > 8 : blocks <= 200 && G > 8) ? 1 : 2;
+    c.waves = 4;  // (8: 10.1 against 9.0 us at N = 4096, K = 7168)
     c.stages = 1;
     if (u.tile_m) c.mb = u.tile_m / 16;
     if (u.tile_n) c.nb = u.tile_n / 16;
     if (u.waves) c.waves = u.waves;
     e.tiles_m = cdiv(mm, 16 * std::max(1, c.mb));
-    e.tiles_n = cdiv(N / 16, std::max(1, c.nb));
-    split = u.split_k ? u.split_k : 1;
+    e.tiles_n = cdiv(n16, std::max(1, c.nb));
+    if (u.split_k) split = u.split_k;
   } else {
     e.kernel = KER_TILED;
-    e.tl.bm = mm <= 16 ? 16 : (mm <= 32 ? 32 : (mm <= 64 ? 64 : 128));
-    e.tl.nbw = mm <= 64 ? 2 : 4;
+    // The lowest row tile that gives no more than so many tiles.  With long K
+    // (32 groups on) the rows are covered in one or two tiles first, and a
+    // split of K fills the chip (128 rows of (4096, 7168): 64-row tiles in 4
+    // splits 15.5, 16-row tiles 19.8 us); with short K a split's second pass
+    // costs more than the lower tile's weight traffic (128 rows of (7168,
+    // 2048): 32-row tiles 7.8, 64-row tiles in 2 splits 13.2 us).
+    const bool longk = G >= 32;
+    const struct {
+      int bm;
+      int64_t most;
+    } tiles[] = {{16, 256}, {32, 256}, {64, G >= 96 ? 256 : 512}, {128, G >= 16 ? 768 : 1200}};
+    e.tl.bm = 128;
+    e.tl.nbw = 4;  // 256 columns: enough tiles whatever the shape
+    for (const auto& t : tiles) {
+      if (longk && ((t.bm == 16 && mm > 32) || (t.bm == 32 && mm > 64))) continue;
+      if (cdiv(mm, t.bm) * n128 > t.most) continue;
+      e.tl.bm = t.bm;
+      e.tl.nbw = 2;
+      break;
+    }
     e.tl.gm = u.tile_group ? u.tile_group : 8;
     if (u.tile_m) e.tl.bm = u.tile_m;
     if (u.tile_n) e.tl.nbw = u.tile_n / 64;
-    e.tl.stages = u.stages ? u.stages : (e.tl.nbw == 4 ? (e.tl.bm <= 32 ? 3 : 2) : (e.tl.bm <= 64 ? 4 : 3));
+    e.tl.stages = u.stages ? u.stages : (e.tl.nbw == 4 || e.tl.bm >= 128 ? 2 : (e.tl.bm == 64 ? 3 : 4));
     e.tiles_m = cdiv(mm, std::max(1, e.tl.bm));
     e.tiles_n = cdiv(N, 64 * std::max(1, e.tl.nbw));
-    const int64_t tiles = e.tiles_m * e.tiles_n;
+    const int64_t count = e.tiles_m * e.tiles_n, most = e.tl.bm < 128 ? 256 : (G >= 96 ? 512 : 400);
     if (u.split_k) split = u.split_k;
-    else if (tiles < 256) split = std::min<int64_t>(cdiv(256, tiles), std::max<int64_t>(1, G / 2));
+    else
+      while (e.tl.nbw == 2 && split < 8 && count * split * 2 <= most && G / (split * 2) >= 12) split *= 2;
   }
   split = std::max<int64_t>(1, std::min<int64_t>({split, G, 64}));
   split = cdiv(G, cdiv(G, split));  // no empty split
@@ -428,7 +459,7 @@ hq_status check_exec(const hq_plan* p, const hq::Exec& e) {
         return fail(HQ_ERR_INVALID_ARG, "no fp8 block tile of %d x %d with %d stages", e.tl.bm, 64 * e.tl.nbw, e.tl.stages);
       if (e.tl.gm < 1 || e.tl.gm > 64) return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_group must be 1..64");
       if (e.tiles_m * e.tiles_n > (int64_t(1) << 31) - 1) return fail(HQ_ERR_UNSUPPORTED, "too many tiles");
-    } else if (!hq::b8_skinny_ok({e.sk.mb, e.sk.nb, e.sk.waves, e.sk.split})) {
+    } else if (e.sk.mb != 1 || !hq::b8_skinny_ok({e.sk.nb, e.sk.waves, e.sk.split})) {
       return fail(HQ_ERR_INVALID_ARG, "no fp8 block skinny shape of %d x %d with %d waves", 16 * e.sk.mb, 16 * e.sk.nb,
                   e.sk.waves);
     }
@@ -549,8 +580,8 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
           return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers are gate_up with the fp8 requant, or down with the combine");
         if (compute->epi == HQ_EPI_SILU_MUL_QFP8 && layer->n % 256)
           return fail(HQ_ERR_UNSUPPORTED, "fp8 block gate_up needs n (gate + up) a multiple of 256");
-        if (tuning && (tuning->kernel == hq::KER_SKINNY || (tuning->tile_n && tuning->tile_n != 256)))
-          return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers run 256-column tiles");
+        if (tuning && (tuning->kernel == hq::KER_SKINNY || tuning->tile_m == 32 || (tuning->tile_n && tuning->tile_n != 256)))
+          return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers run 16-, 64- or 128-row blocks of 256 columns");
       }
       if ((compute->epi == HQ_EPI_SILU_MUL || compute->epi == HQ_EPI_SILU_MUL_QFP8) && layer->n % 32)
         return fail(HQ_ERR_UNSUPPORTED, "SiLU * mul needs n (gate + up) a multiple of 32");
@@ -831,7 +862,7 @@ hq_status dense_run(const hq_plan* p, const hq::Exec& e, int64_t m, const void* 
       b.group_m = (int)std::min<int64_t>(e.tl.gm, std::max<int64_t>(1, e.tiles_m));
       hq::arm_timing({ev.start, split > 1 ? nullptr : ev.stop});
       int err = tiled ? hq::launch_b8_dense({e.tl.bm, 64 * e.tl.nbw, split, e.tl.stages}, b, stream)
-                      : hq::launch_b8_skinny({e.sk.mb, e.sk.nb, e.sk.waves, split}, b, stream);
+                      : hq::launch_b8_skinny({e.sk.nb, e.sk.waves, split}, b, stream);
       if (err == hipSuccess && split > 1) {
         hq::arm_timing({nullptr, ev.stop});
         err = hq::launch_splitk_reduce(b.part, split, m * N, out, b.out_bf16, stream);
@@ -994,11 +1025,16 @@ static MoeChoice moe_choice(const hq_plan* p, int64_t t, int topk) {
   const double per_expert = (double)t * topk / p->layer.num_experts;
   if (p->fmt == hq::FMT_B8) {
     c.tiled = true;
-    c.bm = u.tile_m ? u.tile_m : (per_expert <= 12 ? 16 : (per_expert <= 24 ? 32 : (per_expert <= 64 ? 64 : 128)));
+    // blocks a little taller than what lands on an expert: a block is run with
+    // as many rows as it holds, but one more block reads the weights again
+    // (256 experts, top 8, H = 7168, I = 256, us a layer with 16 / 64 / 128-row
+    // blocks: 128 tokens 238 / 239 / 240, 509 370 / 318 / 345, 1024 560 / 393 /
+    // 415, 4096 1275 / 878 / 744)
+    c.bm = u.tile_m ? u.tile_m : (per_expert <= 6 ? 16 : (per_expert <= 64 ? 64 : 128));
     c.tl.bm = c.bm;
     c.tl.nbw = 4;
     c.tl.split = 1;
-    c.tl.stages = c.bm <= 32 ? 3 : 2;
+    c.tl.stages = c.bm <= 64 ? 3 : 2;
     return c;
   }
   bool tiled;
@@ -1119,7 +1155,7 @@ static int64_t moe_down_cols(const hq_plan* p, int64_t t, int topk, int bm) {
 
 // Columns of a down launch of fp8 block layers: windows whose slot rows fit the
 // last-level cache, so that the sum reads them from there.
-static constexpr int64_t kB8WindowBytes = int64_t(96) << 20;
+static constexpr int64_t kB8WindowBytes = int64_t(240) << 20;
 
 static int64_t b8_window(const hq_plan* p, int64_t t, int topk) {
   const int64_t N = p->layer.n, per = std::max<int64_t>(1, t * topk * 2);
@@ -1741,15 +1777,13 @@ std::vector<hq_tuning> tuning_candidates(const hq_plan* p, int64_t m) {
   if (p->fmt == hq::FMT_B8) {
     // shapes without a kernel are skipped by the caller (check_exec)
     if (m <= 128)
-      for (int tm : {16, 32, 64})
-        for (int tn : {16, 32})
-          for (int waves : {4, 8, 16})
-            for (int split : {1, 2, 4, 8}) c.push_back(hq_tuning{hq::KER_SKINNY, tm, tn, waves, split, 0, 0, 0});
-    for (int bm : {16, 32, 64, 128, 256}) {
+      for (int tn : {16, 32})
+        for (int waves : {4, 8})
+          for (int split : {1, 2, 4, 8}) c.push_back(hq_tuning{hq::KER_SKINNY, 16, tn, waves, split, 0, 0, 0});
+    for (int bm : {16, 32, 64, 128}) {
       if (bm > 16 && bm / 2 >= m) continue;  // no tile taller than the rows need
       for (int tn : {128, 256})
-        for (int stages : {2, 3, 4})
-          for (int split : {1, 2, 4, 8, 16}) c.push_back(hq_tuning{hq::KER_TILED, bm, tn, 0, split, stages, 0, 0});
+        for (int split : {1, 2, 4, 8, 16}) c.push_back(hq_tuning{hq::KER_TILED, bm, tn, 0, split, 0, 0, 0});
     }
     return c;
   }

@@ -51,22 +51,22 @@ struct B8Args {
 
 enum B8Mode : int { B8_DENSE = 0, B8_GATE_UP = 1, B8_DOWN = 2 };
 
-// A dense tile: bm rows (16 .. 256) by bn columns (128, 256), K over `split`
-// workgroups, groups in the load ring.
+// A dense tile: bm rows (16 .. 128) by bn columns (128, 256), K over `split`
+// workgroups, `stages` groups in the load ring.
 struct B8Tile {
   int bm, bn, split, stages;
 };
 bool b8_tile_ok(const B8Tile& t);
 int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream);
-// Grouped: aligned blocks of bm rows (16, 32, 64, 128) by 256 columns.
+// Grouped: aligned blocks of bm rows (16, 64, 128) by 256 columns.
 int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* stream);
 // y = the sum of a token's slot rows over the columns of a's window.
 int launch_b8_combine(const B8Args& a, int64_t t, void* stream);
 
-// Few rows: 16-column blocks, K over the waves of a workgroup and over `split`
-// workgroups.  rb: 16-row blocks per workgroup (1, 2, 4).
+// Few rows: 16 rows by 16 nb columns a workgroup, K over its waves and over
+// `split` workgroups.
 struct B8Skinny {
-  int rb, nb, waves, split;
+  int nb, waves, split;
 };
 bool b8_skinny_ok(const B8Skinny& c);
 int launch_b8_skinny(const B8Skinny& c, const B8Args& a, void* stream);

@@ -1,5 +1,5 @@
 // fp8 x fp8 GEMM with 128-block scales, few rows: bound by reading the weight
-// once.  A workgroup owns NB 16-column blocks and 16 RB rows; its waves take
+// once.  A workgroup owns NB 16-column blocks and 16 rows; its waves take
 // the 128-k groups of its K range in turn, weights straight from memory to
 // registers (no other wave needs them), ST groups of loads in flight per wave.
 // The waves' partial sums meet in LDS in wave order; with K split over
@@ -16,15 +16,15 @@ namespace hq {
 
 namespace {
 
-template <int RB, int NB, int ST, int MAXT>
-__global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
+template <int NB, int ST>
+__global__ void __launch_bounds__(512) b8_skinny(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  extern __shared__ __attribute__((aligned(16))) f4_t red[];  // [waves][RB * NB][64]
+  extern __shared__ __attribute__((aligned(16))) f4_t red[];  // [waves][NB][64]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int c16 = lane & 15, kq = lane >> 4;
   const int N = p.N, K = p.K, G = p.G;
-  const int m0 = blockIdx.z * 16 * RB;
+  const int m0 = blockIdx.z * 16;
   const int g0 = blockIdx.y * p.gps, g1 = min(G, g0 + p.gps);
   const int nblocks = N / 16;
   const int nb0 = blockIdx.x * NB;
@@ -38,13 +38,9 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
   const auto rw = rsrc(p.w, (int64_t)N * K);
   const auto rws = rsrc(p.w_scale, (int64_t)((N + 127) / 128) * G * 4);
   // rows past M load zeros without touching memory (offset past the range)
-  int aoff[RB], soff[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int m = m0 + 16 * b + c16;
-    aoff[b] = m < p.M ? m * K + kq * 16 : (int)0x80000000u;
-    soff[b] = m < p.M ? m * 4 : (int)0x80000000u;
-  }
+  const int am = m0 + c16;
+  const int aoff = am < p.M ? am * K + kq * 16 : (int)0x80000000u;
+  const int soff = am < p.M ? am * 4 : (int)0x80000000u;
   int woff[NB], swoff[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
@@ -53,8 +49,8 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
     swoff[j] = (nb / 8) * G * 4;
   }
 
-  u4_t wr[ST][NB][2], ar[ST][RB][2];
-  uint32_t sw[ST][NB], sa[ST][RB];
+  u4_t wr[ST][NB][2], ar[ST][2];
+  uint32_t sw[ST][NB], sa[ST];
   // Loads are issued without branches, so that the wait before each step's math
   // is for that step's loads alone; steps past the end take offsets past the
   // range, which read nothing.
@@ -67,20 +63,15 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
       for (int h = 0; h < 2; ++h)
         wr[slot][j][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (woff[j] + 1024 * h) | past, g * 2048, 0));
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        ar[slot][b][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (aoff[b] + 64 * h) | past, g * 128, 0));
-      sa[slot][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, soff[b] | past, g * p.a_rows * 4, 0);
-    }
+    for (int h = 0; h < 2; ++h)
+      ar[slot][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, (aoff + 64 * h) | past, g * 128, 0));
+    sa[slot] = __builtin_amdgcn_raw_buffer_load_b32(rs, soff | past, g * p.a_rows * 4, 0);
 #pragma unroll
     for (int j = 0; j < NB; ++j) sw[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(rws, swoff[j] | past, g * 4, 0);
   };
-  f4_t acc[RB][NB];
+  f4_t acc[NB];
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[b][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < NB; ++j) acc[j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll
   for (int s = 0; s < ST; ++s) {
@@ -92,32 +83,27 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
     for (int s = 0; s < ST; ++s) {
       // a step past the end holds zero codes and zero scales: it adds nothing
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+      for (int j = 0; j < NB; ++j) {
+        const f4_t P = b8_mfma(cat8(wr[s][j][0], wr[s][j][1]), cat8(ar[s][0], ar[s][1]));
+        const float f = __uint_as_float(sa[s]) * __uint_as_float(sw[s][j]);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const f4_t P = b8_mfma(cat8(wr[s][j][0], wr[s][j][1]), cat8(ar[s][b][0], ar[s][b][1]));
-          const float f = __uint_as_float(sa[s][b]) * __uint_as_float(sw[s][j]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[b][j][q] = fmaf(f, P[q], acc[b][j][q]);
-        }
+        for (int q = 0; q < 4; ++q) acc[j][q] = fmaf(f, P[q], acc[j][q]);
+      }
       issue(s, g + (s + ST) * waves);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) red[(wave * RB * NB + b * NB + j) * 64 + lane] = acc[b][j];
+  for (int j = 0; j < NB; ++j) red[(wave * NB + j) * 64 + lane] = acc[j];
   __syncthreads();
-  for (int e = tid; e < RB * NB * 64; e += blockDim.x) {
+  for (int e = tid; e < NB * 64; e += blockDim.x) {
     f4_t v = red[e];
     for (int w = 1; w < waves; ++w) {
-      const f4_t u = red[w * RB * NB * 64 + e];
+      const f4_t u = red[w * NB * 64 + e];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += u[q];
     }
-    const int l = e & 63, bj = e >> 6, b = bj / NB, j = bj - b * NB;
-    const int m = m0 + 16 * b + (l & 15), nb = nb0 + j;
+    const int l = e & 63, m = m0 + (l & 15), nb = nb0 + (e >> 6);
     if (m >= p.M || nb >= nblocks) continue;
     const int n = nb * 16 + 4 * (l >> 4);
     if (p.part) {
@@ -131,32 +117,23 @@ __global__ void __launch_bounds__(MAXT) b8_skinny(B8Args p) {
 #endif
 }
 
-template <int RB, int NB, int ST, int MAXT>
+template <int NB, int ST>
 hipError_t launch_t(const B8Skinny& c, const B8Args& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N / 16 + NB - 1) / NB), (unsigned)c.split, (unsigned)((a.M + 16 * RB - 1) / (16 * RB)));
-  return launch_timed(b8_skinny<RB, NB, ST, MAXT>, grid, dim3(64 * c.waves), (size_t)c.waves * RB * NB * 1024, s, a);
+  const dim3 grid((unsigned)((a.N / 16 + NB - 1) / NB), (unsigned)c.split, (unsigned)((a.M + 15) / 16));
+  return launch_timed(b8_skinny<NB, ST>, grid, dim3(64 * c.waves), (size_t)c.waves * NB * 1024, s, a);
 }
 
 }  // namespace
 
 bool b8_skinny_ok(const B8Skinny& c) {
-  if (c.rb != 1 && c.rb != 2 && c.rb != 4) return false;
-  if (c.nb != 1 && c.nb != 2) return false;
-  if (c.waves < 1 || c.waves > 16 || c.split < 1 || c.split > 64) return false;
-  return c.waves <= 8 || c.rb == 1;
+  return (c.nb == 1 || c.nb == 2) && c.waves >= 1 && c.waves <= 8 && c.split >= 1 && c.split <= 64;
 }
 
 int launch_b8_skinny(const B8Skinny& c, const B8Args& a, void* stream) {
-  if (!b8_skinny_ok(c) || a.G < 1 || a.gps < 1) return (int)hipErrorInvalidValue;
+  if (!b8_skinny_ok(c) || a.G < 1 || a.gps < 1 || a.M > 16 * 65535) return (int)hipErrorInvalidValue;
   if ((int64_t)(c.split - 1) * a.gps >= a.G || (int64_t)c.split * a.gps < a.G) return (int)hipErrorInvalidValue;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (c.waves > 8) {
-    if (c.nb == 1) return (int)launch_t<1, 1, 4, 1024>(c, a, s);
-    return (int)launch_t<1, 2, 2, 1024>(c, a, s);
-  }
-  if (c.rb == 1) return c.nb == 1 ? (int)launch_t<1, 1, 8, 512>(c, a, s) : (int)launch_t<1, 2, 4, 512>(c, a, s);
-  if (c.rb == 2) return c.nb == 1 ? (int)launch_t<2, 1, 4, 512>(c, a, s) : (int)launch_t<2, 2, 4, 512>(c, a, s);
-  return c.nb == 1 ? (int)launch_t<4, 1, 3, 512>(c, a, s) : (int)launch_t<4, 2, 2, 512>(c, a, s);
+  return c.nb == 1 ? (int)launch_t<1, 8>(c, a, s) : (int)launch_t<2, 4>(c, a, s);
 }
 
 }  // namespace hq

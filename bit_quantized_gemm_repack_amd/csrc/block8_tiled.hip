@@ -161,13 +161,14 @@ __device__ inline int b8_block_rows(const B8Args& p, int m0, int bm, int lane) {
   return n;
 }
 
-// A workgroup of WM x 4 waves computes BM = 16 MB WM rows by BN = 64 NB
-// columns: wave (wm, wn) owns rows [16 MB wm, + 16 MB) and 16 NB columns.
-template <int MB, int NB, int WM, int ST>
+// A workgroup of 4 waves computes BM = 16 MB rows by BN = 64 NB columns, each
+// wave all the rows and 16 NB columns, so that every weight is read once a
+// tile, straight to registers.
+template <int MB, int NB, int ST>
 struct B8Cfg {
-  static constexpr int WAVES = 4 * WM;
+  static constexpr int WAVES = 4;
   static constexpr int THREADS = 64 * WAVES;
-  static constexpr int BM = 16 * MB * WM;
+  static constexpr int BM = 16 * MB;
   static constexpr int BN = 64 * NB;
   static constexpr int NSEG = BM / 8;  // 1 KiB loads of the activation tile per step
   static constexpr int SEGW = NSEG > WAVES ? NSEG / WAVES : 1;
@@ -179,13 +180,13 @@ struct B8Cfg {
 };
 
 // One tile: rows m0 .. m0 + C::BM - 1, column tile tn.
-template <int MB, int NB, int WM, int ST, int MODE>
+template <int MB, int NB, int ST, int MODE>
 __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using C = B8Cfg<MB, NB, WM, ST>;
+  using C = B8Cfg<MB, NB, ST>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c16 = lane & 15, kq = lane >> 4;
-  const int wn = wave & 3, wm = wave >> 2;
+  const int wn = wave;
   const int N = p.N, K = p.K, G = p.G;
 
   const int split = MODE == B8_DENSE ? (int)blockIdx.y : 0;
@@ -281,8 +282,8 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     float sw[NSW];
 #pragma unroll
     for (int u = 0; u < NSW; ++u) sw[u] = __uint_as_float(sraw[slot][u]);
-    b8_step<MB, NB, NSW>(lds + slot * C::STAGE + wm * (16 * MB) * 128 + c16 * 128,
-                         reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + wm * 16 * MB + c16, c16, kq,
+    b8_step<MB, NB, NSW>(lds + slot * C::STAGE + c16 * 128,
+                         reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + c16, c16, kq,
                          braw[slot], sw, acc);
   };
 
@@ -315,7 +316,6 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
 
   // ---- epilogue: lane (c16, kq) holds token c16 of each row block, columns
   // 4 kq .. 4 kq + 3 of each column block --------------------------------------
-  const int mw = m0 + 16 * MB * wm;
   if constexpr (MODE == B8_GATE_UP) {
     // one tile row holds the 128 outputs of one scale block: SiLU(gate) * up,
     // its largest magnitude over the four column waves, the codes
@@ -334,12 +334,12 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
         }
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      if (kq == 0) red[wn * C::BM + 16 * MB * wm + 16 * mb + c16] = top;
+      if (kq == 0) red[wn * C::BM + 16 * mb + c16] = top;
     }
     __syncthreads();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const int rl = 16 * MB * wm + 16 * mb + c16;
+      const int rl = 16 * mb + c16;
       const float s = b8_scale(max(max(red[rl], red[C::BM + rl]), max(red[2 * C::BM + rl], red[3 * C::BM + rl])));
       if (p.sorted_ids[m0 + rl] >= p.n_slots) continue;
       const int64_t row = m0 + rl;
@@ -360,11 +360,11 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     b8_load_slots(p, m0, C::BM, lid, ltw, tid, C::THREADS);
     __syncthreads();
     uint8_t* buf = lds + C::BM * 8 + wave * b8_rows_lds(4);
-    if (col < p.col0 + p.ncol) b8_store_rows<MB>(p, lid + (mw - m0), ltw + (mw - m0), buf, col, lane, acc);
+    if (col < p.col0 + p.ncol) b8_store_rows<MB>(p, lid, ltw, buf, col, lane, acc);
   } else if (p.part) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const int m = mw + 16 * mb + c16;
+      const int m = m0 + 16 * mb + c16;
       if (m >= p.M) continue;
 #pragma unroll
       for (int j = 0; j < NB; ++j)
@@ -377,7 +377,7 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     const int col = nblk(0) * 16, cols = min(16 * NB, N - col);
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const int m = mw + 16 * mb + c16;
+      const int m = m0 + 16 * mb + c16;
       char* o = reinterpret_cast<char*>(static_cast<uint16_t*>(p.out) + (int64_t)m * N + col);
       b8_rows16<NB>(
           buf, lane,
@@ -394,8 +394,8 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
 #endif
 }
 
-template <int MB, int NB, int WM, int ST>
-__global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2))) b8_dense(B8Args p) {
+template <int MB, int NB, int ST>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_dense(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // ids dealt round-robin to the 8 XCDs get consecutive logical tiles on
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2
   const int grp = lid / per, first = grp * p.group_m;
   const int gsz = min(p.tiles_m - first, p.group_m);
   const int r = lid - grp * per;
-  b8_tile<MB, NB, WM, ST, B8_DENSE>(p, lds, (first + r % gsz) * B8Cfg<MB, NB, WM, ST>::BM, 0, r / gsz);
+  b8_tile<MB, NB, ST, B8_DENSE>(p, lds, (first + r % gsz) * B8Cfg<MB, NB, ST>::BM, 0, r / gsz);
 #endif
 }
 
@@ -422,7 +422,7 @@ __device__ __forceinline__ void b8_grouped_tile(const B8Args& p, uint8_t* lds, i
       return;
     }
   }
-  b8_tile<MB, 4, 1, (MB <= 4 ? 3 : 2), MODE>(p, lds, m0, ex, tn);
+  b8_tile<MB, 4, (MB <= 4 ? 3 : 2), MODE>(p, lds, m0, ex, tn);
 }
 
 template <int MB, int MODE>
@@ -581,29 +581,22 @@ __global__ void __launch_bounds__(256) b8_combine_kernel(const uint4* __restrict
   }
 }
 
-template <int MB, int NB, int WM, int ST>
+template <int MB, int NB, int ST>
 hipError_t launch_dense(const B8Args& a, dim3 grid, hipStream_t s) {
-  using C = B8Cfg<MB, NB, WM, ST>;
-  const hipError_t e = allow_lds<b8_dense<MB, NB, WM, ST>>(C::LDS);
+  using C = B8Cfg<MB, NB, ST>;
+  const hipError_t e = allow_lds<b8_dense<MB, NB, ST>>(C::LDS);
   if (e != hipSuccess) return e;
-  return launch_timed(b8_dense<MB, NB, WM, ST>, grid, dim3(C::THREADS), (size_t)C::LDS, s, a);
+  return launch_timed(b8_dense<MB, NB, ST>, grid, dim3(C::THREADS), (size_t)C::LDS, s, a);
 }
 
 hipError_t dispatch_dense(const B8Tile& t, const B8Args& a, dim3 grid, hipStream_t s) {
-#define HQ_B8(bm_, bn_, st_, MB, NB, WM) \
-  if (t.bm == bm_ && t.bn == bn_ && t.stages == st_) return launch_dense<MB, NB, WM, st_>(a, grid, s);
-  HQ_B8(16, 256, 3, 1, 4, 1)
-  HQ_B8(32, 256, 3, 2, 4, 1)
-  HQ_B8(64, 256, 2, 4, 4, 1)
-  HQ_B8(64, 256, 3, 4, 4, 1)
-  HQ_B8(128, 256, 2, 8, 4, 1)
-  HQ_B8(256, 256, 2, 8, 4, 2)
-  HQ_B8(128, 128, 2, 8, 2, 1)
-  HQ_B8(128, 128, 3, 8, 2, 1)
-  HQ_B8(64, 128, 3, 4, 2, 1)
-  HQ_B8(64, 128, 4, 4, 2, 1)
-  HQ_B8(32, 128, 4, 2, 2, 1)
-  HQ_B8(16, 128, 4, 1, 2, 1)
+#define HQ_B8(bm_, bn_, st_, MB, NB) \
+  if (t.bm == bm_ && t.bn == bn_ && t.stages == st_) return launch_dense<MB, NB, st_>(a, grid, s);
+  HQ_B8(128, 256, 2, 8, 4)
+  HQ_B8(128, 128, 2, 8, 2)
+  HQ_B8(64, 128, 3, 4, 2)
+  HQ_B8(32, 128, 4, 2, 2)
+  HQ_B8(16, 128, 4, 1, 2)
 #undef HQ_B8
   return hipErrorInvalidValue;
 }
@@ -611,9 +604,7 @@ hipError_t dispatch_dense(const B8Tile& t, const B8Args& a, dim3 grid, hipStream
 template <int MB>
 hipError_t launch_grouped(int mode, const B8Args& a, dim3 grid, hipStream_t s) {
   // the largest ring of the row counts a block may run with
-  constexpr size_t lds = std::max<size_t>({(size_t)B8Cfg<1, 4, 1, 3>::LDS, (size_t)B8Cfg<(MB >= 2 ? 2 : 1), 4, 1, 3>::LDS,
-                                           (size_t)B8Cfg<(MB >= 4 ? 4 : 1), 4, 1, 3>::LDS,
-                                           (size_t)B8Cfg<MB, 4, 1, (MB <= 4 ? 3 : 2)>::LDS});
+  constexpr size_t lds = std::max<size_t>(B8Cfg<MB, 4, (MB <= 4 ? 3 : 2)>::LDS, B8Cfg<(MB < 4 ? MB : 4), 4, 3>::LDS);
   if (mode == B8_GATE_UP) {
     const hipError_t e = allow_lds<b8_grouped<MB, B8_GATE_UP>>(lds);
     return e != hipSuccess ? e : launch_timed(b8_grouped<MB, B8_GATE_UP>, grid, dim3(256), lds, s, a);
@@ -633,14 +624,10 @@ hipError_t launch_short(const B8Args& a, dim3 grid, hipStream_t s) {
 }  // namespace
 
 bool b8_tile_ok(const B8Tile& t) {
-  if (t.bn == 256) {
-    if (t.bm == 16 || t.bm == 32) return t.stages == 3;
-    if (t.bm == 64) return t.stages == 2 || t.stages == 3;
-    return (t.bm == 128 || t.bm == 256) && t.stages == 2;
-  }
+  if (t.bn == 256) return t.bm == 128 && t.stages == 2;
   if (t.bn != 128) return false;
-  if (t.bm == 128) return t.stages == 2 || t.stages == 3;
-  if (t.bm == 64) return t.stages == 3 || t.stages == 4;
+  if (t.bm == 128) return t.stages == 2;
+  if (t.bm == 64) return t.stages == 3;
   return (t.bm == 16 || t.bm == 32) && t.stages == 4;
 }
 
@@ -671,7 +658,6 @@ int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* s
   const dim3 grid((unsigned)(blocks * b.tiles_n));
   switch (bm) {
     case 16: return whole ? (int)launch_short<1>(b, grid, s) : (int)launch_grouped<1>(mode, b, grid, s);
-    case 32: return whole ? (int)launch_short<2>(b, grid, s) : (int)launch_grouped<2>(mode, b, grid, s);
     case 64: return whole ? (int)launch_short<4>(b, grid, s) : (int)launch_grouped<4>(mode, b, grid, s);
     case 128: return whole ? (int)launch_short<8>(b, grid, s) : (int)launch_grouped<8>(mode, b, grid, s);
   }

@@ -317,7 +317,7 @@ HQ_HD inline int64_t e4m3_src_index(int64_t K, int64_t eidx) {
 enum KernelKind : int { KER_SKINNY = 1, KER_TILED = 2 };
 
 struct TiledCfgRt {
-  int bm;     // rows per workgroup tile (64, 128; FMT_B8: 16 .. 256)
+  int bm;     // rows per workgroup tile (64, 128; FMT_B8: 16 .. 128)
   int nbw;    // 16-column blocks per wave (2, 4); tile width = 64 * nbw
   int split;   // K split over workgroups (dense; partials + reduce kernel)
   int stages;  // groups in the load pipeline (3; dense also 4, 5)
