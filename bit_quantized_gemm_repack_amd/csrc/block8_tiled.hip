@@ -92,9 +92,10 @@ __device__ __forceinline__ void b8_rows16(uint8_t* buf, int lane, V&& value, S&&
 
 // A slot's weighted row of the down GEMM, 64 columns a wave: the fp32 sums o
 // as 16-bit integers q = o / 2^e with the one 2^e that brings the largest to
-// 15 bits, and topk_w * 2^e as their scale.  Half the bytes of fp32 rows at an
-// error of 2^-16 of the 64 columns' largest (bf16 rows: 2^-9 of each).  A
-// value that is not finite makes the scale NaN, and so the 64 columns.
+// 15 bits, and topk_w * 2^e as their scale.  Half the bytes of fp32 rows, each
+// off by at most half a unit (one at the very top), 2^-15 of the 64 columns'
+// largest; bf16 rows are off by 2^-9 of each value.  A value that is not finite
+// makes the scale NaN, and so the 64 columns.
 template <int MB>
 __device__ __forceinline__ void b8_store_rows(const B8Args& p, const int32_t* ids, const float* tw, uint8_t* buf, int col,
                                               int lane, const f4_t (&acc)[MB][4]) {

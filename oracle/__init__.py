@@ -38,9 +38,12 @@ moe      the grouped MoE layer: align invariants, gate_up + SiLU*mul (+ fp8
 quant    the per-token (per-row) activation quantiser that feeds W4A8:
          s = max|x| / Q, codes = RNE(x / s) as fp8 e4m3 or int8; and the
          MXFP4 block quantiser (OCP MX v1.0) of W4A4 activations.
+block8   fp8 with 128-block scales: the block quantiser, the GEMM, top-k
+         routing and the experts' layer (torch float64).
 
 Parity status: every function is pinned by tests/test_oracle.py,
-tests/test_quant_oracle.py and tests/test_moe_oracle.py against
+tests/test_quant_oracle.py, tests/test_moe_oracle.py and
+tests/test_block8_oracle.py against
 hand-worked examples (tests/golden), code tables derived from the format
 definitions, torch's fp8 decoders, exact rational brute force and
 invariants.  No function is "parity unpinned".
