@@ -180,6 +180,28 @@ struct B8Cfg {
   static constexpr int LDS = ST * STAGE > EPI ? ST * STAGE : EPI;
 };
 
+// Workgroup ids are dealt round-robin to the 8 XCDs, each with an L2 of its own:
+// the id'th of n workgroups takes this logical tile, so that every XCD runs a
+// consecutive run of them.
+__device__ __forceinline__ int b8_xcd_order(int id, int n) {
+  const int xcd = id & 7, each = n >> 3, over = n & 7;
+  return xcd * each + min(xcd, over) + (id >> 3);
+}
+
+// The tile of a grouped launch (row block tm, column tile tn), or false past the
+// padded rows.  The column tiles of a row block and the row blocks of an expert
+// follow each other on one XCD, so that its L2 fetches the rows and the expert's
+// weights once where they keep pace (4096 tokens, 256 experts, top 8, H = 7168,
+// I = 256: gate_up 303 us against 325 with ids in order).
+__device__ __forceinline__ bool b8_grouped_place(const B8Args& p, int bm, int& tm, int& tn) {
+  const int n = *p.num_padded / bm * p.tiles_n;
+  if ((int)blockIdx.x >= n) return false;
+  const int lid = b8_xcd_order(blockIdx.x, n);
+  tm = lid / p.tiles_n;
+  tn = lid - tm * p.tiles_n;
+  return true;
+}
+
 // One tile: rows m0 .. m0 + C::BM - 1, column tile tn.
 template <int MB, int NB, int ST, int MODE>
 __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
@@ -399,11 +421,8 @@ template <int MB, int NB, int ST>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_dense(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  // ids dealt round-robin to the 8 XCDs get consecutive logical tiles on
-  // each; logical tiles run in groups of group_m row tiles, column by column
-  const int nwg = gridDim.x;
-  int lid = blockIdx.x;
-  if ((nwg & 7) == 0) lid = (blockIdx.x & 7) * (nwg >> 3) + (blockIdx.x >> 3);
+  // logical tiles run in groups of group_m row tiles, column by column
+  const int lid = b8_xcd_order(blockIdx.x, gridDim.x);
   const int per = p.group_m * p.tiles_n;
   const int grp = lid / per, first = grp * p.group_m;
   const int gsz = min(p.tiles_m - first, p.group_m);
@@ -430,9 +449,9 @@ template <int MB, int MODE>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_grouped(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
+  int tm, tn;
+  if (!b8_grouped_place(p, 16 * MB, tm, tn)) return;
   const int m0 = tm * 16 * MB;
-  if (m0 >= *p.num_padded) return;
   const int64_t ex = p.block_expert[tm];
   if (ex < 0) {
     if constexpr (MODE == B8_DOWN)
@@ -543,9 +562,9 @@ template <int MB>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_down_short(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
+  int tm, tn;
+  if (!b8_grouped_place(p, 16 * MB, tm, tn)) return;
   const int m0 = tm * 16 * MB;
-  if (m0 >= *p.num_padded) return;
   const int64_t ex = p.block_expert[tm];
   const int c0 = p.col0 + tn * p.cols_wg, c1 = min(c0 + p.cols_wg, p.col0 + p.ncol);
   if (ex < 0) {
