@@ -370,6 +370,7 @@ class Plan:
         self._h = handle
         self._block8 = self.quant.act_scale == ASCALE_BLOCK_F32
         self._ws_need = {}  # rows -> workspace bytes of a block-scaled GEMM
+        self._few_need = {}  # (tokens, topk, down's k) -> workspace bytes of a layer of a few tokens
         self._ws = {}
         self._act_buf = {}
 
@@ -943,7 +944,12 @@ def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2
         raise ValueError(f"x must be fp16 / bf16 [t, {gate_up.k}]")
     if ids.shape != (t, topk) or ids.dtype != torch.int32 or w.shape != (t, topk) or w.dtype != torch.float32:
         raise ValueError(f"topk_ids / topk_w must be int32 / float32 [{t}, {topk}]")
-    ws = torch.empty(t * topk * down.k, dtype=torch.float32, device=x.device)
+    need = gate_up._few_need.get((t, topk, down.k))
+    if need is None:
+        n = ctypes.c_size_t()
+        _check(lib().hq_moe_few_workspace_bytes(gate_up._h, down._h, t, topk, ctypes.byref(n)))
+        need = gate_up._few_need[t, topk, down.k] = n.value
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     out = torch.empty((t, down.n), dtype=_TORCH_OUT[down.quant.out], device=x.device)
     gate_up._check_block_layout(w1, m1), down._check_block_layout(w2, m2)
     with _on(x.device):
@@ -951,7 +957,7 @@ def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2
                                       x.data_ptr(), F32 if logits is None else _LOGITS[logits.dtype], _ptr(logits),
                                       1 if renormalize else 0, ids.data_ptr(), w.data_ptr(), w1.data_ptr(),
                                       m1.data_ptr(), w2.data_ptr(), m2.data_ptr(), out.data_ptr(), ws.data_ptr(),
-                                      ws.numel() * 4, _stream_ptr(x.device)))
+                                      need, _stream_ptr(x.device)))
     return out
 
 

@@ -1607,11 +1607,16 @@ static hq_status few_check(const hq_plan* gu, const hq_plan* dn, int64_t t, int 
   return HQ_OK;
 }
 
+// The intermediate's rows (fp32, or codes and scales), then each tile's units.
+static size_t few_workspace(int64_t t, int topk, const hq_plan* down) {
+  return align256((size_t)t * (size_t)topk * (size_t)down->layer.k * 4) + (size_t)((t + 15) / 16) * hq::kB8FewUnitInts * 4;
+}
+
 hq_status hq_moe_few_workspace_bytes(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, size_t* bytes) {
   if (!bytes) return fail(HQ_ERR_INVALID_ARG, "null argument");
   hq_status s = few_check(gate_up, down, t, topk);
   if (s != HQ_OK) return s;
-  *bytes = align256((size_t)t * (size_t)topk * (size_t)down->layer.k * 4);
+  *bytes = few_workspace(t, topk, down);
   return ok();
 }
 
@@ -1635,7 +1640,7 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
   for (const void* p : {x, (const void*)logits, (const void*)topk_ids, (const void*)topk_w, w1, meta1, w2, meta2, (const void*)out})
     if (!aligned16(p)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
   const int64_t H = gate_up->layer.k, I = down->layer.k;
-  const size_t need = (size_t)t * (size_t)topk * (size_t)I * 4;
+  const size_t need = few_workspace(t, topk, down);
   if (!ws || ws_bytes < need) return fail(HQ_ERR_WORKSPACE, "this call needs %zu workspace bytes", need);
   if (!aligned16(ws)) return fail(HQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   hq::B8FewArgs a{};
@@ -1662,12 +1667,19 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
   a.out_bf16 = down->layer.q.out == HQ_BF16;
   a.logit_type = lt;
   a.renorm = renormalize;
+  a.units = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + align256((size_t)t * (size_t)topk * (size_t)I * 4));
   if (t > 8) {  // the wide gate_up writes codes, and scales behind them
     a.act_codes = static_cast<uint8_t*>(ws);
     a.act = reinterpret_cast<float*>(a.act_codes + t * topk * I);
   }
   hq::arm_timing({ev.start, nullptr});
-  int err = hq::launch_few_gate_up(a, stream);
+  int err = hipSuccess;
+  if (logits && t > 1) {
+    err = hq::launch_route(t, E, topk, lt, logits, renormalize, topk_ids, topk_w, stream);
+    a.logits = nullptr;
+    hq::arm_timing({nullptr, nullptr});
+  }
+  if (err == hipSuccess) err = hq::launch_few_gate_up(a, stream);
   if (err == hipSuccess) {
     hq::arm_timing({nullptr, ev.stop});
     err = hq::launch_few_down(a, stream);

@@ -88,6 +88,10 @@ int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits,
 constexpr int kB8FewMaxTokens = 64;
 constexpr int kB8FewMaxTopk = 16;
 constexpr int kB8FewMaxSlots = kB8FewMaxTokens * kB8FewMaxTopk;
+// A tile's units: how many, their experts from int 16 on, then per unit the slot
+// of each of the 16 tokens as 16-bit integers, -1 for none.
+constexpr int kB8FewUnitInts = 16 + 16 * kB8FewMaxTopk * 9;
+
 struct B8FewArgs {
   const void* x;        // [t][H]
   const void* logits;   // [t][E], or null: topk_ids and topk_w are given
@@ -100,6 +104,7 @@ struct B8FewArgs {
   float* act;           // fp32 rows [t * topk][I], or with act_codes their scales [t * topk][I/128]
   uint8_t* act_codes;   // [t * topk][I], or null
   void* out;            // [t][H]
+  int32_t* units;       // per tile of 16 tokens kB8FewUnitInts, for t > 1 (see few_units)
   int64_t w1_expert, s1_expert, w2_expert, s2_expert;
   int t, topk, E, H, I;
   int x_bf16, out_bf16, logit_type, renorm;

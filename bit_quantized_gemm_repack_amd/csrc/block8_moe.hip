@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block8.h"
 #include "block8_device.h"
@@ -44,11 +45,8 @@ __device__ inline float load_logit(const void* p, int64_t i) {
   const uint32_t b = static_cast<const uint16_t*>(p)[i];
   return LT == 1 ? bf16_bits_to_float(b) : f16_bits_to_float(b);
 }
-__device__ inline float load_logit_rt(const void* p, int64_t i, int lt) {
-  return lt == 0 ? load_logit<0>(p, i) : (lt == 1 ? load_logit<1>(p, i) : load_logit<2>(p, i));
-}
 
-// Wave-wide maximum, minimum and sum, uniform.
+// Wave-wide maximum and sum, uniform.
 __device__ inline uint32_t wave_max(uint32_t v) {
   v = b8_row_max(v);
   const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
@@ -61,46 +59,55 @@ __device__ inline float wave_sum(float v) {
   return v;
 }
 
-// The row of logits a wave holds: lane l keeps experts l, l + 64, ...
+// The row of logits a wave holds: lane l keeps experts l, l + 64, ... and the
+// largest of their keys.
 template <int NPL>
 struct Logits {
-  uint32_t key[NPL];
-  __device__ inline void load(const void* p, int64_t row, int E, int lt, int lane) {
+  uint32_t key[NPL], head;
+  template <int LT>
+  __device__ inline void load_as(const void* p, int64_t row, int E, int lane) {
+    float v[NPL];  // all in flight at once: a type looked up per load would wait for each in turn
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 64 * i;
-      key[i] = e < E ? logit_key(load_logit_rt(p, row * E + e, lt)) : 0u;
-    }
+    for (int i = 0; i < NPL; ++i) v[i] = load_logit<LT>(p, row * E + min(lane + 64 * i, E - 1));
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) key[i] = lane + 64 * i < E ? logit_key(v[i]) : 0u;
+  }
+  __device__ inline void load(const void* p, int64_t row, int E, int lt, int lane) {
+    if (lt == 0)
+      load_as<0>(p, row, E, lane);
+    else if (lt == 1)
+      load_as<1>(p, row, E, lane);
+    else
+      load_as<2>(p, row, E, lane);
+    refresh();
+  }
+  __device__ inline void refresh() {
+    head = key[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) head = max(head, key[i]);
   }
   // The best expert left (largest key, then lowest index), struck out; -1 if
   // none is left.  Uniform.
   __device__ inline int take(int lane, uint32_t* best) {
-    uint32_t m = key[0];
-#pragma unroll
-    for (int i = 1; i < NPL; ++i) m = max(m, key[i]);
-    m = wave_max(m);
+    const uint32_t m = wave_max(head);
     *best = m;
     if (m == 0u) return -1;
+    int mine = NPL - 1;  // the lowest of this lane's that has the key
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const uint64_t has = __ballot(key[i] == m);
-      if (has) {
-        const int l = __builtin_ctzll(has);
-        if (lane == l) key[i] = 0u;
-        return 64 * i + l;
-      }
-    }
-    return -1;
-  }
-  // How many experts come before expert e with key k.  Uniform.
-  __device__ inline int before(int lane, int e, uint32_t k) const {
-    int n = 0;
+    for (int i = NPL - 2; i >= 0; --i) mine = key[i] == m ? i : mine;
+    const uint64_t has = __ballot(head == m);
+    int l = __builtin_ctzll(has);
+    if (NPL > 1 && (has & (has - 1))) {  // in several lanes
+      uint64_t b = 0;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int o = lane + 64 * i;
-      n += __popcll(__ballot(key[i] > k || (key[i] == k && o < e)));
+      for (int i = 0; i < NPL; ++i)
+        if (!b) b = __ballot(key[i] == m);
+      l = __builtin_ctzll(b);
     }
-    return n;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) key[i] = lane == l && mine == i ? 0u : key[i];
+    refresh();
+    return 64 * __builtin_amdgcn_readlane(mine, l) + l;
   }
   __device__ inline float exp_sum(float top) const {
     float s = 0.f;
@@ -119,13 +126,7 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
   if (row >= t) return;
   Logits<NPL> x;
   x.load(logits, row, E, lt, lane);
-  const uint32_t k0 = [&] {
-    uint32_t m = x.key[0];
-#pragma unroll
-    for (int i = 1; i < NPL; ++i) m = max(m, x.key[i]);
-    return wave_max(m);
-  }();
-  const float top = key_logit(k0);
+  const float top = key_logit(wave_max(x.head));
   float sum = renorm ? 0.f : x.exp_sum(top);
   // lane j keeps choice j (topk <= 64)
   int my_id = -1;
@@ -147,6 +148,113 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
   }
 }
 
+__device__ inline uint32_t row_min(uint32_t v) { return ~b8_row_max(~v); }
+__device__ inline float row_sum(float v) {
+  auto ror = [&](auto c) {
+    constexpr int ctrl = decltype(c)::value;
+    v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, 0xF, 0xF, false));
+  };
+  ror(std::integral_constant<int, 0x128>{});
+  ror(std::integral_constant<int, 0x124>{});
+  ror(std::integral_constant<int, 0x122>{});
+  ror(std::integral_constant<int, 0x121>{});
+  return v;
+}
+
+// Sixteen lanes per token, for many tokens: a choice costs the wave one maximum
+// over 16 lanes for four tokens.  Lane l keeps experts l, l + 16, ...  16-bit
+// logits carry their expert in the key's low half (the lower the larger), which
+// makes the keys unique and a choice one comparison per key.
+template <int LT, int NPL>
+__global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict__ logits, int t, int E, int topk, int renorm,
+                                                         int32_t* __restrict__ ids, float* __restrict__ w) {
+  const int row = blockIdx.x * 16 + (threadIdx.x >> 4), lane = threadIdx.x & 15;
+  const int r = min(row, t - 1);
+  // 16-bit logits as float keys have their value in the high half (bf16) or
+  // are kept as the order of their own bits (fp16)
+  auto key16 = [](uint32_t b) -> uint32_t {  // 0 for -inf and NaN
+    constexpr uint32_t inf = LT == 1 ? 0x7F80u : 0x7C00u;
+    const uint32_t mag = b & 0x7FFFu;
+    if (mag > inf || b == (0x8000u | inf)) return 0u;
+    if (mag == 0u) b = 0u;  // -0 and 0 are equal
+    return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
+  };
+  auto value = [](uint32_t k) -> float {
+    if constexpr (LT == 0) return key_logit(k);
+    if ((k >> 16) == 0u) return -__builtin_inff();
+    const uint32_t h = k >> 16, b = (h & 0x8000u) ? (h & 0x7FFFu) : (~h & 0xFFFFu);
+    return LT == 1 ? bf16_bits_to_float(b) : f16_bits_to_float(b);
+  };
+  uint32_t key[NPL];
+  {
+    uint32_t raw[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int64_t at = (int64_t)r * E + min(lane + 16 * i, E - 1);
+      raw[i] = LT == 0 ? static_cast<const uint32_t*>(logits)[at] : static_cast<const uint16_t*>(logits)[at];
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = lane + 16 * i;
+      if constexpr (LT == 0)
+        key[i] = e < E ? logit_key(__uint_as_float(raw[i])) : 0u;
+      else {
+        const uint32_t k = key16(raw[i]);
+        key[i] = e < E && k ? (k << 16) | (0xFFFFu - e) : 0u;
+      }
+    }
+  }
+  auto largest = [&] {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) m = max(m, key[i]);
+    return m;
+  };
+  // (weights below 2^-126 are zero)
+  auto exp_of = [](float d) { return __builtin_amdgcn_exp2f(d * 1.44269504f); };
+  uint32_t head = largest();
+  uint32_t best = b8_row_max(head);
+  const float top = value(best);
+  float sum = 0.f;
+  if (!renorm) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (key[i]) sum += exp_of(value(key[i]) - top);
+    sum = row_sum(sum);
+  }
+  int my_id = -1;
+  float my_e = 0.f;
+  for (int j = 0; j < topk; ++j) {
+    const uint32_t m = best;  // zero once a token's row is used up
+    int e;
+    if constexpr (LT == 0) {
+      int mine = NPL - 1;  // the lowest of this lane's that has the key
+#pragma unroll
+      for (int i = NPL - 2; i >= 0; --i) mine = key[i] == m ? i : mine;
+      e = (int)row_min(head == m ? (uint32_t)(16 * mine + lane) : 0xFFFFu);
+      const int strike = (e & 15) == lane ? e >> 4 : -1;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) key[i] = i == strike ? 0u : key[i];
+    } else {
+      e = (int)(0xFFFFu - (m & 0xFFFFu));
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) key[i] = key[i] == m ? 0u : key[i];
+    }
+    const float v = m ? exp_of(value(m) - top) : 0.f;
+    if (renorm) sum += v;
+    if (lane == j && m) {
+      my_id = e;
+      my_e = v;
+    }
+    head = largest();
+    best = b8_row_max(head);
+  }
+  if (lane < topk && row < t) {
+    ids[(int64_t)row * topk + lane] = my_id;
+    w[(int64_t)row * topk + lane] = my_id < 0 ? 0.f : my_e / sum;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // gate_up.  A workgroup row per slot; the first of the slots that share an
 // expert does the work for all of them.  Two shapes:
@@ -157,7 +265,8 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
 //           and the workgroup holds a whole scale block, so that it writes
 //           codes and scales.  The routing above the stream is paid an eighth
 //           as often.
-// With logits one more block column writes the routing.
+// One more row of workgroups writes the routing where there are logits, and
+// otherwise the units that the down kernel walks.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;  // of a down workgroup
 constexpr int kFewLds = 128 * 1024;  // most dynamic LDS of a workgroup
@@ -165,13 +274,9 @@ constexpr int kFewLds = 128 * 1024;  // most dynamic LDS of a workgroup
 // The routing of slot z, for the down kernel and the caller (one wave).
 template <int NPL>
 __device__ inline void few_write_routing(const B8FewArgs& p, int z, int lane) {
-  const int tok = z / p.topk;
   Logits<NPL> r;
-  r.load(p.logits, tok, p.E, p.logit_type, lane);
-  uint32_t k0 = r.key[0];
-#pragma unroll
-  for (int i = 1; i < NPL; ++i) k0 = max(k0, r.key[i]);
-  const float top = key_logit(wave_max(k0));
+  r.load(p.logits, 0, p.E, p.logit_type, lane);
+  const float top = key_logit(wave_max(r.head));
   float sum = p.renorm ? 0.f : r.exp_sum(top);
   int e = -1;
   float mine = 0.f;
@@ -181,7 +286,7 @@ __device__ inline void few_write_routing(const B8FewArgs& p, int z, int lane) {
     if (id < 0) break;
     const float v = expf(key_logit(k) - top);
     if (p.renorm) sum += v;
-    if (j == z - tok * p.topk) {
+    if (j == z) {
       e = id;
       mine = v;
       if (!p.renorm) break;
@@ -198,10 +303,9 @@ template <int NPL>
 __device__ inline int few_expert(const B8FewArgs& p, int z, int lane) {
   int e = -1;
   if (p.logits) {
-    const int tok = z / p.topk;
     Logits<NPL> x;
-    x.load(p.logits, tok, p.E, p.logit_type, lane);
-    for (int j = z - tok * p.topk; j >= 0; --j) {
+    x.load(p.logits, 0, p.E, p.logit_type, lane);
+    for (int j = z; j >= 0; --j) {
       uint32_t k;
       e = x.take(lane, &k);
       if (e < 0) break;
@@ -215,38 +319,12 @@ __device__ inline int few_expert(const B8FewArgs& p, int z, int lane) {
 
 // The slots that hold expert e, in order, into picks; returns how many.  Ends
 // with a barrier.
-template <int NPL>
-__device__ inline int few_slots(const B8FewArgs& p, int e, int* picks, int* npicks, int lane, int wave, int waves) {
-  const int T = p.t, topk = p.topk;
-  if (p.logits) {
-    // slot of token t that holds e: how many logits come before e's
-    for (int t0 = wave; t0 < T; t0 += 2 * waves) {
-      Logits<NPL> y[2];
-      uint32_t k[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = min(t0 + u * waves, T - 1);
-        y[u].load(p.logits, t, p.E, p.logit_type, lane);
-        k[u] = logit_key(load_logit_rt(p.logits, (int64_t)t * p.E + e, p.logit_type));
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = t0 + u * waves, rank = y[u].before(lane, e, k[u]);
-        if (lane == 0 && t < T) picks[t] = (k[u] && rank < topk) ? t * topk + rank : -1;
-      }
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const int s = lane < T ? picks[lane] : -1;  // T <= 64
-      const uint64_t has = __ballot(s >= 0);
-      if (s >= 0) picks[__popcll(has & ((1ull << lane) - 1))] = s;
-      if (lane == 0) *npicks = __popcll(has);
-    }
-  } else if (wave == 0) {
+__device__ inline int few_slots(const B8FewArgs& p, int e, int* picks, int* npicks, int lane, int wave) {
+  if (wave == 0) {
     int n = 0;
-    for (int b = 0; b < T * topk; b += 64) {
+    for (int b = 0; b < p.t * p.topk; b += 64) {
       const int s = b + lane;
-      const bool hit = s < T * topk && p.topk_ids[s] == e;
+      const bool hit = s < p.t * p.topk && p.topk_ids[s] == e;
       const uint64_t has = __ballot(hit);
       if (hit) picks[n + __popcll(has & ((1ull << lane) - 1))] = s;
       n += __popcll(has);
@@ -255,6 +333,60 @@ __device__ inline int few_slots(const B8FewArgs& p, int e, int* picks, int* npic
   }
   __syncthreads();
   return *npicks;
+}
+
+// The units of a tile of 16 tokens, for the down kernel: the distinct experts of
+// its slots.  A token may hold an expert more than once (given ids): each
+// occurrence is a unit of its own, so that a unit has at most one slot per
+// token.  One workgroup; key: 2 kMax + 4 ints of LDS.  Found here, beside the
+// stream, as in every down workgroup it cost up to a third of its time (13
+// tokens: 36 us against 31).
+template <int NW>
+__device__ inline void few_units(const B8FewArgs& p, int tile, int* key, int tid) {
+  constexpr int kMax = 16 * kB8FewMaxTopk;  // slots of a tile
+  static_assert(64 * NW >= kMax);
+  int* unit_of = key + kMax;  // index of a slot's unit, at the unit's first slot
+  int* wcount = unit_of + kMax;
+  const int lane = tid & 63, wave = tid >> 6;
+  const int topk = p.topk, t0 = tile * 16, ns = min(16, p.t - t0) * topk;
+  int32_t* out = p.units + (int64_t)tile * kB8FewUnitInts;
+  for (int i = tid; i < ns * 8; i += 64 * NW) out[16 + kMax + i] = -1;
+  int id = -1;
+  if (tid < ns) {
+    id = p.topk_ids[t0 * topk + tid];
+    if (id < 0 || id >= p.E) id = -1;
+  }
+  if (tid < kMax) key[tid] = id;
+  __syncthreads();
+  const int tok = tid / topk, from = tok * topk;
+  const bool have = tid < ns && id >= 0;
+  int occ = 0;
+  for (int j = 0; j < topk; ++j) occ += have && from + j < tid && key[min(from + j, kMax - 1)] == id;
+  __syncthreads();
+  const int k = id | (occ << 16);  // E is below 2^16
+  if (have) key[tid] = k;
+  __syncthreads();
+  int first = kMax;
+  for (int s = 0; s < ns; s += 4) {  // four keys a read, no read waits for another's result
+    const int4 v = *reinterpret_cast<const int4*>(key + s);
+    const int c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) first = min(first, c[q] == k ? s + q : kMax);
+  }
+  const bool lead = have && first == tid;
+  const uint64_t leads = __ballot(lead);
+  if (lane == 0 && wave < 4) wcount[wave] = __popcll(leads);
+  __syncthreads();
+  if (tid == 0) out[0] = wcount[0] + wcount[1] + wcount[2] + wcount[3];
+  if (lead) {
+    int at = __popcll(leads & ((1ull << lane) - 1));
+    for (int w = 0; w < wave; ++w) at += wcount[w];
+    unit_of[tid] = at;
+    out[16 + at] = id;
+  }
+  __syncthreads();
+  if (have) reinterpret_cast<int16_t*>(out + 16 + kMax)[unit_of[first] * 16 + tok] = (int16_t)tid;
+  __syncthreads();  // before the next tile
 }
 
 __device__ inline __amdgpu_buffer_rsrc_t few_rsrc(const void* base, int64_t bytes) {
@@ -282,15 +414,20 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // rows: codes [R][pitch], scales [R][G]
   __shared__ f4_t red[WIDE ? 1 : NW][2][64];
   __shared__ uint32_t tops[NW][16];
-  __shared__ int picks[kB8FewMaxSlots];
+  __shared__ __attribute__((aligned(16))) int picks[kB8FewMaxSlots];
   __shared__ int npicks;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kq = lane >> 4;
   const int z = blockIdx.y, K = p.H, G = K / 128;
   const int nbi = p.I / 16;
-  if (p.logits && blockIdx.x == gridDim.x - 1) {
-    if (wave == 0) few_write_routing<NPL>(p, z, lane);
+  if (z == p.t * p.topk) {  // the last row
+    if (p.logits) {
+      if (wave == 0)
+        for (int j = blockIdx.x; j < p.topk; j += gridDim.x) few_write_routing<NPL>(p, j, lane);
+    } else {
+      for (int tile = blockIdx.x; tile * 16 < p.t; tile += gridDim.x) few_units<NW>(p, tile, picks, tid);
+    }
     return;
   }
   // the slot's own row of x is the first of the rows below: its loads (up to
@@ -332,10 +469,10 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
   }
 
   int n = 1;
-  if (p.t == 1 && p.logits) {
+  if (p.logits) {  // one token, whose experts differ
     if (tid == 0) picks[0] = z;
   } else {
-    n = few_slots<NPL>(p, e, picks, &npicks, lane, wave, NW);
+    n = few_slots(p, e, picks, &npicks, lane, wave);
     if (picks[0] != z) return;
   }
 
@@ -436,76 +573,40 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
 // activation rows lie quantised in LDS (as many 128-k groups at a time as
 // fit); the waves take the (expert, group) steps in turn.
 // ---------------------------------------------------------------------------
-template <bool WIDE, int ST>
+template <bool WIDE, bool ONE, int ST>
 __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(4))) few_down(B8FewArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int kMaxTile = 16 * kB8FewMaxTopk;
+  constexpr int kMax = 16 * kB8FewMaxTopk;  // slots of a tile
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // codes [ns][pitch], scales [ns][gmax]
   __shared__ f4_t red[kFewWaves][64];
-  __shared__ int key[kMaxTile];            // expert | occurrence << 16, -1: none
-  __shared__ int unit_of[kMaxTile];        // index of a slot's unit, at the unit's first slot
-  __shared__ int unit_expert[kMaxTile];
-  __shared__ short slot_of[kMaxTile][16];  // [unit][token of the tile]: the slot with that key, -1 none
-  __shared__ float wt[kMaxTile];
-  __shared__ int wcount[4];
+  __shared__ int slots_of[ONE ? 1 : kMax * 8];  // [unit][token of the tile]: its slot as 16 bits, -1 none
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kq = lane >> 4;
   const int topk = p.topk, t0 = blockIdx.y * 16, nt = min(16, p.t - t0), ns = nt * topk;
   const int G = p.I / 128, N = p.H, nb = blockIdx.x;
 
-  // ---- the distinct experts of the tile's slots --------------------------------
-  // A token may hold an expert more than once (given ids): each occurrence is
-  // a unit of its own, so that a unit has at most one slot per token.
-  for (int i = tid; i < ns * 8; i += 64 * kFewWaves) reinterpret_cast<int*>(slot_of)[i] = -1;
-  int id = -1;
-  if (tid < ns) {
-    id = p.topk_ids[t0 * topk + tid];
-    if (id < 0 || id >= p.E) id = -1;
-    key[tid] = id;
-    wt[tid] = p.topk_w[t0 * topk + tid];
-  }
-  __syncthreads();
-  int first = -1, my_tok = 0;
-  if (nt == 1) {
-    first = id >= 0 ? tid : -1;  // every slot of one token is a unit
+  // A lane keeps the experts of four units (-1: none), so that a step finds its
+  // own without a trip to LDS.  One token's slots are its units, those without
+  // an expert too: their steps read nothing.
+  int nu, ue[4] = {-1, -1, -1, -1};
+  if constexpr (ONE) {
+    nu = ns;
+    ue[0] = lane < ns ? p.topk_ids[lane] : -1;
+    if (ue[0] >= p.E) ue[0] = -1;
   } else {
-    my_tok = tid / topk;
-    int occ = 0;
-    if (tid < ns && id >= 0)
-      for (int s = my_tok * topk; s < tid; ++s) occ += key[s] == id;
-    __syncthreads();
-    const int k = id | (occ << 16);
-    if (tid < ns && id >= 0) key[tid] = k;
-    __syncthreads();
-    if (tid < ns && id >= 0)
-      for (first = 0; key[first] != k; ++first) {
-      }
+    const int32_t* un = p.units + (int64_t)blockIdx.y * kB8FewUnitInts;
+    nu = __builtin_amdgcn_readfirstlane(un[0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ue[i] = un[16 + lane + 64 * i];  // (past nu whatever lies there, not used)
+    for (int i = tid; i < nu * 8; i += 64 * kFewWaves) slots_of[i] = un[16 + kMax + i];
   }
-  const bool lead = first >= 0 && first == tid;
-  const uint64_t leads = __ballot(lead);
-  if (lane == 0 && wave < 4) wcount[wave] = __popcll(leads);
-  __syncthreads();
-  const int nu = wcount[0] + wcount[1] + wcount[2] + wcount[3];
-  if (lead) {
-    int at = __popcll(leads & ((1ull << lane) - 1));
-    for (int w = 0; w < wave; ++w) at += wcount[w];
-    unit_of[tid] = at;
-    unit_expert[at] = id;
-  }
-  __syncthreads();
-  if (first >= 0) slot_of[unit_of[first]][my_tok] = (short)tid;
 
   const int gmax = p.down_groups, pitch = gmax * 128 + 16;
   float* sc = reinterpret_cast<float*>(lds + ns * pitch);  // [ns][gmax]
   u4_t wr[ST][2];
   uint32_t sw[ST];
   f4_t acc = f4_t{0.f, 0.f, 0.f, 0.f};
-  // a lane keeps the experts of four units, so that a step finds its own
-  // without a trip to LDS
-  int ue[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) ue[i] = lane + 64 * i < nu ? unit_expert[lane + 64 * i] : 0;
   for (int gc0 = 0; gc0 < G && nu; gc0 += gmax) {
     const int gc = min(gmax, G - gc0), steps = nu * gc;
     // step i is (unit i / gc, group i % gc), kept as a pair that the waves'
@@ -524,10 +625,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
     };
     Step ahead{wave / gc, wave % gc}, now = ahead;
     auto issue = [&](int slot) {
-      const bool in = ahead.u < nu;
+      bool in = ahead.u < nu;
       const int u = in ? ahead.u : 0, g = gc0 + ahead.g;
       int e = __builtin_amdgcn_readlane(ue[0], u & 63);
-      if (nu > 64) {
+      if constexpr (ONE) {
+        in &= e >= 0;
+        e = max(e, 0);
+      } else if (nu > 64) {
         const int e1 = __builtin_amdgcn_readlane(ue[1], u & 63);
         const int e2 = __builtin_amdgcn_readlane(ue[2], u & 63), e3 = __builtin_amdgcn_readlane(ue[3], u & 63);
         e = u < 128 ? (u < 64 ? e : e1) : (u < 192 ? e2 : e3);
@@ -549,8 +653,10 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 #pragma unroll 1
     for (int i = tid >> 4; i < ns * gc; i += 4 * kFewWaves) {
       const int s = i / gc, g = i - s * gc;
-      if (key[s] < 0) continue;  // its row was not written
+      // (the row of a slot without an expert was not written: what lies there
+      // is quantised and not used)
       const int64_t slot = t0 * topk + s;
+      const float ws = p.topk_w[slot];
       float f;
       uint2 q;
       if constexpr (WIDE) {
@@ -567,7 +673,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
         q = uint2{b8_codes(a[0], a[1], a[2], a[3], d), b8_codes(b[0], b[1], b[2], b[3], d)};
       }
       *reinterpret_cast<uint2*>(lds + s * pitch + g * 128 + c16 * 8) = q;
-      if (c16 == 0) sc[s * gmax + g] = f * wt[s];  // the top-k weight rides on the scale
+      if (c16 == 0) sc[s * gmax + g] = f * ws;  // the top-k weight rides on the scale
     }
     __syncthreads();
 #pragma unroll 1
@@ -575,9 +681,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 #pragma unroll
       for (int s = 0; s < ST; ++s) {
         const bool in = now.u < nu;
-        const int sl = slot_of[in ? now.u : 0][c16];
+        int sl;
+        if constexpr (ONE)
+          sl = c16 == 0 && __builtin_amdgcn_readlane(ue[0], in ? now.u : 0) >= 0 ? now.u : -1;
+        else
+          sl = reinterpret_cast<const int16_t*>(slots_of)[(in ? now.u : 0) * 16 + c16];
         const bool has = in && sl >= 0;  // lanes of other tokens take nothing
-        const int row = max(sl, 0);
+        const int row = has ? sl : 0;
         const uint8_t* ar = lds + row * pitch + now.g * 128 + kq * 16;
         const f4_t P = b8_mfma(cat8(wr[s][0], wr[s][1]),
                                cat8(*reinterpret_cast<const u4_t*>(ar), *reinterpret_cast<const u4_t*>(ar + 64)));
@@ -612,16 +722,13 @@ hipError_t gate_up_k(const B8FewArgs& a, dim3 grid, size_t lds, hipStream_t s) {
   return launch_timed(few_gate_up<NPL, BF16, WIDE, NW, ST>, grid, dim3(64 * NW), lds, s, a);
 }
 
-template <int NPL, bool BF16>
+template <bool BF16>
 hipError_t gate_up_s(const B8FewArgs& a, dim3 grid, size_t lds, hipStream_t s) {
-  if (a.act_codes) return gate_up_k<NPL, BF16, true, 8, 6>(a, grid, lds, s);
-  if (a.t == 1) return gate_up_k<NPL, BF16, false, 8, 7>(a, grid, lds, s);
-  return gate_up_k<NPL, BF16, false, 4, 4>(a, grid, lds, s);
-}
-
-template <int NPL>
-hipError_t gate_up_t(const B8FewArgs& a, dim3 grid, size_t lds, hipStream_t s) {
-  return a.x_bf16 ? gate_up_s<NPL, true>(a, grid, lds, s) : gate_up_s<NPL, false>(a, grid, lds, s);
+  if (a.act_codes) return gate_up_k<1, BF16, true, 8, 6>(a, grid, lds, s);
+  if (a.t > 1) return gate_up_k<1, BF16, false, 4, 4>(a, grid, lds, s);
+  if (!a.logits || a.E <= 64) return gate_up_k<1, BF16, false, 8, 7>(a, grid, lds, s);
+  if (a.E <= 256) return gate_up_k<4, BF16, false, 8, 7>(a, grid, lds, s);
+  return gate_up_k<16, BF16, false, 8, 7>(a, grid, lds, s);
 }
 
 }  // namespace
@@ -631,6 +738,18 @@ int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits,
   const dim3 grid((unsigned)((t + 3) / 4)), block(256);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int ti = (int)t;
+  // 64 experts or fewer leave a wave per token nothing to gain; for more, a wave
+  // has the shorter chain and sixteen lanes the fewer instructions (256 experts,
+  // top 8, fp32: 4096 tokens 6.0 us by waves, 6.5 by rows, 16383 15.6 and 11.0)
+  if (topk <= 16 && (E <= 64 || (E <= 256 && t >= 6144))) {
+    const dim3 rows((unsigned)((t + 15) / 16));
+    auto go = [&]<int LT>() -> int {
+      if (E <= 64) return (int)launch_timed(route_rows_kernel<LT, 4>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
+      if (E <= 128) return (int)launch_timed(route_rows_kernel<LT, 8>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
+      return (int)launch_timed(route_rows_kernel<LT, 16>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
+    };
+    return logit_type == 0 ? go.template operator()<0>() : (logit_type == 1 ? go.template operator()<1>() : go.template operator()<2>());
+  }
   if (E <= 64) return (int)launch_timed(route_kernel<1>, grid, block, 0, s, logits, logit_type, ti, E, topk, renorm, ids, w);
   if (E <= 128) return (int)launch_timed(route_kernel<2>, grid, block, 0, s, logits, logit_type, ti, E, topk, renorm, ids, w);
   if (E <= 256) return (int)launch_timed(route_kernel<4>, grid, block, 0, s, logits, logit_type, ti, E, topk, renorm, ids, w);
@@ -657,12 +776,10 @@ int launch_few_gate_up(const B8FewArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   B8FewArgs b = a;
   b.rows = few_rows(a);
-  const dim3 grid((unsigned)(a.I / (a.act_codes ? 128 : 16) + (a.logits ? 1 : 0)), (unsigned)(a.t * a.topk));
+  const dim3 grid((unsigned)(a.I / (a.act_codes ? 128 : 16)), (unsigned)(a.t * a.topk + (a.logits || a.t > 1 ? 1 : 0)));
   const size_t lds = (size_t)b.rows * (a.H + 16 + a.H / 128 * 4);
-  if (lds > kFewLds) return (int)hipErrorInvalidValue;
-  if (!a.logits || a.E <= 64) return (int)gate_up_t<1>(b, grid, lds, s);
-  if (a.E <= 256) return (int)gate_up_t<4>(b, grid, lds, s);
-  return (int)gate_up_t<16>(b, grid, lds, s);
+  if (lds > kFewLds || (a.logits && a.t > 1)) return (int)hipErrorInvalidValue;
+  return a.x_bf16 ? (int)gate_up_s<true>(b, grid, lds, s) : (int)gate_up_s<false>(b, grid, lds, s);
 }
 
 int launch_few_down(const B8FewArgs& a, void* stream) {
@@ -671,14 +788,15 @@ int launch_few_down(const B8FewArgs& a, void* stream) {
   b.down_groups = few_down_groups(a);
   const size_t lds = (size_t)std::min(a.t, 16) * a.topk * (b.down_groups * 132 + 16);
   const dim3 grid((unsigned)(a.H / 16), (unsigned)((a.t + 15) / 16)), block(64 * kFewWaves);
-  auto go = [&]<bool WIDE, int ST>() -> int {
-    const hipError_t e = allow_lds<few_down<WIDE, ST>>(kFewLds);
-    return e != hipSuccess ? (int)e : (int)launch_timed(few_down<WIDE, ST>, grid, block, lds, s, b);
+  auto go = [&]<bool WIDE, bool ONE, int ST>() -> int {
+    const hipError_t e = allow_lds<few_down<WIDE, ONE, ST>>(kFewLds);
+    return e != hipSuccess ? (int)e : (int)launch_timed(few_down<WIDE, ONE, ST>, grid, block, lds, s, b);
   };
   // up to two steps a wave need no deeper ring
-  if (std::min(a.t, 16) * a.topk * b.down_groups <= 2 * kFewWaves)
-    return a.act_codes ? go.template operator()<true, 2>() : go.template operator()<false, 2>();
-  return a.act_codes ? go.template operator()<true, 6>() : go.template operator()<false, 6>();
+  const bool little = std::min(a.t, 16) * a.topk * b.down_groups <= 2 * kFewWaves;
+  if (a.act_codes) return little ? go.template operator()<true, false, 2>() : go.template operator()<true, false, 6>();
+  if (a.t == 1) return little ? go.template operator()<false, true, 2>() : go.template operator()<false, true, 6>();
+  return little ? go.template operator()<false, false, 2>() : go.template operator()<false, false, 6>();
 }
 
 }  // namespace hq

@@ -252,7 +252,7 @@ def test_few_call_refused():
     wide = [hq.MoePlan(512, 1024, q, 1100, 64, "silu_mul_qfp8"), hq.MoePlan(1024, 256, q, 1100, 64, "topk_combine")]
     assert call(gu=wide[0], dn=wide[1]) == hq.HQ_ERR_UNSUPPORTED                      # routing: up to 1024 experts
     b = ctypes.c_size_t()
-    assert L.hq_moe_few_workspace_bytes(g._h, d._h, 4, 2, ctypes.byref(b)) == hq.HQ_OK and b.value == 4 * 2 * 256 * 4
+    assert L.hq_moe_few_workspace_bytes(g._h, d._h, 4, 2, ctypes.byref(b)) == hq.HQ_OK and b.value >= 4 * 2 * 256 * 4
     assert L.hq_moe_few_workspace_bytes(g._h, d._h, 65, 2, ctypes.byref(b)) == hq.HQ_ERR_INVALID_ARG
 
 
