@@ -305,6 +305,26 @@ class _on:
             torch.cuda.set_device(self.was)
 
 
+def _run(dev, fn, *args):
+    """fn(*args, dev's current stream) with dev current."""
+    i = dev.index
+    if torch._C._cuda_getDevice() == i:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with _on(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status != HQ_OK:
+        _check(status)
+
+
+def _same_device(dev, *tensors) -> bool:
+    """All contiguous tensors on dev, a GPU (the quick form of _dev's checks)."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
+            return False
+    return dev.type == "cuda"
+
+
 _TORCH_OUT = {F16: torch.float16, BF16: torch.bfloat16}
 _LOGITS = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _DT_NAME = {F16: "f16", BF16: "bf16", FP8_E4M3: "fp8", INT8: "int8", FP4_E2M1: "mxfp4"}
@@ -491,9 +511,10 @@ class Plan:
         the call's own unless one is given, so that calls on several streams, or
         captured into several graphs, do not share one."""
         dev = a.device
-        for t, name in ((a, "a"), (w, "w"), (meta, "meta"), (a_scale, "a_scale")):
-            if _dev(t, name).device != dev:
-                raise ValueError(f"{name} must be on a's device")
+        if not _same_device(dev, a, w, meta, a_scale):
+            for t, name in ((a, "a"), (w, "w"), (meta, "meta"), (a_scale, "a_scale")):
+                if _dev(t, name).device != dev:
+                    raise ValueError(f"{name} must be on a's device")
         if a.dim() != 2 or a.shape[1] != self.k or a.element_size() != 1:
             raise ValueError(f"a must hold one-byte fp8 codes [m, {self.k}]")
         m = a.shape[0]
@@ -501,22 +522,21 @@ class Plan:
             raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
         self._check_block_layout(w, meta)
         if out is None:
-            out = torch.empty((m, self.n), dtype=_TORCH_OUT[self.quant.out], device=dev)
+            out = a.new_empty((m, self.n), dtype=_TORCH_OUT[self.quant.out])
         elif _dev(out, "out").shape != (m, self.n) or out.dtype != _TORCH_OUT[self.quant.out] or out.device != dev:
             raise ValueError(f"out must be {_TORCH_OUT[self.quant.out]} [m, {self.n}] on a's device")
         need = self._ws_need.get(m)
         if need is None:
             need = self._ws_need[m] = self.workspace_bytes(m)
         if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        with _on(dev):
-            _check(lib().hq_gemm(self._h, m, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), meta.data_ptr(), out.data_ptr(),
-                                 _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_ptr(dev)))
+            ws = a.new_empty(need, dtype=torch.uint8)
+        _run(dev, lib().hq_gemm, self._h, m, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), meta.data_ptr(), out.data_ptr(),
+             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
         return out
 
     def _check_block_layout(self, w, meta):
-        if w.numel() * w.element_size() < self.num_experts * self.n * self.k or \
-                meta.numel() * meta.element_size() < self.num_experts * (-(-self.n // 128)) * (self.k // 128) * 4:
+        if w.nbytes < self.num_experts * self.n * self.k or \
+                meta.nbytes < self.num_experts * (-(-self.n // 128)) * (self.k // 128) * 4:
             raise ValueError("w and meta must be what repack returned for this plan")
 
     def linear(self, x: torch.Tensor, w: torch.Tensor, meta: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -720,16 +740,15 @@ def quantize_blocks(x: torch.Tensor, silu_mul: bool = False, codes: Optional[tor
         k //= 2
     dev = x.device
     if codes is None:
-        codes = torch.empty((m, k), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((m, k), dtype=torch.uint8) if silu_mul else torch.empty_like(x, dtype=torch.uint8)
     elif _dev(codes, "codes").shape != (m, k) or codes.element_size() != 1 or codes.device != dev:
         raise ValueError("codes must be 1-byte [m, k] on x's device")
     if scales is None:
-        scales = torch.empty((k // 128, m), dtype=torch.float32, device=dev)
+        scales = x.new_empty((k // 128, m), dtype=torch.float32)
     elif _dev(scales, "scales").shape != (k // 128, m) or scales.dtype != torch.float32 or scales.device != dev:
         raise ValueError("scales must be float32 [k/128, m] on x's device")
-    with _on(dev):
-        _check(lib().hq_quantize_blocks(m, k, BF16 if x.dtype == torch.bfloat16 else F16, 1 if silu_mul else 0,
-                                        x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream_ptr(dev)))
+    _run(dev, lib().hq_quantize_blocks, m, k, BF16 if x.dtype == torch.bfloat16 else F16, 1 if silu_mul else 0,
+         x.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -919,11 +938,11 @@ def route_topk(logits: torch.Tensor, topk: int, renormalize: bool = True):
     if logits.dim() != 2 or logits.dtype not in _LOGITS:
         raise ValueError("logits must be fp32 / fp16 / bf16 [t, experts]")
     t, experts = logits.shape
-    ids = torch.empty((t, int(topk)), dtype=torch.int32, device=logits.device)
-    w = torch.empty((t, int(topk)), dtype=torch.float32, device=logits.device)
-    with _on(logits.device):
-        _check(lib().hq_route_topk(t, experts, int(topk), _LOGITS[logits.dtype], logits.data_ptr(), 1 if renormalize else 0,
-                                   ids.data_ptr(), w.data_ptr(), _stream_ptr(logits.device)))
+    topk = int(topk)
+    ids = logits.new_empty((t, topk), dtype=torch.int32)
+    w = logits.new_empty((t, topk), dtype=torch.float32)
+    _run(logits.device, lib().hq_route_topk, t, experts, topk, _LOGITS[logits.dtype], logits.data_ptr(),
+         1 if renormalize else 0, ids.data_ptr(), w.data_ptr())
     return ids, w
 
 
@@ -936,9 +955,11 @@ def _uses_few(gate_up: "MoePlan", t: int, topk: int) -> bool:
 
 
 def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2):
-    for v, nm in ((x, "x"), (ids, "topk_ids"), (w, "topk_w"), (w1, "w1"), (m1, "m1"), (w2, "w2"), (m2, "m2")):
-        if _dev(v, nm).device != x.device:
-            raise ValueError(f"{nm} must be on x's device")
+    dev = x.device
+    if not _same_device(dev, x, ids, w, w1, m1, w2, m2):
+        for v, nm in ((x, "x"), (ids, "topk_ids"), (w, "topk_w"), (w1, "w1"), (m1, "m1"), (w2, "w2"), (m2, "m2")):
+            if _dev(v, nm).device != dev:
+                raise ValueError(f"{nm} must be on x's device")
     t = x.shape[0]
     if x.dim() != 2 or x.shape[1] != gate_up.k or x.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"x must be fp16 / bf16 [t, {gate_up.k}]")
@@ -949,15 +970,12 @@ def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2
         n = ctypes.c_size_t()
         _check(lib().hq_moe_few_workspace_bytes(gate_up._h, down._h, t, topk, ctypes.byref(n)))
         need = gate_up._few_need[t, topk, down.k] = n.value
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    out = torch.empty((t, down.n), dtype=_TORCH_OUT[down.quant.out], device=x.device)
+    ws = x.new_empty(need, dtype=torch.uint8)
+    out = x.new_empty((t, down.n), dtype=_TORCH_OUT[down.quant.out])
     gate_up._check_block_layout(w1, m1), down._check_block_layout(w2, m2)
-    with _on(x.device):
-        _check(lib().hq_moe_layer_few(gate_up._h, down._h, t, topk, BF16 if x.dtype == torch.bfloat16 else F16,
-                                      x.data_ptr(), F32 if logits is None else _LOGITS[logits.dtype], _ptr(logits),
-                                      1 if renormalize else 0, ids.data_ptr(), w.data_ptr(), w1.data_ptr(),
-                                      m1.data_ptr(), w2.data_ptr(), m2.data_ptr(), out.data_ptr(), ws.data_ptr(),
-                                      need, _stream_ptr(x.device)))
+    _run(dev, lib().hq_moe_layer_few, gate_up._h, down._h, t, topk, BF16 if x.dtype == torch.bfloat16 else F16, x.data_ptr(),
+         F32 if logits is None else _LOGITS[logits.dtype], _ptr(logits), 1 if renormalize else 0, ids.data_ptr(), w.data_ptr(),
+         w1.data_ptr(), m1.data_ptr(), w2.data_ptr(), m2.data_ptr(), out.data_ptr(), ws.data_ptr(), need)
     return out
 
 
@@ -972,8 +990,8 @@ def moe_layer_routed(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, logit
             logits.device != x.device:
         raise ValueError(f"logits must be fp32 / fp16 / bf16 [{x.shape[0]}, {gate_up.num_experts}] on x's device")
     if _uses_few(gate_up, x.shape[0], topk) and gate_up.num_experts <= 1024:
-        ids = torch.empty((x.shape[0], topk), dtype=torch.int32, device=x.device)
-        w = torch.empty((x.shape[0], topk), dtype=torch.float32, device=x.device)
+        ids = x.new_empty((x.shape[0], topk), dtype=torch.int32)
+        w = x.new_empty((x.shape[0], topk), dtype=torch.float32)
         return _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2), ids, w
     ids, w = route_topk(logits, topk, renormalize)
     return moe_layer(gate_up, down, x, ids, w, w1, m1, w2, m2), ids, w
