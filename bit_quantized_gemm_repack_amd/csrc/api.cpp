@@ -261,9 +261,11 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
     // The lowest row tile that gives no more than so many tiles.  With long K
     // (32 groups on) the rows are covered in one or two tiles first, and a
     // split of K fills the chip (128 rows of (4096, 7168): 64-row tiles in 4
-    // splits 15.5, 16-row tiles 19.8 us); with short K a split's second pass
-    // costs more than the lower tile's weight traffic (128 rows of (7168,
-    // 2048): 32-row tiles 7.8, 64-row tiles in 2 splits 13.2 us).
+    // splits 15.5, 16-row tiles 19.8 us), unless a narrow N leaves few tiles
+    // even so (200 rows of (576, 7168): 32-row tiles in 4 splits 10.7, 64-row
+    // tiles in 8 12.1 us); with short K a split's second pass costs more than
+    // the lower tile's weight traffic (128 rows of (7168, 2048): 32-row tiles
+    // 7.8, 64-row tiles in 2 splits 13.2 us).
     const bool longk = G >= 32;
     const struct {
       int bm;
@@ -272,7 +274,7 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
     e.tl.bm = 128;
     e.tl.nbw = 4;  // 256 columns: enough tiles whatever the shape
     for (const auto& t : tiles) {
-      if (longk && ((t.bm == 16 && mm > 32) || (t.bm == 32 && mm > 64))) continue;
+      if (longk && ((t.bm == 16 && mm > 32) || (t.bm == 32 && mm > 64 && cdiv(mm, 32) * n128 > 56))) continue;
       if (cdiv(mm, t.bm) * n128 > t.most) continue;
       e.tl.bm = t.bm;
       e.tl.nbw = 2;
