@@ -665,10 +665,13 @@ int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* s
   B8Args b = a;
   const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) + 4 * b8_rows_lds(4) <= kShortLds;
   if (whole) {
-    // columns a workgroup walks: at least four tiles' worth where that leaves
-    // the chip four workgroups a CU, and never more than the window
+    // column tiles a workgroup walks: two where there are plenty (they share
+    // the rows' staging; more leave the last workgroups a long tail).  256
+    // experts, H = 7168, I = 256, by 1 / 2 / 4 / 7 / 14 tiles: 100 tokens 78.1 /
+    // 77.8 / 79.7 / 86.5 / 85.9 us, 509 122 / 118 / 121 / 127 / 134, 4096 340 /
+    // 323 / 347 / 364 / 399; 64 experts of H = 2048, 1000 tokens 27.2 / 28.4 / 33.2.
     const int64_t tiles = (a.ncol + 255) / 256;
-    const int64_t per = std::max<int64_t>(1, std::min<int64_t>(tiles, tiles * blocks / 1024));
+    const int64_t per = tiles * blocks >= 1536 ? 2 : 1;
     b.cols_wg = (int)(256 * per);
     b.tiles_n = (int)((tiles + per - 1) / per);
   } else {
