@@ -456,8 +456,7 @@ class Plan:
         self._check_block_weight(codes, scales)
         w, meta = self._repack_outputs(codes.device)
         zx = e8m0 if e8m0 is not None else zeros
-        _check(lib().hq_repack(self._h, _ptr(codes), _ptr(scales), _ptr(zx), _ptr(w), _ptr(meta),
-                               _stream_ptr(codes.device)))
+        _run(codes.device, lib().hq_repack, self._h, _ptr(codes), _ptr(scales), _ptr(zx), _ptr(w), _ptr(meta))
         return w, meta
 
     def repack_host(self, codes: torch.Tensor, scales: Optional[torch.Tensor] = None,
@@ -799,8 +798,8 @@ def moe_align(topk_ids: torch.Tensor, num_experts: int, block_m: int):
     sorted_ids = torch.empty(mp, dtype=torch.int32, device=dev)
     block_expert = torch.empty(max(mp // block_m, 1), dtype=torch.int32, device=dev)
     num_padded = torch.empty(1, dtype=torch.int32, device=dev)
-    _check(lib().hq_moe_align(t, topk, int(num_experts), int(block_m), _ptr(topk_ids), _ptr(sorted_ids),
-                              _ptr(block_expert), _ptr(num_padded), _stream_ptr(dev)))
+    _run(dev, lib().hq_moe_align, t, topk, int(num_experts), int(block_m), _ptr(topk_ids), _ptr(sorted_ids),
+         _ptr(block_expert), _ptr(num_padded))
     return sorted_ids, block_expert, num_padded
 
 
@@ -867,6 +866,19 @@ class MoePlan(Plan):
                     a.element_size() != 1 or a.numel() != rows * self.k:
                 raise ValueError(f"a must hold [{rows}, {self.k}] one-byte codes and a_scale float32 [{self.k // 128}, {rows}]")
             self._check_block_layout(w, meta)
+            down = self.epi == EPI_TOPK_COMBINE
+            if not _same_device(dev, a_scale, sorted_ids, block_expert, num_padded, w, meta, out) or \
+                    not _same_device(dev, topk_w if down else out_scale):
+                raise ValueError("the tensors of a w8a8_block GEMM must be contiguous and on a's device")
+            if any(v.dtype != torch.int32 for v in (sorted_ids, block_expert, num_padded)):
+                raise ValueError("sorted_ids, block_expert and num_padded must be int32")
+            if down and (topk_w.dtype != torch.float32 or topk_w.numel() != t * topk):
+                raise ValueError(f"topk_w must be float32 [{t}, {topk}]")
+            if out.dtype != (_TORCH_OUT[self.quant.out] if down else torch.uint8) or \
+                    out.numel() != (t * self.n if down else mp * (self.n // 2)):
+                raise ValueError("out must be [t, n] of the output type, or uint8 codes [rows, n/2]")
+            if not down and (out_scale.dtype != torch.float32 or out_scale.numel() != mp * (self.n // 256)):
+                raise ValueError(f"out_scale must be float32 [{self.n // 256}, {mp}]")
             if ws is None and self.epi == EPI_TOPK_COMBINE:  # of the call's own, as in gemm
                 b = ctypes.c_size_t()
                 _check(lib().hq_moe_workspace_bytes(self._h, int(t), int(topk), ctypes.byref(b)))
@@ -874,9 +886,9 @@ class MoePlan(Plan):
         if ws is None and not self._block8:
             ws = self.moe_workspace(t, topk, dev)
         ws_bytes = 0 if ws is None else ws.numel()
-        _check(lib().hq_moe_gemm(self._h, int(t), int(topk), _ptr(a), _ptr(a_scale), _ptr(sorted_ids),
-                                 _ptr(block_expert), _ptr(num_padded), _ptr(topk_w), _ptr(w), _ptr(meta), _ptr(out),
-                                 _ptr(out_scale), _ptr(ws), ws_bytes, _stream_ptr(dev)))
+        _run(dev, lib().hq_moe_gemm, self._h, int(t), int(topk), _ptr(a), _ptr(a_scale), _ptr(sorted_ids),
+             _ptr(block_expert), _ptr(num_padded), _ptr(topk_w), _ptr(w), _ptr(meta), _ptr(out), _ptr(out_scale),
+             _ptr(ws), ws_bytes)
         return (out, out_scale) if self.epi == EPI_SILU_MUL_QFP8 else out
 
     def moe_gemm_by_slot(self, a: torch.Tensor, t: int, topk: int, topk_ids: torch.Tensor, w: torch.Tensor,
@@ -1014,6 +1026,8 @@ def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: to
     if gate_up._block8:
         if by_slot:
             raise ValueError("w8a8_block layers have no by-slot path")
+        if t == 0:
+            return x.new_empty((0, down.n), dtype=_TORCH_OUT[down.quant.out])
         if x_scale is None and _uses_few(gate_up, t, topk):
             return _moe_few(gate_up, down, x, topk, topk_ids, topk_w, None, False, w1, m1, w2, m2)
         by_slot = False

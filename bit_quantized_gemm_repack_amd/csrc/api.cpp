@@ -1564,6 +1564,11 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* p, int64_t t, int topk, const void*
 }
 
 static int logit_type_of(hq_dtype t) { return t == HQ_F32 ? 0 : (t == HQ_BF16 ? 1 : (t == HQ_F16 ? 2 : -1)); }
+// Slices of a batch start anywhere: these are read element by element.
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+static bool aligned_logits(const void* p, int logit_type) {
+  return (reinterpret_cast<uintptr_t>(p) & (logit_type == 0 ? 3 : 1)) == 0;
+}
 
 hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, int renormalize,
                         int32_t* topk_ids, float* topk_w, void* stream) {
@@ -1577,8 +1582,8 @@ hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_typ
   if (renormalize != 0 && renormalize != 1) return fail(HQ_ERR_INVALID_ARG, "renormalize must be 0 or 1");
   if (t == 0) return ok();
   if (!logits || !topk_ids || !topk_w) return fail(HQ_ERR_INVALID_ARG, "null device pointer");
-  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_w))
-    return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  if (!aligned_logits(logits, lt) || !aligned4(topk_ids) || !aligned4(topk_w))
+    return fail(HQ_ERR_INVALID_ARG, "logits, topk_ids and topk_w must be aligned to their elements");
   hq::arm_timing(ev);
   const int err = hq::launch_route(t, num_experts, topk, lt, logits, renormalize, topk_ids, topk_w, stream);
   hq::arm_timing({nullptr, nullptr});
@@ -1639,8 +1644,10 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
   if (t == 0) return ok();
   if (!x || !topk_ids || !topk_w || !w1 || !meta1 || !w2 || !meta2 || !out)
     return fail(HQ_ERR_INVALID_ARG, "null device pointer");
-  for (const void* p : {x, (const void*)logits, (const void*)topk_ids, (const void*)topk_w, w1, meta1, w2, meta2, (const void*)out})
+  for (const void* p : {x, w1, meta1, w2, meta2, (const void*)out})
     if (!aligned16(p)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  if (!aligned_logits(logits, lt) || !aligned4(topk_ids) || !aligned4(topk_w))
+    return fail(HQ_ERR_INVALID_ARG, "logits, topk_ids and topk_w must be aligned to their elements");
   const int64_t H = gate_up->layer.k, I = down->layer.k;
   const size_t need = few_workspace(t, topk, down);
   if (!ws || ws_bytes < need) return fail(HQ_ERR_WORKSPACE, "this call needs %zu workspace bytes", need);

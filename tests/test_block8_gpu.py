@@ -564,6 +564,71 @@ def test_layer_dispatch_and_refusals():
         L.routed(x[:2], torch.randn(2, 8, device=DEV), 9)
 
 
+def test_layer_odd_calls():
+    """No tokens, slices of a batch that start anywhere, one token with an expert
+    several times and ids outside the experts, codes where few tokens would run."""
+    L = Layer(12, 9, 512, 128, 64)
+    x = _x(L.g, 24, 512, torch.bfloat16)
+    logits = _logits(L.g, 24, 9, torch.bfloat16, masked=False)
+    ids, w = hq.route_topk(logits, 3)
+    y, ri, rw = L.routed(x[:0], logits[:0], 3)
+    assert y.shape == (0, 512) and ri.shape == rw.shape == (0, 3)
+    assert L.run(x[:0], ids[:0], w[:0]).shape == (0, 512)
+    for a, b in ((1, 2), (3, 8), (5, 24)):            # 18-byte rows of logits, 12-byte rows of ids
+        y, ri, rw = L.routed(x[a:b], logits[a:b], 3)
+        z = L.run(x[a:b], ids[a:b], w[a:b])
+        torch.cuda.synchronize()
+        assert torch.equal(ri, ids[a:b]) and torch.equal(hq.route_topk(logits[a:b], 3)[0], ids[a:b])
+        L.check(y, x[a:b], ri, rw, "routed slice", ROW_ERR)
+        L.check(z, x[a:b], ids[a:b], w[a:b], "slice", ROW_ERR)
+    one = torch.tensor([[4, 4, -1, 9, 4, 0]], dtype=torch.int32, device=DEV)
+    ow = torch.rand(1, 6, generator=L.g, device=DEV)
+    y = L.run(x[:1], one, ow)
+    torch.cuda.synchronize()
+    L.check(y, x[:1], one, ow, "one token")
+    none = torch.full((1, 6), -1, dtype=torch.int32, device=DEV)
+    assert (L.run(x[:1], none, ow) == 0).all()
+    q, s = hq.quantize_blocks(x[:4].contiguous())
+    y = L.run(q, ids[:4], w[:4], x_scale=s)
+    torch.cuda.synchronize()
+    L.check(y, x[:4], ids[:4], w[:4], "codes of few tokens", ROW_ERR)
+
+
+def test_grouped_refuses_wrong_tensors():
+    L = Layer(13, 8, 512, 128, 64)
+    x = _x(L.g, 40, 512, torch.bfloat16)
+    ids, w = _routing(L.g, 40, 8, 2)
+    q, s = hq.quantize_blocks(x)
+    al = hq.moe_align(ids, 8, L.gu.block_m(40, 2))
+    codes, sc = L.gu.moe_gemm(q, 40, 2, *al, *L.wm[:2], a_scale=s)
+    down = lambda a_scale=sc, topk_w=w, **kw: L.dn.moe_gemm(codes, 40, 2, *al, *L.wm[2:], a_scale=a_scale, topk_w=topk_w, **kw)
+    down()
+    for kw in (dict(topk_w=w.cpu()), dict(topk_w=w.double()), dict(topk_w=w[:20].contiguous()), dict(topk_w=None),
+               dict(a_scale=sc.cpu()), dict(out=torch.empty(39, 512, dtype=torch.bfloat16, device=DEV)),
+               dict(out=torch.empty(40, 512, device=DEV))):
+        with pytest.raises(ValueError):
+            down(**kw)
+    with pytest.raises(ValueError):
+        L.gu.moe_gemm(q, 40, 2, *al, *L.wm[:2], a_scale=s, out=codes[:-1].contiguous())
+    with pytest.raises(ValueError):
+        L.gu.moe_gemm(q, 40, 2, *al, *L.wm[:2], a_scale=s, out_scale=sc[:0].contiguous())
+
+
+def test_quantize_beyond_32_bits():
+    """More than 2^31 values: the last rows are right."""
+    m, k = 300001, 7168
+    _log(f"quantize {m} {k}")
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device=DEV)
+    for r in (0, m // 2, m - 1):
+        x[r] = _x(_gen(r), 1, k, torch.bfloat16)[0]
+    codes, s = hq.quantize_blocks(x)
+    torch.cuda.synchronize()
+    for r in (0, m // 2, m - 1):
+        want, ws = o8.quantize(x[r:r + 1].double())
+        assert torch.equal(codes[r:r + 1].view(E4).double(), want) and torch.equal(s[:, r:r + 1].t().double(), ws)
+    assert (s[:, 1:m // 2] == 1).all()
+
+
 # ------------------------------------------------------------ streams, graphs --
 def test_graph_of_everything():
     """Quantise, split-K GEMM, routing and both layers in one graph: every replay

@@ -225,7 +225,7 @@ def test_route_call_refused():
         assert r(4, e, k, hq.F32, FAKE, 0, FAKE, FAKE, None) == hq.HQ_ERR_INVALID_ARG
     assert r(-1, 8, 2, hq.F32, FAKE, 0, FAKE, FAKE, None) == hq.HQ_ERR_INVALID_ARG
     assert r(4, 8, 2, hq.F32, FAKE, 2, FAKE, FAKE, None) == hq.HQ_ERR_INVALID_ARG
-    for bad in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (FAKE + 4, FAKE, FAKE)):
+    for bad in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (FAKE + 2, FAKE, FAKE), (FAKE, FAKE + 2, FAKE)):
         assert r(4, 8, 2, hq.F32, bad[0], 0, bad[1], bad[2], None) == hq.HQ_ERR_INVALID_ARG
     assert r(0, 8, 2, hq.F32, None, 0, None, None, None) == hq.HQ_OK
 
