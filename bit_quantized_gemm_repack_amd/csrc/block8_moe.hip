@@ -507,11 +507,11 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
 #pragma unroll
       for (int s = 0; s < ST; ++s) {
         const int gg = min(g + s * gd, G - 1);
-        const i8_t av = cat8(*reinterpret_cast<const u4_t*>(ar + gg * 128), *reinterpret_cast<const u4_t*>(ar + gg * 128 + 64));
+        const auto av = b8_halves(*reinterpret_cast<const u4_t*>(ar + gg * 128), *reinterpret_cast<const u4_t*>(ar + gg * 128 + 64));
         const float f = sa[rl * G + gg];  // past the end the weights and their scales are zero
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const f4_t P = b8_mfma(cat8(wr[s][u][0], wr[s][u][1]), av);
+          const f4_t P = b8_mfma_exact(b8_halves(wr[s][u][0], wr[s][u][1]), av);
           const float m = f * __uint_as_float(sw[s][u]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[u][q] = fmaf(m, P[q], acc[u][q]);
