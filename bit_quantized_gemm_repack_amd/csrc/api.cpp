@@ -1283,6 +1283,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.s_expert = (int64_t)(p->meta_bytes_per_expert / 4);
       b.out_scale = out_scale;
       b.out_rows = (int)mp;
+      b.out_bf16 = p->layer.q.out == HQ_BF16;
       err = hipSuccess;
       if (!down) {
         hq::arm_timing(ev);
@@ -1292,7 +1293,6 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       const int64_t win = down ? b8_window(p, t, topk) : 1;
       b.rows16 = reinterpret_cast<int16_t*>(rows16);
       b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win) * 2));
-      b.out_bf16 = p->layer.q.out == HQ_BF16;
       for (int64_t c = 0; down && c < N && err == hipSuccess; c += win) {
         b.col0 = (int)c;
         b.ncol = (int)std::min(win, N - c);

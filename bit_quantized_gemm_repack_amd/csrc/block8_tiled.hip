@@ -69,6 +69,51 @@ __device__ __forceinline__ void b8_step(const uint8_t* at, const float* st, int 
 #endif
 }
 
+// The step of the gate_up GEMM, whose sums are quantised again: products through
+// fp16 (b8_mfma_exact).  The two weight fragments are converted once, each row
+// block as it comes; its promotion follows behind the next one's products.
+template <int MB>
+__device__ __forceinline__ void b8_step_exact(const uint8_t* at, const float* st, int c16, int kq, const u4_t (&b)[2][2],
+                                              const float (&sw)[2], f4_t (&acc)[MB][2]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  u4_t a[2][2];
+  float sa[2];
+  auto read = [&](int mb) {
+    a[mb & 1][0] = *reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, kq) * 16);
+    a[mb & 1][1] = *reinterpret_cast<const u4_t*>(at + mb * 2048 + swz<8>(c16, 4 + kq) * 16);
+    sa[mb & 1] = st[16 * mb];
+  };
+  f4_t P[2][2];
+  float f[2][2];
+  auto promote = [&](int mb) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[mb][u][q] = fmaf(f[mb & 1][u], P[mb & 1][u][q], acc[mb][u][q]);
+  };
+  read(0);
+  const B8Halves<4> w[2] = {b8_halves(b[0][0], b[0][1]), b8_halves(b[1][0], b[1][1])};
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    if (mb + 1 < MB) read(mb + 1);
+    const B8Halves<4> v = b8_halves(a[mb & 1][0], a[mb & 1][1]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      P[mb & 1][u] = f4_t{0.f, 0.f, 0.f, 0.f};
+      f[mb & 1][u] = sa[mb & 1] * sw[u];
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        P[mb & 1][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u].v[s], v.v[s], P[mb & 1][u], 0, 0, 0);
+    if (mb) promote(mb - 1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  promote(MB - 1);
+#endif
+}
+
 // Sixteen rows of 16 NB 16-bit values from the operand layout (lane (c16, kq),
 // fragment j: columns 16 j + 4 kq .. + 3 of row c16) to 16 bytes a lane, so
 // that a store instruction covers whole 64-byte runs of its rows; through the
@@ -162,15 +207,15 @@ __device__ inline int b8_block_rows(const B8Args& p, int m0, int bm, int lane) {
   return n;
 }
 
-// A workgroup of 4 waves computes BM = 16 MB rows by BN = 64 NB columns, each
-// wave all the rows and 16 NB columns, so that every weight is read once a
+// A workgroup of WV waves computes BM = 16 MB rows by BN = 16 NB WV columns,
+// each wave all the rows and 16 NB columns, so that every weight is read once a
 // tile, straight to registers.
-template <int MB, int NB, int ST>
+template <int MB, int NB, int ST, int WV = 4>
 struct B8Cfg {
-  static constexpr int WAVES = 4;
+  static constexpr int WAVES = WV;
   static constexpr int THREADS = 64 * WAVES;
   static constexpr int BM = 16 * MB;
-  static constexpr int BN = 64 * NB;
+  static constexpr int BN = 16 * NB * WV;
   static constexpr int NSEG = BM / 8;  // 1 KiB loads of the activation tile per step
   static constexpr int SEGW = NSEG > WAVES ? NSEG / WAVES : 1;
   static constexpr int SROWS = BM < 64 ? 64 : BM;  // row scales per step (whole 64-lane loads)
@@ -203,10 +248,10 @@ __device__ __forceinline__ bool b8_grouped_place(const B8Args& p, int bm, int& t
 }
 
 // One tile: rows m0 .. m0 + C::BM - 1, column tile tn.
-template <int MB, int NB, int ST, int MODE>
+template <int MB, int NB, int ST, int MODE, int WV = 4>
 __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using C = B8Cfg<MB, NB, ST>;
+  using C = B8Cfg<MB, NB, ST, WV>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c16 = lane & 15, kq = lane >> 4;
   const int wn = wave;
@@ -305,9 +350,12 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     float sw[NSW];
 #pragma unroll
     for (int u = 0; u < NSW; ++u) sw[u] = __uint_as_float(sraw[slot][u]);
-    b8_step<MB, NB, NSW>(lds + slot * C::STAGE + c16 * 128,
-                         reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + c16, c16, kq,
-                         braw[slot], sw, acc);
+    const uint8_t* at = lds + slot * C::STAGE + c16 * 128;
+    const float* st = reinterpret_cast<const float*>(lds + slot * C::STAGE + C::BM * 128) + c16;
+    if constexpr (MODE == B8_GATE_UP && NB == 2)
+      b8_step_exact<MB>(at, st, c16, kq, braw[slot], sw, acc);
+    else
+      b8_step<MB, NB, NSW>(at, st, c16, kq, braw[slot], sw, acc);
   };
 
   auto gclamp = [&](int g) { return g < Gl ? g : Gl - 1; };
@@ -341,8 +389,8 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
   // 4 kq .. 4 kq + 3 of each column block --------------------------------------
   if constexpr (MODE == B8_GATE_UP) {
     // one tile row holds the 128 outputs of one scale block: SiLU(gate) * up,
-    // its largest magnitude over the four column waves, the codes
-    uint32_t* red = reinterpret_cast<uint32_t*>(lds);  // [4][BM]
+    // its largest magnitude over the column waves, the codes
+    uint32_t* red = reinterpret_cast<uint32_t*>(lds);  // [WAVES][BM]
     __syncthreads();                              // every wave is done with the stage ring
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -363,7 +411,10 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       const int rl = 16 * mb + c16;
-      const float s = b8_scale(max(max(red[rl], red[C::BM + rl]), max(red[2 * C::BM + rl], red[3 * C::BM + rl])));
+      uint32_t top = 0u;
+#pragma unroll
+      for (int w = 0; w < C::WAVES; ++w) top = max(top, red[w * C::BM + rl]);
+      const float s = b8_scale(top);
       if (p.sorted_ids[m0 + rl] >= p.n_slots) continue;
       const int64_t row = m0 + rl;
       const B8Div d(s);
@@ -431,22 +482,27 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
 #endif
 }
 
+// gate_up through fp16 (EXACT) takes 8 waves of 16 gate and 16 up columns, one
+// workgroup a CU; otherwise 4 waves of twice as many, as the down GEMM.
+constexpr int b8_grouped_waves(bool exact) { return exact ? 8 : 4; }
+constexpr int b8_grouped_stages(int MB) { return MB <= 4 ? 3 : 2; }
+
 // A grouped tile of up to 16 MB rows: an aligned block is run with as many row
 // blocks (a power of two) as hold slots, so that the half-empty blocks that end
 // each expert's segment cost what they hold.
-template <int MB, int MODE>
+template <int MB, int MODE, bool EXACT>
 __device__ __forceinline__ void b8_grouped_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn, int rows) {
   if constexpr (MB > 1) {
     if (rows <= 8 * MB) {
-      b8_grouped_tile<MB / 2, MODE>(p, lds, m0, ex, tn, rows);
+      b8_grouped_tile<MB / 2, MODE, EXACT>(p, lds, m0, ex, tn, rows);
       return;
     }
   }
-  b8_tile<MB, 4, (MB <= 4 ? 3 : 2), MODE>(p, lds, m0, ex, tn);
+  b8_tile<MB, EXACT ? 2 : 4, b8_grouped_stages(MB), MODE, b8_grouped_waves(EXACT)>(p, lds, m0, ex, tn);
 }
 
-template <int MB, int MODE>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b8_grouped(B8Args p) {
+template <int MB, int MODE, bool EXACT>
+__global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((amdgpu_waves_per_eu(2))) b8_grouped(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int tm, tn;
@@ -458,7 +514,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
       b8_zero_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
     return;
   }
-  b8_grouped_tile<MB, MODE>(p, lds, m0, ex, tn, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+  b8_grouped_tile<MB, MODE, EXACT>(p, lds, m0, ex, tn, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
 #endif
 }
 
@@ -621,16 +677,28 @@ hipError_t dispatch_dense(const B8Tile& t, const B8Args& a, dim3 grid, hipStream
   return hipErrorInvalidValue;
 }
 
+template <int MB, int MODE, bool EXACT>
+hipError_t launch_grouped_k(const B8Args& a, dim3 grid, hipStream_t s) {
+  // the largest ring of the row counts a block may run with
+  constexpr int LOW = MB < 4 ? MB : 4, NB = EXACT ? 2 : 4, WV = b8_grouped_waves(EXACT);
+  constexpr size_t lds = std::max<size_t>(B8Cfg<MB, NB, b8_grouped_stages(MB), WV>::LDS, B8Cfg<LOW, NB, b8_grouped_stages(LOW), WV>::LDS);
+  const hipError_t e = allow_lds<b8_grouped<MB, MODE, EXACT>>(lds);
+  return e != hipSuccess ? e : launch_timed(b8_grouped<MB, MODE, EXACT>, grid, dim3(64 * WV), lds, s, a);
+}
+
 template <int MB>
 hipError_t launch_grouped(int mode, const B8Args& a, dim3 grid, hipStream_t s) {
-  // the largest ring of the row counts a block may run with
-  constexpr size_t lds = std::max<size_t>(B8Cfg<MB, 4, (MB <= 4 ? 3 : 2)>::LDS, B8Cfg<(MB < 4 ? MB : 4), 4, 3>::LDS);
-  if (mode == B8_GATE_UP) {
-    const hipError_t e = allow_lds<b8_grouped<MB, B8_GATE_UP>>(lds);
-    return e != hipSuccess ? e : launch_timed(b8_grouped<MB, B8_GATE_UP>, grid, dim3(256), lds, s, a);
-  }
-  const hipError_t e = allow_lds<b8_grouped<MB, B8_DOWN>>(lds);
-  return e != hipSuccess ? e : launch_timed(b8_grouped<MB, B8_DOWN>, grid, dim3(256), lds, s, a);
+  if (mode == B8_DOWN) return launch_grouped_k<MB, B8_DOWN, false>(a, grid, s);
+  // The sums of gate_up are quantised again, where what the fp8 instruction
+  // drops decides codes (b8_mfma_exact).  With up to 64 rows a block the
+  // weights' loads bound both forms (256 experts, top 8, H = 7168, I = 256: 509
+  // tokens 172 us through fp16 and 170 through fp8, 1024 208 and 194); with 128
+  // fp16 has half the rate (4096 tokens 381 and 277), for what an output of
+  // bf16, itself off by 1.7e-3, shows as 2.3e-3 at most, and one of fp16 as
+  // five times its rounding.
+  if constexpr (MB == 8)
+    if (a.out_bf16) return launch_grouped_k<MB, B8_GATE_UP, false>(a, grid, s);
+  return launch_grouped_k<MB, B8_GATE_UP, true>(a, grid, s);
 }
 
 constexpr int kShortLds = 72 * 1024;  // two workgroups a CU

@@ -564,6 +564,21 @@ def test_layer_dispatch_and_refusals():
         L.routed(x[:2], torch.randn(2, 8, device=DEV), 9)
 
 
+@pytest.mark.parametrize("t", [1, 5, 13, 40, 500, 1500])
+def test_layer_keeps_fp16(t):
+    """The intermediate is quantised to 4-bit significands, so that sums a little
+    off turn into other codes.  Where no code differs, fp16 outputs are off by
+    their own rounding, eps / 2 of each value at most: the root mean square over
+    all of them stays below that."""
+    L = Layer(20 + t, 16, 2048, 512, t, "f16")
+    x = _x(L.g, t, 2048, torch.float16)
+    ids, w = _routing(L.g, t, 16, 2)
+    y = L.run(x, ids, w).double()
+    torch.cuda.synchronize()
+    want = o8.layer(x.double(), ids.long(), w, L.w1, L.s1, L.w2, L.s2)[0]
+    assert ((y - want).pow(2).mean() / want.pow(2).mean()).sqrt() < torch.finfo(torch.float16).eps / 2
+
+
 def test_layer_odd_calls():
     """No tokens, slices of a batch that start anywhere, one token with an expert
     several times and ids outside the experts, codes where few tokens would run."""
