@@ -13,6 +13,7 @@
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
+#include <cmath>
 #include <new>
 #include <string>
 
@@ -1030,9 +1031,16 @@ static MoeChoice moe_choice(const hq_plan* p, int64_t t, int topk) {
     // blocks a little taller than what lands on an expert: a block is run with
     // as many rows as it holds, but one more block reads the weights again
     // (256 experts, top 8, H = 7168, I = 256, us a layer with 16 / 64 / 128-row
-    // blocks: 128 tokens 238 / 239 / 240, 509 370 / 318 / 345, 1024 560 / 393 /
-    // 415, 4096 1275 / 878 / 744)
-    c.bm = u.tile_m ? u.tile_m : (per_expert <= 6 ? 16 : (per_expert <= 64 ? 64 : 128));
+    // blocks: 128 tokens 230 / 234 / 233, 509 336 / 311 / 322, 1024 427 / 379 /
+    // 383, 2048 606 / 498 / 470) ...
+    c.bm = per_expert <= 6 ? 16 : (per_expert <= 64 ? 64 : 128);
+    // ... and lower ones where gate_up would leave CUs idle (16 experts, top 2, H
+    // = 4096, I = 512: 300 tokens 46.8 / 63.1 / 69.1, 700 66.0 / 68.2 / 77.7, 1500
+    // 116 / 84 / 87).  Both plans of a layer come to the same block.
+    const int64_t inter = p->compute.epi == HQ_EPI_TOPK_COMBINE ? p->layer.k : N / 2;
+    const double hit = std::min<double>(p->layer.num_experts, (double)t * topk);
+    while (c.bm > 16 && hit * std::ceil(per_expert / c.bm) * (double)(inter / 128) < 150) c.bm = c.bm == 128 ? 64 : 16;
+    if (u.tile_m) c.bm = u.tile_m;
     c.tl.bm = c.bm;
     c.tl.nbw = 4;
     c.tl.split = 1;
@@ -1156,7 +1164,9 @@ static int64_t moe_down_cols(const hq_plan* p, int64_t t, int topk, int bm) {
 }
 
 // Columns of a down launch of fp8 block layers: windows whose slot rows fit the
-// last-level cache, so that the sum reads them from there.
+// last-level cache, so that the sum reads them from there and the workspace
+// stays small (4096 tokens, top 8, H = 7168: windows of 60 / 120 / 160 / 240 MiB
+// 424 / 355 / 328 / 311 us, one of 448 309).
 static constexpr int64_t kB8WindowBytes = int64_t(240) << 20;
 
 static int64_t b8_window(const hq_plan* p, int64_t t, int topk) {

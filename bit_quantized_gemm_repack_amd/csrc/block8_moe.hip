@@ -8,10 +8,17 @@
 //
 // Both GEMMs are bound by reading the chosen experts' weights, which every
 // workgroup streams straight to registers; tokens that picked the same expert
-// share one read (they are the columns of the matrix instruction).  The expert
-// a slot stands for is found inside the kernels: a workgroup row per slot
-// takes its token's j-th best logit, and the slots that share its expert are
-// found by counting, per token, the logits that come before the expert's.
+// share one read (they are the columns of the matrix instruction).  One token's
+// expert is found inside the kernel: a workgroup row per slot takes the j-th
+// best logit.  More tokens are routed by the routing kernel first: counting the
+// slots of an expert from the logits in every workgroup took 9 us of 8 tokens'
+// 76, the launch takes 4.
+//
+// 256 experts, top 8, H = 7168, I = 256, in a graph, and the experts' bytes over
+// a streaming read's 6 TB/s: 1 token 17.3 us (7.3), 2 29 (15), 4 45 (28), 8 67
+// (49), 13 92 (71), 16 102 (80); 24 tokens 154, where the aligned path takes 128.
+// About 9 us are the two kernels' launches and their chains of dependent loads
+// (ids, weights); the rest runs at 5.6 TB/s.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -118,7 +125,8 @@ struct Logits {
   }
 };
 
-// One wave per token.
+// One wave per token: the chain of a choice is short (a maximum over 64 lanes),
+// 3.6 us for one token of 256 experts.
 template <int NPL>
 __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ logits, int lt, int t, int E, int topk,
                                                     int renorm, int32_t* __restrict__ ids, float* __restrict__ w) {
@@ -164,7 +172,8 @@ __device__ inline float row_sum(float v) {
 // Sixteen lanes per token, for many tokens: a choice costs the wave one maximum
 // over 16 lanes for four tokens.  Lane l keeps experts l, l + 16, ...  16-bit
 // logits carry their expert in the key's low half (the lower the larger), which
-// makes the keys unique and a choice one comparison per key.
+// makes the keys unique and a choice one comparison per key.  Bound by
+// instructions: 16383 x 160 bf16 top 6, 7 us (a wave per token 12), 6 MB.
 template <int LT, int NPL>
 __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict__ logits, int t, int E, int topk, int renorm,
                                                          int32_t* __restrict__ ids, float* __restrict__ w) {
@@ -259,12 +268,14 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict_
 // gate_up.  A workgroup row per slot; the first of the slots that share an
 // expert does the work for all of them.  Two shapes:
 //   narrow  16 outputs a workgroup, its waves share K (their sums meet in
-//           LDS); the fp32 rows are quantised by the down kernel.  For one or
-//           two tokens, whose few experts would leave most CUs idle otherwise.
+//           LDS); the fp32 rows are quantised by the down kernel.  For up to 8
+//           tokens, whose few experts would leave most CUs idle otherwise: one
+//           token 12 us with 8 waves and all of a wave's loads in flight at
+//           once, more with 4.
 //   wide    128 outputs a workgroup, 16 a wave over all of K: no sums to join,
 //           and the workgroup holds a whole scale block, so that it writes
-//           codes and scales.  The routing above the stream is paid an eighth
-//           as often.
+//           codes and scales.  13 tokens 57 us, 5.5 TB/s.
+// The products go through fp16 (b8_mfma_exact): their sums are quantised again.
 // One more row of workgroups writes the routing where there are logits, and
 // otherwise the units that the down kernel walks.
 // ---------------------------------------------------------------------------
@@ -571,7 +582,8 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
 // ---------------------------------------------------------------------------
 // down + combine: grid (16-column blocks, tiles of 16 tokens).  The tile's
 // activation rows lie quantised in LDS (as many 128-k groups at a time as
-// fit); the waves take the (expert, group) steps in turn.
+// fit); the waves take the (expert, group) steps in turn.  One token 6.0 us
+// (14.7 MB), 13 tokens 32 us (141 MB).
 // ---------------------------------------------------------------------------
 template <bool WIDE, bool ONE, int ST>
 __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(4))) few_down(B8FewArgs p) {

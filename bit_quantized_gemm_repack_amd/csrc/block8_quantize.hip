@@ -8,7 +8,9 @@
 // lanes hold a block (8 values, one 16-byte load each), so the maximum is
 // four rotations within the lanes' row; consecutive sixteens take consecutive
 // rows of one block column, so that their scales, stored [k/128][m], are
-// consecutive words.
+// consecutive words.  One token of 7168: 2.2 us, a launch; SiLU of 8191 x 2048,
+// 84 MB: 22.4 us a call, 3.7 TB/s (a large copy reaches 4.9); 4096 x 7168, 88
+// MB: 19.5 us, 4.5 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -220,7 +220,9 @@ typedef struct hq_compute {
  * Zero in any field means "let the heuristic choose". */
 typedef struct hq_tuning {
   int kernel;  /* 0 auto, 1 skinny (small M, split-K), 2 tiled (large M)  */
-  int tile_m;  /* skinny: rows per workgroup (16, 32, 64); tiled: 64 or 128     */
+  int tile_m;  /* skinny: rows per workgroup (16, 32, 64); tiled: 64 or 128
+                  (W8A8-BLOCK: skinny 16; tiled 16, 32, 64 or 128; grouped:
+                  aligned blocks of 16, 64 or 128 rows)                    */
   int tile_n;  /* skinny: columns per workgroup (16, 32, 64); tiled: 128, 256 */
   int waves;   /* wavefronts per workgroup                                 */
   int split_k; /* workgroups sharing one output tile along K (dense)     */
@@ -408,7 +410,7 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  * (TOPK_COMBINE only).  Rows of padding slots (and, for gate_up, of slots
  * with an out-of-range expert id) are left unwritten.  ws: the workspace of
  * hq_moe_workspace_bytes (the fp8 requant's fp32 rows, or the combine's
- * t*topk weighted bf16 slot rows); every call writes what it reads, so its
+ * t*topk slot rows); every call writes what it reads, so its
  * contents need no initialisation and no state carries over between calls
  * (two calls that overlap in time must not share one workspace).  As for
  * hq_gemm, activations or one expert's weights of 2 GiB or more are
@@ -458,24 +460,28 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* plan, int64_t t, int topk, const vo
  * others ends in ids of -1 with weight 0.  A logit of +inf gives unspecified
  * weights.  topk_ids int32 and topk_w fp32 [t, topk], fully overwritten, as
  * hq_moe_align / hq_moe_gemm take them.  num_experts <= 1024, topk <= 64,
- * t <= 2^24; t = 0 is a no-op.  Honours hq_time_next_launch (one kernel). */
+ * t <= 2^24; t = 0 is a no-op.  The three are aligned to their elements (slices
+ * of a batch may start at any row).  Honours hq_time_next_launch (one kernel). */
 hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, int renormalize,
                         int32_t* topk_ids, float* topk_w, void* stream);
 
 /* A whole experts' layer of fp8 weights with block scales (W8A8-BLOCK plans:
  * gate_up [2 I, H] with SILU_MUL_QFP8, down [H, I] with TOPK_COMBINE, the same
- * experts) for a few tokens, in two kernels: routing, the block quantisation
- * of x, gate_up and SiLU * mul in the first; the block quantisation of the
- * activation, down and the top-k sum in the second.
+ * experts) for a few tokens, in two kernels: the block quantisation of x,
+ * gate_up and SiLU * mul in the first; the block quantisation of the activation,
+ * down and the top-k sum in the second.  One token's routing is part of the
+ * first; more tokens' is a kernel of its own before it.
  *   x         device [t, H] fp16 / bf16 (x_type)
  *   logits    device [t, num_experts]: topk_ids and topk_w (device [t, topk])
  *             are outputs, as hq_route_topk writes them; or NULL: they are
  *             inputs (ids outside [0, num_experts) contribute zero, an id may
  *             come twice in a row)
  *   out       device [t, H] in the down plan's out dtype
- *   ws        hq_moe_few_workspace_bytes bytes; holds the fp32 activations
- *             [t * topk, I] between the kernels, no initialisation needed; two
- *             calls that overlap in time must not share one
+ *   ws        hq_moe_few_workspace_bytes bytes; holds the activations [t * topk,
+ *             I] and the slots by expert between the kernels, no initialisation
+ *             needed; two calls that overlap in time must not share one
+ * logits, topk_ids and topk_w are aligned to their elements, the others to 16
+ * bytes.
  * The activations are rounded where hq_quantize_blocks and the grouped gate_up
  * round them, and the sum over a token's experts is one fp32 accumulator
  * rounded once.  Deterministic.  t <= 64, topk <= 16, num_experts <= 4096

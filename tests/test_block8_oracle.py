@@ -269,3 +269,16 @@ def test_binding_refuses_cpu_tensors():
         p.repack_host(torch.zeros(256, 512, dtype=torch.uint8), torch.zeros(2, 3))   # scales of another shape
     with pytest.raises(ValueError):
         p.repack_host(torch.zeros(256, 256, dtype=torch.uint8), torch.zeros(2, 4))
+
+
+def test_layer_plans_share_blocks():
+    """gate_up and down come to one alignment block for every call of a layer."""
+    q = hq.w8a8_block()
+    seen = set()
+    for e, h, i in ((8, 512, 128), (16, 4096, 512), (32, 2048, 768), (256, 7168, 256), (2, 256, 1024)):
+        g, d = hq.MoePlan(2 * i, h, q, e, 8192, "silu_mul_qfp8"), hq.MoePlan(h, i, q, e, 8192, "topk_combine")
+        for t in (1, 2, 17, 24, 100, 300, 700, 1500, 4096, 8192):
+            for k in (1, 2, 8):
+                assert g.block_m(t, k) == d.block_m(t, k)
+                seen.add(g.block_m(t, k))
+    assert seen == {16, 64, 128}
