@@ -178,8 +178,10 @@ def test_grouped_plans_refused():
     for t in (dict(kernel=1), dict(tile_m=32), dict(tile_n=128), dict(tile_m=48)):
         with pytest.raises(hq.HQError):
             hq.MoePlan(512, 256, q, 4, 8, "silu_mul_qfp8", tuning=t)
+    g = hq.MoePlan(512, 256, q, 256, 4096, "silu_mul_qfp8")  # blocks by rows per expert, where there are plenty
+    assert g.block_m(64, 8) == 16 and g.block_m(1024, 8) == 64 and g.block_m(4096, 8) == 128
     g = hq.MoePlan(512, 256, q, 4, 64, "silu_mul_qfp8")
-    assert g.block_m(1, 2) == 16 and g.block_m(64, 2) == 64 and g.block_m(64, 64) == 128
+    assert g.block_m(1, 2) == 16 and g.block_m(64, 64) == 16  # few workgroups: low blocks
     L = hq.lib()
     assert L.hq_moe_gemm_by_slot(g._h, 1, 1, *[FAKE] * 9, 1 << 30, None) == hq.HQ_ERR_UNSUPPORTED
 
