@@ -16,6 +16,7 @@ Quick use::
 from __future__ import annotations
 
 import ctypes
+import importlib
 import json
 import os
 import re
@@ -26,6 +27,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhq.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "hq.h")
 
 # ------------------------------------------------------------------ enums --
@@ -253,7 +255,24 @@ def lib():
             f.restype = res
             f.argtypes = args
         _lib = L
+        _bind_calls(L)
     return _lib
+
+
+# The native form of the short calls (csrc/binding/calls.cpp), once the library
+# is loaded and if it is built; it answers None to anything but the ordinary
+# call, which the Python below then checks.
+_calls = None
+
+
+def _bind_calls(L):
+    global _calls
+    if not os.path.exists(CALLS_PATH):
+        return
+    native = importlib.import_module("._calls", __package__)
+    native.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes)))
+    _calls = native
 
 
 def header_functions(path: str = HEADER_PATH):
@@ -478,6 +497,10 @@ class Plan:
              out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
         """out[m, n] = A . W_deq^T (see include/hq.h, hq_gemm)."""
         if self._block8:
+            if _calls is not None and out is None and ws is None:
+                r = _calls.gemm_block(self._h.value, self.n, self.k, self.quant.out == BF16, a, a_scale, w, meta)
+                if r is not None:
+                    return r
             return self._gemm_block(a, w, meta, a_scale, out, ws)
         _dev(a, "a"), _dev(w, "w"), _dev(meta, "meta")
         act4 = self.quant.act == FP4_E2M1
@@ -729,6 +752,10 @@ def quantize_blocks(x: torch.Tensor, silu_mul: bool = False, codes: Optional[tor
     a gate_up GEMM, of which SiLU(x[:, :k]) * x[:, k:] is quantised.  Returns
     (codes uint8 [m, k], scales float32 [k/128, m]), the (a, a_scale) of a
     w8a8_block GEMM."""
+    if _calls is not None and codes is None and scales is None:
+        r = _calls.quantize_blocks(x, silu_mul)
+        if r is not None:
+            return r
     _dev(x, "x")
     if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("x must be fp16 / bf16 [m, k]")
@@ -946,6 +973,10 @@ def route_topk(logits: torch.Tensor, topk: int, renormalize: bool = True):
     """The topk experts of each row of logits [t, experts] (fp32, fp16 or bf16)
     and their softmax weights (see hq_route_topk): (ids int32 [t, topk],
     weights float32 [t, topk]), the (topk_ids, topk_w) of moe_layer."""
+    if _calls is not None:
+        r = _calls.route_topk(logits, topk, renormalize)
+        if r is not None:
+            return r
     _dev(logits, "logits")
     if logits.dim() != 2 or logits.dtype not in _LOGITS:
         raise ValueError("logits must be fp32 / fp16 / bf16 [t, experts]")

@@ -1,4 +1,5 @@
-"""Build the HIP library (libhq.so) in-tree for gfx950 with hipcc.
+"""Build the HIP library (libhq.so) in-tree for gfx950 with hipcc, and the
+binding's native calls (_calls.so) with g++.
 
 Every source is compiled to an object in parallel, then linked into
 ``bit_quantized_gemm_repack_amd/libhq.so``.  HIP device code is built with
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhq.so")
+CALLS = os.path.join(PKG, "_calls.so")
 ARCH = os.environ.get("HQ_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -45,11 +47,35 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_calls() -> str:
+    """The binding's native short calls (csrc/binding/calls.cpp), host code
+    against the installed torch."""
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding", "calls.cpp"), "-o", tmp,
+           "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(_compile, srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, *DEVICE, "-shared", "-fPIC", "-o", tmp, *objs, *LINK]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -57,7 +83,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}", file=sys.stderr)
+        print(f"built {LIB} and {CALLS}", file=sys.stderr)
     return LIB
 
 

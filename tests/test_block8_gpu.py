@@ -644,6 +644,36 @@ def test_quantize_beyond_32_bits():
     assert (s[:, 1:m // 2] == 1).all()
 
 
+def test_native_calls_are_the_same(monkeypatch):
+    """The binding's native short calls against the same calls through ctypes, on
+    another stream too; what they do not take goes through ctypes."""
+    x = _x(_gen(30), 9, 1024, torch.bfloat16)
+    h = _x(_gen(31), 9, 2048, torch.float16)
+    lg = _logits(_gen(32), 9, 40, torch.float32)
+    w, sw = _w(_gen(33), 272, 1024)
+    plan = hq.Plan(272, 1024, hq.w8a8_block(), max_m=16, tuning=dict(kernel=1, split_k=2))
+    wm = plan.repack(_codes(w), sw)
+    a, s = hq.quantize_blocks(x)
+
+    def calls():
+        return [*hq.quantize_blocks(x), *hq.quantize_blocks(h, silu_mul=True), *hq.route_topk(lg, 4), *hq.route_topk(lg, 2, False),
+                plan.gemm(a, *wm, a_scale=s), *hq.quantize_blocks(x[:0]), *hq.route_topk(lg[:0], 3)]
+    assert hq._calls is not None
+    native = calls()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        other = calls()
+    torch.cuda.synchronize()
+    assert hq._calls.quantize_blocks(x.t(), False) is None and hq._calls.route_topk(lg, 41, True) is None
+    assert hq._calls.gemm_block(plan._h.value, 272, 1024, True, a, s.double(), *wm) is None
+    assert hq._calls.gemm_block(plan._h.value, 272, 1024, True, a, None, *wm) is None
+    monkeypatch.setattr(hq, "_calls", None)
+    plain = calls()
+    torch.cuda.synchronize()
+    for p, q, r in zip(native, other, plain):
+        assert p.dtype == r.dtype and p.shape == r.shape and torch.equal(p, r) and torch.equal(q, r)
+
+
 # ------------------------------------------------------------ streams, graphs --
 def test_graph_of_everything():
     """Quantise, split-K GEMM, routing and both layers in one graph: every replay

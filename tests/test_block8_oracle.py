@@ -284,3 +284,20 @@ def test_layer_plans_share_blocks():
                 assert g.block_m(t, k) == d.block_m(t, k)
                 seen.add(g.block_m(t, k))
     assert seen == {16, 64, 128}
+
+
+def test_native_calls_take_nothing_else():
+    """What is no GPU tensor of the right kind is left to the Python checks."""
+    hq.lib()
+    if hq._calls is None:
+        pytest.skip("the native calls are not built")
+    x = torch.zeros(2, 256, dtype=torch.bfloat16)
+    for args in ((), (x,), (None, False), (x, False), (x.float(), True), ("x", 1)):
+        assert hq._calls.quantize_blocks(*args) is None
+    for args in ((x, 2, True), (x, "2", True), (x, 1 << 70, True), (3, 2, True), (x, 2)):
+        assert hq._calls.route_topk(*args) is None
+    assert hq._calls.gemm_block(0, 16, 128, True, x, x, x, x) is None and hq._calls.gemm_block() is None
+    with pytest.raises(TypeError):
+        hq._calls.bind(1, 2)
+    with pytest.raises(ValueError):
+        hq.quantize_blocks(x)
