@@ -328,18 +328,28 @@ __device__ inline int few_expert(const B8FewArgs& p, int z, int lane) {
   return __builtin_amdgcn_readfirstlane(e);
 }
 
+// The ids a wave's lanes scan for an expert's slots, the first kScan of them in
+// flight before the expert is known.
+constexpr int kScan = 4;
+__device__ inline void few_ids(const B8FewArgs& p, int (&ids)[kScan], int lane) {
+#pragma unroll
+  for (int i = 0; i < kScan; ++i) ids[i] = p.topk_ids[min(64 * i + lane, p.t * p.topk - 1)];
+}
+
 // The slots that hold expert e, in order, into picks; returns how many.  Ends
 // with a barrier.
-__device__ inline int few_slots(const B8FewArgs& p, int e, int* picks, int* npicks, int lane, int wave) {
+__device__ inline int few_slots(const B8FewArgs& p, int e, const int (&ids)[kScan], int* picks, int* npicks, int lane, int wave) {
   if (wave == 0) {
     int n = 0;
-    for (int b = 0; b < p.t * p.topk; b += 64) {
-      const int s = b + lane;
-      const bool hit = s < p.t * p.topk && p.topk_ids[s] == e;
+    auto scan = [&](int b, int id) {
+      const bool hit = b + lane < p.t * p.topk && id == e;
       const uint64_t has = __ballot(hit);
-      if (hit) picks[n + __popcll(has & ((1ull << lane) - 1))] = s;
+      if (hit) picks[n + __popcll(has & ((1ull << lane) - 1))] = b + lane;
       n += __popcll(has);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) scan(64 * i, ids[i]);
+    for (int b = 64 * kScan; b < p.t * p.topk; b += 64) scan(b, p.topk_ids[min(b + lane, p.t * p.topk - 1)]);
     if (lane == 0) *npicks = n;
   }
   __syncthreads();
@@ -450,6 +460,8 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
     const int g = min((tid >> 4) + 4 * NW * u, G - 1);
     xr[u] = static_cast<const u4_t*>(p.x)[(int64_t)(z / p.topk) * (K / 8) + g * 16 + c16];
   }
+  int ids[kScan] = {};
+  if (!p.logits && wave == 0) few_ids(p, ids, lane);
   const int e = few_expert<NPL>(p, z, lane);
   if (e < 0) return;
 
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
   if (p.logits) {  // one token, whose experts differ
     if (tid == 0) picks[0] = z;
   } else {
-    n = few_slots(p, e, picks, &npicks, lane, wave);
+    n = few_slots(p, e, ids, picks, &npicks, lane, wave);
     if (picks[0] != z) return;
   }
 
