@@ -4,7 +4,8 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI declared in ``include/hq.h``.  PyTorch supplies the
 device memory (tensors) and the stream (the current HIP stream); there is no
 CPU fallback, and every entry point raises if the library is not built or a
-tensor is not on the GPU.
+tensor is not on the GPU.  The short calls of the fp8 block layers go through
+native code where it is built (csrc/binding/calls.cpp).
 
 Quick use::
 
