@@ -770,6 +770,7 @@ int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits,
     auto go = [&]<int LT>() -> int {
       if (E <= 64) return (int)launch_timed(route_rows_kernel<LT, 4>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
       if (E <= 128) return (int)launch_timed(route_rows_kernel<LT, 8>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
+      if (E <= 192) return (int)launch_timed(route_rows_kernel<LT, 12>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
       return (int)launch_timed(route_rows_kernel<LT, 16>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);
     };
     return logit_type == 0 ? go.template operator()<0>() : (logit_type == 1 ? go.template operator()<1>() : go.template operator()<2>());
