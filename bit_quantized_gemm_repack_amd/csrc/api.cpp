@@ -249,14 +249,9 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
     // half a CU and K is long (N = 4096, one row: 9.0 against 9.5 us; N = 14336:
     // two 14.0, one 25; K = 2048, N = 512, 16 rows: two 4.4, one 4.8)
     c.nb = (mm <= 16 ? n16 < 384 : blocks <= 200) && G > 16 ? 1 : 2;
-    // a narrow N with long K leaves the chip idle and its waves two rings deep:
-    // two column blocks and four splits of K, the reduce included (33 rows of
-    // (576, 7168) 7.4 against 8.1 us, 16 of (1024, 7168) 7.4 against 8.0; up to 8
-    // rows 6.6 against 6.2, and with K = 4096 6.6 against 5.5)
-    if (mm > 8 && G >= 48 && cdiv(n16, 2) * cdiv(mm, 16) * 4 <= 256 && !u.tile_n && !u.waves && !u.split_k) {
-      c.nb = 2;
-      split = 4;
-    }
+    // (A narrow N with long K would gain from four splits in a graph, 33 rows of
+    // (576, 7168) 7.4 against 8.1 us, and lose launched one by one, 9.1 against
+    // 7.4: left to tuning.)
     c.waves = 4;  // (8: 10.1 against 9.0 us at N = 4096, K = 7168)
     c.stages = 1;
     if (u.tile_m) c.mb = u.tile_m / 16;
