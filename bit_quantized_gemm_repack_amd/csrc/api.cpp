@@ -1297,6 +1297,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.out_scale = out_scale;
       b.out_rows = (int)mp;
       b.out_bf16 = p->layer.q.out == HQ_BF16;
+      b.once = 2 * t * topk <= (int64_t)bm * p->layer.num_experts;
       err = hipSuccess;
       if (!down) {
         hq::arm_timing(ev);

@@ -36,6 +36,7 @@ struct B8Args {
   const int32_t* block_expert;
   const int32_t* num_padded;
   const float* topk_w;
+  int once;                // most experts' rows lie in one block
   int topk, n_slots;
   int64_t w_expert;        // code bytes per expert
   int64_t s_expert;        // weight scales per expert

@@ -56,6 +56,10 @@ __device__ inline uint32_t b8_mag(float v) { return __float_as_uint(v) & 0x7FFFF
 
 __device__ inline float b8_silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
+// Cache policy of a buffer load of what is read once: it leaves the caches as
+// they are.
+constexpr int kReadOnce = 2;
+
 // Codes as fp16 values (exact), eight from two words: the operand of a 16 x 16 x
 // 32 fp16 matrix instruction.
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));

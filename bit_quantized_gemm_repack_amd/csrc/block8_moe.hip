@@ -17,6 +17,8 @@
 // 256 experts, top 8, H = 7168, I = 256, in a graph, and the experts' bytes over
 // a streaming read's 6 TB/s: 1 token 17.3 us (7.3), 2 29 (15), 4 45 (28), 8 67
 // (49), 13 92 (71), 16 102 (80); 24 tokens 154, where the aligned path takes 128.
+// More than one token's weights are read past the caches (4 tokens 42 us against
+// 45, 13 88.6 against 93); one token's may stay there (17.3 against 18.4).
 // About 9 us are the two kernels' launches and their chains of dependent loads
 // (ids, weights); the rest runs at 5.6 TB/s.
 #include <hip/hip_ext.h>
@@ -470,6 +472,7 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
   const int gs = WIDE ? 0 : wave, gd = WIDE ? 1 : NW;  // groups gs, gs + gd, ...
   const auto rw = few_rsrc(p.w1 + (int64_t)e * p.w1_expert, p.w1_expert);
   const auto rws = few_rsrc(p.s1 + (int64_t)e * p.s1_expert, p.s1_expert * 4);
+  constexpr int AUX = WIDE || NW == 4 ? kReadOnce : 0;  // more than one token
   u4_t wr[ST][2][2];
   uint32_t sw[ST][2];
   auto issue = [&](int slot, int g) {
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         wr[slot][u][h] = __builtin_bit_cast(
-            u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (lane * 16 + 1024 * h) | past, (nb * G + g) * 2048, 0));
+            u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (lane * 16 + 1024 * h) | past, (nb * G + g) * 2048, AUX));
       sw[slot][u] = __builtin_amdgcn_raw_buffer_load_b32(rws, past, ((nb / 8) * G + g) * 4, 0);
     }
   };
@@ -628,6 +631,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
 
   const int gmax = p.down_groups, pitch = gmax * 128 + 16;
   float* sc = reinterpret_cast<float*>(lds + ns * pitch);  // [ns][gmax]
+  constexpr int AUX = ONE ? 0 : kReadOnce;
   u4_t wr[ST][2];
   uint32_t sw[ST];
   f4_t acc = f4_t{0.f, 0.f, 0.f, 0.f};
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_pe
       const auto rs = few_rsrc(p.s2 + (int64_t)e * p.s2_expert, in ? p.s2_expert * 4 : 0);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        wr[slot][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + 1024 * h, (nb * G + g) * 2048, 0));
+        wr[slot][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + 1024 * h, (nb * G + g) * 2048, AUX));
       sw[slot] = __builtin_amdgcn_raw_buffer_load_b32(rs, 0, ((nb / 8) * G + g) * 4, 0);
       next(ahead);
     };

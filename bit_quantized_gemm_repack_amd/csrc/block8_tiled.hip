@@ -255,7 +255,7 @@ __device__ __forceinline__ bool b8_grouped_place(const B8Args& p, int bm, int& t
 }
 
 // One tile: rows m0 .. m0 + C::BM - 1, column tile tn.
-template <int MB, int NB, int ST, int MODE, int WV = 4>
+template <int MB, int NB, int ST, int MODE, int WV = 4, bool ONCE = false>
 __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using C = B8Cfg<MB, NB, ST, WV>;
@@ -341,7 +341,7 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         braw[slot][j][h] =
-            __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, woff + 1024 * h, wsc_off[j] + gg * 2048, 0));
+            __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, woff + 1024 * h, wsc_off[j] + gg * 2048, ONCE ? kReadOnce : 0));
 #pragma unroll
     for (int u = 0; u < NSW; ++u) sraw[slot][u] = __builtin_amdgcn_raw_buffer_load_b32(rws, 0, swoff[u] + gg * 4, 0);
   };
@@ -497,18 +497,18 @@ constexpr int b8_grouped_stages(int MB) { return MB <= 4 ? 3 : 2; }
 // A grouped tile of up to 16 MB rows: an aligned block is run with as many row
 // blocks (a power of two) as hold slots, so that the half-empty blocks that end
 // each expert's segment cost what they hold.
-template <int MB, int MODE, bool EXACT>
+template <int MB, int MODE, bool EXACT, bool ONCE>
 __device__ __forceinline__ void b8_grouped_tile(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int tn, int rows) {
   if constexpr (MB > 1) {
     if (rows <= 8 * MB) {
-      b8_grouped_tile<MB / 2, MODE, EXACT>(p, lds, m0, ex, tn, rows);
+      b8_grouped_tile<MB / 2, MODE, EXACT, ONCE>(p, lds, m0, ex, tn, rows);
       return;
     }
   }
-  b8_tile<MB, EXACT ? 2 : 4, b8_grouped_stages(MB), MODE, b8_grouped_waves(EXACT)>(p, lds, m0, ex, tn);
+  b8_tile<MB, EXACT ? 2 : 4, b8_grouped_stages(MB), MODE, b8_grouped_waves(EXACT), ONCE>(p, lds, m0, ex, tn);
 }
 
-template <int MB, int MODE, bool EXACT>
+template <int MB, int MODE, bool EXACT, bool ONCE>
 __global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((amdgpu_waves_per_eu(2))) b8_grouped(B8Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((a
       b8_zero_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
     return;
   }
-  b8_grouped_tile<MB, MODE, EXACT>(p, lds, m0, ex, tn, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+  b8_grouped_tile<MB, MODE, EXACT, ONCE>(p, lds, m0, ex, tn, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
 #endif
 }
 
@@ -687,13 +687,13 @@ hipError_t dispatch_dense(const B8Tile& t, const B8Args& a, dim3 grid, hipStream
   return hipErrorInvalidValue;
 }
 
-template <int MB, int MODE, bool EXACT>
+template <int MB, int MODE, bool EXACT, bool ONCE = false>
 hipError_t launch_grouped_k(const B8Args& a, dim3 grid, hipStream_t s) {
   // the largest ring of the row counts a block may run with
   constexpr int LOW = MB < 4 ? MB : 4, NB = EXACT ? 2 : 4, WV = b8_grouped_waves(EXACT);
   constexpr size_t lds = std::max<size_t>(B8Cfg<MB, NB, b8_grouped_stages(MB), WV>::LDS, B8Cfg<LOW, NB, b8_grouped_stages(LOW), WV>::LDS);
-  const hipError_t e = allow_lds<b8_grouped<MB, MODE, EXACT>>(lds);
-  return e != hipSuccess ? e : launch_timed(b8_grouped<MB, MODE, EXACT>, grid, dim3(64 * WV), lds, s, a);
+  const hipError_t e = allow_lds<b8_grouped<MB, MODE, EXACT, ONCE>>(lds);
+  return e != hipSuccess ? e : launch_timed(b8_grouped<MB, MODE, EXACT, ONCE>, grid, dim3(64 * WV), lds, s, a);
 }
 
 template <int MB>
@@ -708,6 +708,11 @@ hipError_t launch_grouped(int mode, const B8Args& a, dim3 grid, hipStream_t s) {
   // five times its rounding.
   if constexpr (MB == 8)
     if (a.out_bf16) return launch_grouped_k<MB, B8_GATE_UP, false>(a, grid, s);
+  // Weights that one block reads go past the caches (509 tokens of 256 experts
+  // 161 us against 179); where blocks share an expert they stay (700 tokens of 16
+  // experts in 16-row blocks 38 us, past the caches 59).
+  if constexpr (MB <= 4)
+    if (a.once) return launch_grouped_k<MB, B8_GATE_UP, true, true>(a, grid, s);
   return launch_grouped_k<MB, B8_GATE_UP, true>(a, grid, s);
 }
 
