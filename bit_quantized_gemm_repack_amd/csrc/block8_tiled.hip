@@ -12,7 +12,7 @@
 // 53): the operand reads from LDS beside the matrix and vector instructions, and
 // the clock, which the same product of zeros keeps higher (88 us).  200 x 14336
 // x 4096 takes 22.6 us: without its loads 17, without its products 21.  Up to 64
-// rows an expert the grouped products read weights at 5.1 .. 5.6 TB/s.
+// rows an expert the grouped products read weights at 5.0 .. 5.8 TB/s.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((a
 // barrier and no refill between tiles (with two or four groups of K per tile
 // the loads' latency at each tile's start would cost as much as its math).
 // 256 experts, top 8, H = 7168, I = 256: 509 tokens 105 us (470 MB of weights and
-// 58 of rows, 5.0 TB/s), 4096 tokens two windows of 117 us (5 TB/s).
+// 58 of rows, 5.0 TB/s), 4096 tokens two windows of 115 us (5 TB/s).
 template <int MB>
 __device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int c0, int c1) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
 
 // y[t][col0 + c] = RNE(sum over the token's topk slots of q * scale), in slot
 // order; eight columns a thread.  Bound by reading the rows: a window of 4096
-// tokens, 235 MB, 42 us, 6.3 TB/s with its output.  The rows are done with once
+// tokens, 235 MB, 43 us, 6.1 TB/s with its output.  The rows are done with once
 // read: loads that do not keep them leave the cache to the next window's (a layer
 // of 4096 tokens 648 us against 661).
 __global__ void __launch_bounds__(256) b8_combine_kernel(const u4_t* __restrict__ rows, const float* __restrict__ scale,
