@@ -420,6 +420,19 @@ def test_grouped_stages(t, e, topk, h, i, bm):
         assert (y[3] == 0).all()
 
 
+@pytest.mark.parametrize("bm", [16, 64, 128])
+@pytest.mark.parametrize("t", [1, 90, 700])
+def test_grouped_fp16(t, bm):
+    """fp16 layers on every block, alone and shared by an expert's rows."""
+    L = Layer(40 + t, 5, 640, 384, t, "f16", tuning=dict(tile_m=bm))
+    x = _x(L.g, t, 640, torch.float16)
+    ids, w = _routing(L.g, t, 5, 2)
+    q, s = hq.quantize_blocks(x)
+    y = L.run(q, ids, w, x_scale=s)
+    torch.cuda.synchronize()
+    L.check(y, x, ids, w, f"block {bm}", ROW_ERR)
+
+
 def test_grouped_windows(monkeypatch):
     """Enough slots for two column windows of the down GEMM (240 MiB of rows)."""
     t, e, topk, h, i = 9000, 8, 8, 2048, 128
