@@ -998,6 +998,19 @@ def _uses_few(gate_up: "MoePlan", t: int, topk: int) -> bool:
     return gate_up._block8 and 0 < t <= MOE_FEW_MAX_TOKENS and topk <= 16 and gate_up.k <= 98304
 
 
+def _check_layer_plans(gate_up: "MoePlan", down: "MoePlan"):
+    """Both plans of a layer index one set of experts, and down takes gate_up's
+    rows: a plan of another shape would read past its weights."""
+    if down.epi != EPI_TOPK_COMBINE or gate_up.epi not in (EPI_SILU_MUL, EPI_SILU_MUL_QFP8):
+        raise ValueError("moe_layer takes a gate_up plan (silu_mul / silu_mul_qfp8) and a topk_combine plan")
+    if gate_up._block8 != down._block8:
+        raise ValueError("gate_up and down must both be w8a8_block plans, or neither")
+    if down.num_experts < gate_up.num_experts or (gate_up._block8 and down.num_experts != gate_up.num_experts):
+        raise ValueError(f"gate_up has {gate_up.num_experts} experts, down {down.num_experts}")
+    if gate_up.n != 2 * down.k:
+        raise ValueError(f"gate_up gives rows of {gate_up.n // 2}, down takes {down.k}")
+
+
 def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2):
     dev = x.device
     if not _same_device(dev, x, ids, w, w1, m1, w2, m2):
@@ -1028,6 +1041,7 @@ def moe_layer_routed(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, logit
     """An MoE layer from the router's logits [t, experts] on: (y [t, n_down],
     topk_ids, topk_w).  w8a8_block plans run a few tokens in two kernels
     (hq_moe_layer_few); otherwise route_topk, then moe_layer."""
+    _check_layer_plans(gate_up, down)
     _dev(logits, "logits")
     topk = int(topk)
     if logits.dim() != 2 or logits.shape != (x.shape[0], gate_up.num_experts) or logits.dtype not in _LOGITS or \
@@ -1052,8 +1066,7 @@ def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: to
     quantize_blocks, and always the aligned path beyond.  x: [t, k] activations (fp8 codes with x_scale for
     W4A8); topk_ids int32 / topk_w fp32 [t, topk] on the GPU."""
     t, topk = topk_ids.shape
-    if down.epi != EPI_TOPK_COMBINE or gate_up.epi not in (EPI_SILU_MUL, EPI_SILU_MUL_QFP8):
-        raise ValueError("moe_layer takes a gate_up plan (silu_mul / silu_mul_qfp8) and a topk_combine plan")
+    _check_layer_plans(gate_up, down)
     fp8 = gate_up.epi == EPI_SILU_MUL_QFP8
     if gate_up._block8:
         if by_slot:

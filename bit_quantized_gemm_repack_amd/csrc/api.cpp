@@ -1292,6 +1292,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.topk_w = topk_w;
       b.topk = topk;
       b.n_slots = n_slots;
+      b.experts = p->layer.num_experts;
       b.w_expert = (int64_t)p->w_bytes_per_expert;
       b.s_expert = (int64_t)(p->meta_bytes_per_expert / 4);
       b.out_scale = out_scale;

@@ -38,6 +38,7 @@ struct B8Args {
   const float* topk_w;
   int once;                // most experts' rows lie in one block
   int topk, n_slots;
+  int experts;             // a block_expert outside [0, experts) is no expert
   int64_t w_expert;        // code bytes per expert
   int64_t s_expert;        // weight scales per expert
   float* out_scale;        // gate_up: scales of the requantised rows [N/256][out_rows]

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((a
   if (!b8_grouped_place(p, 16 * MB, tm, tn)) return;
   const int m0 = tm * 16 * MB;
   const int64_t ex = p.block_expert[tm];
-  if (ex < 0) {
+  if (ex < 0 || ex >= p.experts) {
     if constexpr (MODE == B8_DOWN)
       b8_zero_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
     return;
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
   const int m0 = tm * 16 * MB;
   const int64_t ex = p.block_expert[tm];
   const int c0 = p.col0 + tn * p.cols_wg, c1 = min(c0 + p.cols_wg, p.col0 + p.ncol);
-  if (ex < 0) {
+  if (ex < 0 || ex >= p.experts) {
     b8_zero_rows(p, m0, 16 * MB, c0, c1, threadIdx.x, 256);
     return;
   }

@@ -402,7 +402,9 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  *                             token's topk rows in fp32 in slot order and
  *                             rounds once, so the result is deterministic.
  *                             Slots with an out-of-range expert id
- *                             contribute zero.
+ *                             contribute zero.  sorted_ids, block_expert and
+ *                             num_padded are those of hq_moe_align for this
+ *                             plan's num_experts.
  *   epi HQ_EPI_NONE           gate_up rows without the activation: out
  *                             [max_padded, n] (plan out dtype).
  * a_scale: per-row fp32 scales of 8-bit activations (per token for gate_up,
