@@ -994,8 +994,8 @@ def route_topk(logits: torch.Tensor, topk: int, renormalize: bool = True):
 MOE_FEW_MAX_TOKENS = 16
 
 
-def _uses_few(gate_up: "MoePlan", t: int, topk: int) -> bool:
-    return gate_up._block8 and 0 < t <= MOE_FEW_MAX_TOKENS and topk <= 16 and gate_up.k <= 98304
+def _uses_few(gate_up: "MoePlan", down: "MoePlan", t: int, topk: int) -> bool:
+    return gate_up._block8 and 0 < t <= MOE_FEW_MAX_TOKENS and topk <= 16 and gate_up.k == down.n <= 98304
 
 
 def _check_layer_plans(gate_up: "MoePlan", down: "MoePlan"):
@@ -1047,7 +1047,7 @@ def moe_layer_routed(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, logit
     if logits.dim() != 2 or logits.shape != (x.shape[0], gate_up.num_experts) or logits.dtype not in _LOGITS or \
             logits.device != x.device:
         raise ValueError(f"logits must be fp32 / fp16 / bf16 [{x.shape[0]}, {gate_up.num_experts}] on x's device")
-    if _uses_few(gate_up, x.shape[0], topk) and gate_up.num_experts <= 1024:
+    if _uses_few(gate_up, down, x.shape[0], topk) and gate_up.num_experts <= 1024:
         ids = x.new_empty((x.shape[0], topk), dtype=torch.int32)
         w = x.new_empty((x.shape[0], topk), dtype=torch.float32)
         return _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2), ids, w
@@ -1073,7 +1073,7 @@ def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: to
             raise ValueError("w8a8_block layers have no by-slot path")
         if t == 0:
             return x.new_empty((0, down.n), dtype=_TORCH_OUT[down.quant.out])
-        if x_scale is None and _uses_few(gate_up, t, topk):
+        if x_scale is None and _uses_few(gate_up, down, t, topk):
             return _moe_few(gate_up, down, x, topk, topk_ids, topk_w, None, False, w1, m1, w2, m2)
         by_slot = False
         if x_scale is None:

@@ -41,3 +41,9 @@ def test_int4_plans_that_do_not_belong_together(t):
     for n, k, e, what in ((1024, 256, 7, "experts"), (1024, 512, 8, "rows")):
         with pytest.raises(ValueError, match=what):
             _call(gu, hq.MoePlan(n, k, hq.w4a16("bf16"), e, 64, "topk_combine"), False, t)
+
+def test_few_tokens_need_equal_hidden_sizes():
+    """The two-kernel layer writes rows of x's size; other outputs take the aligned path."""
+    gu, dn = _block8(512, 1024, 8, "silu_mul_qfp8"), _block8(512, 256, 8, "topk_combine")
+    assert not hq._uses_few(gu, dn, 4, 2)
+    assert hq._uses_few(gu, _block8(1024, 256, 8, "topk_combine"), 4, 2)

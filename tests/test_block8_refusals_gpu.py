@@ -1,0 +1,56 @@
+"""Calls of the fp8 block path with tensors that do not fit: refused before
+anything is launched, natively and through ctypes."""
+import pytest
+import torch
+
+import bit_quantized_gemm_repack_amd as hq
+from oracle import block8 as o8
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E4 = torch.float8_e4m3fn
+
+
+def _gen(seed):
+    g = torch.Generator(DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _weight(g, n, k, experts=None):
+    lead = () if experts is None else (experts,)
+    codes = (torch.randn(*lead, n, k, generator=g, device=DEV) * 96).clamp_(-448, 448).to(E4)
+    return codes, (0.5 + torch.rand(*lead, -(-n // 128), k // 128, generator=g, device=DEV)) / (96 * k ** 0.5)
+
+
+def _dense(m=24, n=272, k=1024, **kw):
+    g = _gen(m + n)
+    w, s = _weight(g, n, k)
+    plan = hq.Plan(n, k, hq.w8a8_block(), max_m=64, **kw)
+    a, sa = hq.quantize_blocks(torch.randn(m, k, generator=g, device=DEV, dtype=torch.bfloat16))
+    return plan, w, s, plan.repack(w.view(torch.uint8), s), a, sa
+
+
+@pytest.fixture(params=[True, False], ids=["native", "ctypes"])
+def way(request, monkeypatch):
+    hq.lib()
+    if not request.param:
+        monkeypatch.setattr(hq, "_calls", None)
+
+
+def test_layer_of_another_output_size():
+    """x of 512, y of 768 columns: the same answer on both sides of the few-token switch."""
+    g = _gen(1)
+    w1, s1 = _weight(g, 512, 512, 6)
+    w2, s2 = _weight(g, 768, 256, 6)
+    gu, dn = (hq.MoePlan(n, k, hq.w8a8_block(), 6, 64, e) for n, k, e in ((512, 512, "silu_mul_qfp8"), (768, 256, "topk_combine")))
+    wm = (*gu.repack(w1.view(torch.uint8), s1), *dn.repack(w2.view(torch.uint8), s2))
+    for t in (1, 4, 20):
+        x = torch.randn(t, 512, generator=g, device=DEV, dtype=torch.bfloat16)
+        y, ids, w = hq.moe_layer_routed(gu, dn, x, torch.randn(t, 6, generator=g, device=DEV), 2, *wm)
+        z = hq.moe_layer(gu, dn, x, ids, w, *wm)
+        torch.cuda.synchronize()
+        want, tol = o8.layer(x.double(), ids.long(), w, w1, s1, w2, s2, 2.0 ** -11)
+        for v in (y, z):
+            assert v.shape == (t, 768)
+            assert ((v.double() - want).abs() <= tol + o8.half_step(want.abs() + tol, torch.bfloat16)).all()
