@@ -345,6 +345,12 @@ def _same_device(dev, *tensors) -> bool:
     return dev.type == "cuda"
 
 
+def _block_ws(ws, dev):
+    """A given workspace of a block-scaled call: the kernels write it."""
+    if ws is not None and not _same_device(dev, ws):
+        raise ValueError("ws must be contiguous and on the inputs' device")
+
+
 _TORCH_OUT = {F16: torch.float16, BF16: torch.bfloat16}
 _LOGITS = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _DT_NAME = {F16: "f16", BF16: "bf16", FP8_E4M3: "fp8", INT8: "int8", FP4_E2M1: "mxfp4"}
@@ -533,17 +539,9 @@ class Plan:
         """gemm of a w8a8_block plan.  Split-K partials live in a workspace of
         the call's own unless one is given, so that calls on several streams, or
         captured into several graphs, do not share one."""
-        dev = a.device
-        if not _same_device(dev, a, w, meta, a_scale):
-            for t, name in ((a, "a"), (w, "w"), (meta, "meta"), (a_scale, "a_scale")):
-                if _dev(t, name).device != dev:
-                    raise ValueError(f"{name} must be on a's device")
-        if a.dim() != 2 or a.shape[1] != self.k or a.element_size() != 1:
-            raise ValueError(f"a must hold one-byte fp8 codes [m, {self.k}]")
-        m = a.shape[0]
-        if a_scale.dtype != torch.float32 or a_scale.numel() != m * (self.k // 128):
-            raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
-        self._check_block_layout(w, meta)
+        self._check_block_inputs(a, w, meta, a_scale)
+        dev, m = a.device, a.shape[0]
+        _block_ws(ws, dev)
         if out is None:
             out = a.new_empty((m, self.n), dtype=_TORCH_OUT[self.quant.out])
         elif _dev(out, "out").shape != (m, self.n) or out.dtype != _TORCH_OUT[self.quant.out] or out.device != dev:
@@ -556,6 +554,18 @@ class Plan:
         _run(dev, lib().hq_gemm, self._h, m, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), meta.data_ptr(), out.data_ptr(),
              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
         return out
+
+    def _check_block_inputs(self, a, w, meta, a_scale):
+        dev = a.device
+        if not _same_device(dev, a, w, meta, a_scale):
+            for t, name in ((a, "a"), (w, "w"), (meta, "meta"), (a_scale, "a_scale")):
+                if _dev(t, name).device != dev:
+                    raise ValueError(f"{name} must be on a's device")
+        if a.dim() != 2 or a.shape[1] != self.k or a.element_size() != 1:
+            raise ValueError(f"a must hold one-byte fp8 codes [m, {self.k}]")
+        if a_scale.dtype != torch.float32 or a_scale.numel() != a.shape[0] * (self.k // 128):
+            raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
+        self._check_block_layout(w, meta)
 
     def _check_block_layout(self, w, meta):
         if w.nbytes < self.num_experts * self.n * self.k or \
@@ -894,6 +904,7 @@ class MoePlan(Plan):
                     a.element_size() != 1 or a.numel() != rows * self.k:
                 raise ValueError(f"a must hold [{rows}, {self.k}] one-byte codes and a_scale float32 [{self.k // 128}, {rows}]")
             self._check_block_layout(w, meta)
+            _block_ws(ws, dev)
             down = self.epi == EPI_TOPK_COMBINE
             if not _same_device(dev, a_scale, sorted_ids, block_expert, num_padded, w, meta, out) or \
                     not _same_device(dev, topk_w if down else out_scale):
@@ -913,7 +924,7 @@ class MoePlan(Plan):
                 ws = torch.empty(b.value, dtype=torch.uint8, device=dev)
         if ws is None and not self._block8:
             ws = self.moe_workspace(t, topk, dev)
-        ws_bytes = 0 if ws is None else ws.numel()
+        ws_bytes = 0 if ws is None else ws.nbytes
         _run(dev, lib().hq_moe_gemm, self._h, int(t), int(topk), _ptr(a), _ptr(a_scale), _ptr(sorted_ids),
              _ptr(block_expert), _ptr(num_padded), _ptr(topk_w), _ptr(w), _ptr(meta), _ptr(out), _ptr(out_scale),
              _ptr(ws), ws_bytes)

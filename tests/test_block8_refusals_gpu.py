@@ -54,3 +54,26 @@ def test_layer_of_another_output_size():
         for v in (y, z):
             assert v.shape == (t, 768)
             assert ((v.double() - want).abs() <= tol + o8.half_step(want.abs() + tol, torch.bfloat16)).all()
+
+
+def test_workspace_elsewhere_is_refused():
+    """Split-K partials and slot rows are written to the workspace given: one in host memory is no place for them."""
+    plan, w, s, wm, a, sa = _dense(tuning=dict(kernel=1, split_k=4))
+    need = plan.workspace_bytes(24)
+    assert need
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2], need):
+        with pytest.raises(ValueError, match="ws"):
+            plan.gemm(a, *wm, a_scale=sa, ws=ws)
+    y = plan.gemm(a, *wm, a_scale=sa, ws=torch.empty(need // 4, device=DEV))
+    assert torch.equal(y, plan.gemm(a, *wm, a_scale=sa))
+    g = _gen(3)
+    dn = hq.MoePlan(512, 256, hq.w8a8_block(), 4, 64, "topk_combine")
+    w2, s2 = _weight(g, 512, 256, 4)
+    wd = dn.repack(w2.view(torch.uint8), s2)
+    ids, p = hq.route_topk(torch.randn(24, 4, generator=g, device=DEV), 2)
+    al = hq.moe_align(ids, 4, dn.block_m(24, 2))
+    c, sc = hq.quantize_blocks(torch.randn(al[0].numel(), 256, generator=g, device=DEV, dtype=torch.bfloat16))
+    call = lambda ws: dn.moe_gemm(c, 24, 2, *al, *wd, a_scale=sc, topk_w=p, ws=ws)
+    with pytest.raises(ValueError, match="ws"):
+        call(torch.empty(1 << 20, dtype=torch.uint8))
+    assert torch.equal(call(torch.empty(1 << 18, device=DEV)), call(None))
