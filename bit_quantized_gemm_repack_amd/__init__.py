@@ -616,6 +616,8 @@ class Plan:
         """Time the candidate execution choices for m = a.shape[0] rows on these
         buffers and install the fastest for that m (see hq_plan_autotune).
         Returns {"tuning", "best_us", "current_us", "candidates"}."""
+        if self._block8:
+            self._check_block_inputs(a, w, meta, a_scale)
         _dev(a, "a"), _dev(w, "w"), _dev(meta, "meta")
         if a_scale is not None:
             _dev(a_scale, "a_scale")

@@ -77,3 +77,12 @@ def test_workspace_elsewhere_is_refused():
     with pytest.raises(ValueError, match="ws"):
         call(torch.empty(1 << 20, dtype=torch.uint8))
     assert torch.equal(call(torch.empty(1 << 18, device=DEV)), call(None))
+
+
+def test_autotune_checks_its_tensors():
+    plan, w, s, wm, a, sa = _dense()
+    for args in ((a[:, :512].contiguous(), *wm, sa), (a, *wm, sa[:4].contiguous()), (a, *wm, sa.double()), (a, *wm, sa.cpu()),
+                 (a, wm[0][:4096], wm[1], sa), (a, wm[0], wm[1][:16], sa)):
+        with pytest.raises(ValueError):
+            plan.autotune(*args, reps=1, flush_bytes=0)
+    assert plan.autotune(a, *wm, sa, reps=1, flush_bytes=0)["candidates"] > 0
