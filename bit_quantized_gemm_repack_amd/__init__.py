@@ -460,11 +460,14 @@ class Plan:
     def _check_block_weight(self, codes, scales):
         if not self._block8:
             return
-        if codes.numel() * codes.element_size() != self.num_experts * self.n * self.k:
+        # by shape: [k, n] codes, or scales of [k/128, n/128], hold as many values
+        if codes.element_size() != 1 or codes.shape[-2:] != (self.n, self.k) or \
+                codes.numel() != self.num_experts * self.n * self.k:
             raise ValueError(f"codes must hold {self.num_experts} x [{self.n}, {self.k}] bytes")
-        if scales is None or scales.dtype != torch.float32 or \
-                scales.numel() != self.num_experts * (-(-self.n // 128)) * (self.k // 128):
-            raise ValueError(f"scales must be float32, {self.num_experts} x [{-(-self.n // 128)}, {self.k // 128}]")
+        blocks = (-(-self.n // 128), self.k // 128)
+        if scales is None or scales.dtype != torch.float32 or scales.shape[-2:] != blocks or \
+                scales.numel() != self.num_experts * blocks[0] * blocks[1]:
+            raise ValueError(f"scales must be float32, {self.num_experts} x [{blocks[0]}, {blocks[1]}]")
 
     def _repack_outputs(self, device):
         wb, mb = self.repacked_bytes()
@@ -563,7 +566,8 @@ class Plan:
                     raise ValueError(f"{name} must be on a's device")
         if a.dim() != 2 or a.shape[1] != self.k or a.element_size() != 1:
             raise ValueError(f"a must hold one-byte fp8 codes [m, {self.k}]")
-        if a_scale.dtype != torch.float32 or a_scale.numel() != a.shape[0] * (self.k // 128):
+        # by shape: row-major [m, k/128] scales hold as many values
+        if a_scale.dtype != torch.float32 or a_scale.shape != (self.k // 128, a.shape[0]):
             raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
         self._check_block_layout(w, meta)
 
@@ -902,8 +906,8 @@ class MoePlan(Plan):
             rows = mp if self.epi == EPI_TOPK_COMBINE else t
             if mp != need:
                 raise ValueError(f"sorted_ids must hold {need} ids: the block scales are laid out for that many rows")
-            if a_scale is None or a_scale.dtype != torch.float32 or a_scale.numel() != rows * (self.k // 128) or \
-                    a.element_size() != 1 or a.numel() != rows * self.k:
+            if a_scale is None or a_scale.dtype != torch.float32 or a_scale.shape != (self.k // 128, rows) or \
+                    a.element_size() != 1 or a.shape != (rows, self.k):
                 raise ValueError(f"a must hold [{rows}, {self.k}] one-byte codes and a_scale float32 [{self.k // 128}, {rows}]")
             self._check_block_layout(w, meta)
             _block_ws(ws, dev)

@@ -106,7 +106,7 @@ PyObject* gemm_block(PyObject*, PyObject* const* v, Py_ssize_t count) {
     if (s->device() != a->device() || w->device() != a->device() || meta->device() != a->device()) return nullptr;
     if (a->dim() != 2 || a->size(1) != k || a->element_size() != 1) return nullptr;
     const int64_t m = a->size(0);
-    if (s->scalar_type() != at::kFloat || s->numel() != m * (k / 128)) return nullptr;
+    if (s->scalar_type() != at::kFloat || s->dim() != 2 || s->size(0) != k / 128 || s->size(1) != m) return nullptr;
     if ((int64_t)w->nbytes() < n * k || (int64_t)meta->nbytes() < (n + 127) / 128 * (k / 128) * 4) return nullptr;
     size_t need = 0;
     if (workspace_fn(plan, m, &need) != HQ_OK) return nullptr;

@@ -301,3 +301,13 @@ def test_native_calls_take_nothing_else():
         hq._calls.bind(1, 2)
     with pytest.raises(ValueError):
         hq.quantize_blocks(x)
+
+
+def test_repack_refuses_transposed_tensors():
+    """Scales [k/128, n/128] and codes [k, n] hold as many values as the right ones."""
+    p = _plan(n=256, k=512)
+    codes, s = torch.zeros(256, 512, dtype=torch.uint8), torch.ones(2, 4)
+    p.repack_host(codes, s)
+    for c, v in ((codes, s.t()), (codes, s.flatten()), (codes.t(), s), (codes.flatten(), s), (codes.view(torch.int32), s)):
+        with pytest.raises(ValueError):
+            p.repack_host(c, v)

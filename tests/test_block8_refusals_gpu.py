@@ -86,3 +86,38 @@ def test_autotune_checks_its_tensors():
         with pytest.raises(ValueError):
             plan.autotune(*args, reps=1, flush_bytes=0)
     assert plan.autotune(a, *wm, sa, reps=1, flush_bytes=0)["candidates"] > 0
+
+
+@pytest.mark.parametrize("m", [8, 24, 64])
+def test_scales_of_another_order_are_refused(way, m):
+    """Row-major scales [m, k/128], which other libraries keep, hold as many values as [k/128, m]."""
+    plan, w, s, wm, a, sa = _dense(m)
+    want = plan.gemm(a, *wm, a_scale=sa)
+    if m != 8:
+        for bad in (sa.t().contiguous(), sa.flatten(), sa.unsqueeze(0)):
+            with pytest.raises(ValueError, match="a_scale"):
+                plan.gemm(a, *wm, a_scale=bad)
+            with pytest.raises(ValueError, match="a_scale"):
+                plan.autotune(a, *wm, a_scale=bad, reps=1, flush_bytes=0)
+    with pytest.raises(ValueError, match="scales"):
+        plan.repack(w.view(torch.uint8), s.t().contiguous())
+    with pytest.raises(ValueError, match="codes"):
+        plan.repack(w.view(torch.uint8).t().contiguous(), s)
+    assert torch.equal(plan.gemm(a, *wm, a_scale=sa), want)
+
+
+def test_grouped_scales_of_another_order_are_refused():
+    g = _gen(4)
+    gu = hq.MoePlan(512, 512, hq.w8a8_block(), 4, 64, "silu_mul_qfp8")
+    w1, s1 = _weight(g, 512, 512, 4)
+    with pytest.raises(ValueError, match="scales"):
+        gu.repack(w1.view(torch.uint8), s1.flatten(0, 1).t().contiguous())
+    wm = gu.repack(w1.view(torch.uint8), s1)
+    x = torch.randn(24, 512, generator=g, device=DEV, dtype=torch.bfloat16)
+    ids, p = hq.route_topk(torch.randn(24, 4, generator=g, device=DEV), 2)
+    al = hq.moe_align(ids, 4, gu.block_m(24, 2))
+    q, s = hq.quantize_blocks(x)
+    gu.moe_gemm(q, 24, 2, *al, *wm, a_scale=s)
+    for kw in (dict(a=q, a_scale=s.t().contiguous()), dict(a=q.view(48, 256), a_scale=s)):
+        with pytest.raises(ValueError):
+            gu.moe_gemm(t=24, topk=2, sorted_ids=al[0], block_expert=al[1], num_padded=al[2], w=wm[0], meta=wm[1], **kw)
