@@ -352,6 +352,8 @@ def _block_ws(ws, dev):
 
 
 _TORCH_OUT = {F16: torch.float16, BF16: torch.bfloat16}
+# What may hold e4m3 codes: the type itself, or raw bytes (not another fp8 type's)
+_E4M3 = (torch.uint8, torch.int8, torch.float8_e4m3fn)
 _LOGITS = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _DT_NAME = {F16: "f16", BF16: "bf16", FP8_E4M3: "fp8", INT8: "int8", FP4_E2M1: "mxfp4"}
 
@@ -461,9 +463,9 @@ class Plan:
         if not self._block8:
             return
         # by shape: [k, n] codes, or scales of [k/128, n/128], hold as many values
-        if codes.element_size() != 1 or codes.shape[-2:] != (self.n, self.k) or \
+        if codes.dtype not in _E4M3 or codes.shape[-2:] != (self.n, self.k) or \
                 codes.numel() != self.num_experts * self.n * self.k:
-            raise ValueError(f"codes must hold {self.num_experts} x [{self.n}, {self.k}] bytes")
+            raise ValueError(f"codes must hold {self.num_experts} x [{self.n}, {self.k}] e4m3 codes (or their bytes)")
         blocks = (-(-self.n // 128), self.k // 128)
         if scales is None or scales.dtype != torch.float32 or scales.shape[-2:] != blocks or \
                 scales.numel() != self.num_experts * blocks[0] * blocks[1]:
@@ -564,8 +566,8 @@ class Plan:
             for t, name in ((a, "a"), (w, "w"), (meta, "meta"), (a_scale, "a_scale")):
                 if _dev(t, name).device != dev:
                     raise ValueError(f"{name} must be on a's device")
-        if a.dim() != 2 or a.shape[1] != self.k or a.element_size() != 1:
-            raise ValueError(f"a must hold one-byte fp8 codes [m, {self.k}]")
+        if a.dim() != 2 or a.shape[1] != self.k or a.dtype not in _E4M3:
+            raise ValueError(f"a must hold e4m3 codes (or their bytes) [m, {self.k}]")
         # by shape: row-major [m, k/128] scales hold as many values
         if a_scale.dtype != torch.float32 or a_scale.shape != (self.k // 128, a.shape[0]):
             raise ValueError(f"a_scale must be float32 [{self.k // 128}, m]")
@@ -784,8 +786,8 @@ def quantize_blocks(x: torch.Tensor, silu_mul: bool = False, codes: Optional[tor
     dev = x.device
     if codes is None:
         codes = x.new_empty((m, k), dtype=torch.uint8) if silu_mul else torch.empty_like(x, dtype=torch.uint8)
-    elif _dev(codes, "codes").shape != (m, k) or codes.element_size() != 1 or codes.device != dev:
-        raise ValueError("codes must be 1-byte [m, k] on x's device")
+    elif _dev(codes, "codes").shape != (m, k) or codes.dtype not in _E4M3 or codes.device != dev:
+        raise ValueError("codes must be e4m3 (or bytes) [m, k] on x's device")
     if scales is None:
         scales = x.new_empty((k // 128, m), dtype=torch.float32)
     elif _dev(scales, "scales").shape != (k // 128, m) or scales.dtype != torch.float32 or scales.device != dev:
@@ -907,8 +909,8 @@ class MoePlan(Plan):
             if mp != need:
                 raise ValueError(f"sorted_ids must hold {need} ids: the block scales are laid out for that many rows")
             if a_scale is None or a_scale.dtype != torch.float32 or a_scale.shape != (self.k // 128, rows) or \
-                    a.element_size() != 1 or a.shape != (rows, self.k):
-                raise ValueError(f"a must hold [{rows}, {self.k}] one-byte codes and a_scale float32 [{self.k // 128}, {rows}]")
+                    a.dtype not in _E4M3 or a.shape != (rows, self.k):
+                raise ValueError(f"a must hold [{rows}, {self.k}] e4m3 codes (or their bytes) and a_scale float32 [{self.k // 128}, {rows}]")
             self._check_block_layout(w, meta)
             _block_ws(ws, dev)
             down = self.epi == EPI_TOPK_COMBINE

@@ -104,7 +104,9 @@ PyObject* gemm_block(PyObject*, PyObject* const* v, Py_ssize_t count) {
     const at::Tensor *a = tensor(v[4]), *s = tensor(v[5]), *w = tensor(v[6]), *meta = tensor(v[7]);
     if (!plan || n < 1 || k < 128 || !a || !s || !w || !meta || !current(*a)) return nullptr;
     if (s->device() != a->device() || w->device() != a->device() || meta->device() != a->device()) return nullptr;
-    if (a->dim() != 2 || a->size(1) != k || a->element_size() != 1) return nullptr;
+    const auto type = a->scalar_type();
+    if (type != at::kByte && type != at::kFloat8_e4m3fn && type != at::kChar) return nullptr;
+    if (a->dim() != 2 || a->size(1) != k) return nullptr;
     const int64_t m = a->size(0);
     if (s->scalar_type() != at::kFloat || s->dim() != 2 || s->size(0) != k / 128 || s->size(1) != m) return nullptr;
     if ((int64_t)w->nbytes() < n * k || (int64_t)meta->nbytes() < (n + 127) / 128 * (k / 128) * 4) return nullptr;

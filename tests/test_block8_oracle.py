@@ -311,3 +311,13 @@ def test_repack_refuses_transposed_tensors():
     for c, v in ((codes, s.t()), (codes, s.flatten()), (codes.t(), s), (codes.flatten(), s), (codes.view(torch.int32), s)):
         with pytest.raises(ValueError):
             p.repack_host(c, v)
+
+
+def test_repack_refuses_other_types():
+    p = _plan(n=256, k=512)
+    codes, s = torch.zeros(256, 512, dtype=torch.uint8), torch.ones(2, 4)
+    for dt in (torch.float8_e4m3fn, torch.int8):
+        p.repack_host(codes.view(dt), s)
+    for dt in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.bool):
+        with pytest.raises(ValueError, match="e4m3"):
+            p.repack_host(codes.view(dt), s)

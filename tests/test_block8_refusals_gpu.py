@@ -121,3 +121,19 @@ def test_grouped_scales_of_another_order_are_refused():
     for kw in (dict(a=q, a_scale=s.t().contiguous()), dict(a=q.view(48, 256), a_scale=s)):
         with pytest.raises(ValueError):
             gu.moe_gemm(t=24, topk=2, sorted_ids=al[0], block_expert=al[1], num_padded=al[2], w=wm[0], meta=wm[1], **kw)
+
+
+@pytest.mark.parametrize("dt", [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.bool])
+def test_codes_of_another_type_are_refused(way, dt):
+    """One byte a value, but other values."""
+    plan, w, s, wm, a, sa = _dense()
+    with pytest.raises(ValueError, match="e4m3"):
+        plan.gemm(a.view(dt), *wm, a_scale=sa)
+    with pytest.raises(ValueError, match="e4m3"):
+        plan.repack(w.view(dt), s)
+    with pytest.raises(ValueError, match="e4m3"):
+        hq.quantize_blocks(torch.zeros(2, 256, dtype=torch.bfloat16, device=DEV), codes=torch.empty(2, 256, device=DEV).to(dt))
+    want = plan.gemm(a, *wm, a_scale=sa)
+    for ok in (E4, torch.int8):
+        assert torch.equal(plan.gemm(a.view(ok), *wm, a_scale=sa), want)
+        assert torch.equal(plan.repack(w.view(ok), s)[0], wm[0])
