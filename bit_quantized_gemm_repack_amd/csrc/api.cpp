@@ -239,12 +239,21 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
   // row: 9.7 against 12.3 us), beyond while the blocks are few (33 rows of N =
   // 576: 8.2 us against 10 for the best tile).
   bool skinny = mm <= 16 ? n128 < 160 : (mm <= 128 && blocks <= 512);
+  // Given fields come first: the kernel that has the shape they name, at any
+  // number of rows, and the free fields chosen to go with them.  Where none has
+  // it, what is left is no shape and check_exec refuses it.
+  auto tile = [&](int bm, int bn) {  // may this tile be chosen?
+    return (!u.tile_m || u.tile_m == bm) && (!u.tile_n || u.tile_n == bn) && (!u.stages || u.stages == b8_stages(bm));
+  };
+  const bool has_skinny = (!u.tile_m || u.tile_m == 16) && (!u.tile_n || u.tile_n == 16 || u.tile_n == 32);
+  const bool has_tile = tile(16, 128) || tile(32, 128) || tile(64, 128) || tile(128, 128) || tile(128, 256);
   if (u.kernel) skinny = u.kernel == KER_SKINNY;
+  else if (has_skinny != has_tile) skinny = has_skinny;
   int64_t split = 1;
   if (skinny) {
     e.kernel = KER_SKINNY;
     SkinnyCfg& c = e.sk;
-    c.mb = 1;
+    c.mb = has_skinny ? 1 : 0;
     // one column block a workgroup while that leaves under a workgroup and a
     // half a CU and K is long (N = 4096, one row: 9.0 against 9.5 us; N = 14336:
     // two 14.0, one 25; K = 2048, N = 512, 16 rows: two 4.4, one 4.8)
@@ -254,10 +263,9 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
     // 7.4: left to tuning.)
     c.waves = 4;  // (8: 10.1 against 9.0 us at N = 4096, K = 7168)
     c.stages = 1;
-    if (u.tile_m) c.mb = u.tile_m / 16;
     if (u.tile_n) c.nb = u.tile_n / 16;
     if (u.waves) c.waves = u.waves;
-    e.tiles_m = cdiv(mm, 16 * std::max(1, c.mb));
+    e.tiles_m = cdiv(mm, 16);
     e.tiles_n = cdiv(n16, std::max(1, c.nb));
     if (u.split_k) split = u.split_k;
   } else {
@@ -275,9 +283,16 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
       int bm;
       int64_t most;
     } tiles[] = {{16, 256}, {32, 256}, {64, G >= 96 ? 256 : 512}, {128, G >= 16 ? 768 : 1200}};
-    e.tl.bm = 128;
+    e.tl.bm = has_tile ? 128 : u.tile_m;
     e.tl.nbw = 4;  // 256 columns: enough tiles whatever the shape
+    if (!tile(128, 256))  // then the tallest of 128 columns
+      for (const auto& t : tiles)
+        if (tile(t.bm, 128)) {
+          e.tl.bm = t.bm;
+          e.tl.nbw = 2;
+        }
     for (const auto& t : tiles) {
+      if (!tile(t.bm, 128)) continue;
       if (longk && ((t.bm == 16 && mm > 32) || (t.bm == 32 && mm > 64 && cdiv(mm, 32) * n128 > 56))) continue;
       if (cdiv(mm, t.bm) * n128 > t.most) continue;
       e.tl.bm = t.bm;
@@ -285,9 +300,7 @@ static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {
       break;
     }
     e.tl.gm = u.tile_group ? u.tile_group : 8;
-    if (u.tile_m) e.tl.bm = u.tile_m;
-    if (u.tile_n) e.tl.nbw = u.tile_n / 64;
-    e.tl.stages = u.stages ? u.stages : (e.tl.nbw == 4 || e.tl.bm >= 128 ? 2 : (e.tl.bm == 64 ? 3 : 4));
+    e.tl.stages = has_tile ? b8_stages(e.tl.bm) : 0;
     e.tiles_m = cdiv(mm, std::max(1, e.tl.bm));
     e.tiles_n = cdiv(N, 64 * std::max(1, e.tl.nbw));
     const int64_t count = e.tiles_m * e.tiles_n, most = e.tl.bm < 128 ? 256 : (G >= 96 ? 512 : 400);
@@ -460,14 +473,17 @@ namespace {
 hq_status check_exec(const hq_plan* p, const hq::Exec& e) {
   if (p->user.split_k < 0 || p->user.split_k > 64) return fail(HQ_ERR_INVALID_ARG, "split_k must be 1..64");
   if (p->fmt == hq::FMT_B8) {
+    // the plan's fields that only one of its kernels reads, whichever runs
+    if (p->user.waves < 0 || p->user.waves > 8) return fail(HQ_ERR_INVALID_ARG, "fp8 block kernels: waves must be 1..8");
+    if (p->user.tile_group < 0 || p->user.tile_group > 64)
+      return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_group must be 1..64");
     if (e.kernel == hq::KER_TILED) {
       if (!hq::b8_tile_ok({e.tl.bm, 64 * e.tl.nbw, e.tl.split, e.tl.stages}))
-        return fail(HQ_ERR_INVALID_ARG, "no fp8 block tile of %d x %d with %d stages", e.tl.bm, 64 * e.tl.nbw, e.tl.stages);
+        return fail(HQ_ERR_INVALID_ARG, "no fp8 block tile has this tuning's shape (16, 32, 64 or 128 x 128, 128 x 256)");
       if (e.tl.gm < 1 || e.tl.gm > 64) return fail(HQ_ERR_INVALID_ARG, "tiled kernel: tile_group must be 1..64");
       if (e.tiles_m * e.tiles_n > (int64_t(1) << 31) - 1) return fail(HQ_ERR_UNSUPPORTED, "too many tiles");
     } else if (e.sk.mb != 1 || !hq::b8_skinny_ok({e.sk.nb, e.sk.waves, e.sk.split})) {
-      return fail(HQ_ERR_INVALID_ARG, "no fp8 block skinny shape of %d x %d with %d waves", 16 * e.sk.mb, 16 * e.sk.nb,
-                  e.sk.waves);
+      return fail(HQ_ERR_INVALID_ARG, "no fp8 block skinny shape is this tuning's (16 x 16 or 32, 1..8 waves)");
     }
     return HQ_OK;
   }

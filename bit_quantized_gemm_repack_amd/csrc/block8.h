@@ -58,6 +58,7 @@ enum B8Mode : int { B8_DENSE = 0, B8_GATE_UP = 1, B8_DOWN = 2 };
 struct B8Tile {
   int bm, bn, split, stages;
 };
+inline int b8_stages(int bm) { return bm >= 128 ? 2 : (bm == 64 ? 3 : 4); }
 bool b8_tile_ok(const B8Tile& t);
 int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream);
 // Grouped: aligned blocks of bm rows (16, 64, 128) by 256 columns.

@@ -729,11 +729,9 @@ hipError_t launch_short(const B8Args& a, dim3 grid, hipStream_t s) {
 }  // namespace
 
 bool b8_tile_ok(const B8Tile& t) {
-  if (t.bn == 256) return t.bm == 128 && t.stages == 2;
-  if (t.bn != 128) return false;
-  if (t.bm == 128) return t.stages == 2;
-  if (t.bm == 64) return t.stages == 3;
-  return (t.bm == 16 || t.bm == 32) && t.stages == 4;
+  if (t.stages != b8_stages(t.bm)) return false;
+  if (t.bn == 256) return t.bm == 128;
+  return t.bn == 128 && (t.bm == 16 || t.bm == 32 || t.bm == 64 || t.bm == 128);
 }
 
 int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream) {

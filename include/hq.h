@@ -222,7 +222,9 @@ typedef struct hq_tuning {
   int kernel;  /* 0 auto, 1 skinny (small M, split-K), 2 tiled (large M)  */
   int tile_m;  /* skinny: rows per workgroup (16, 32, 64); tiled: 64 or 128
                   (W8A8-BLOCK: skinny 16; tiled 16, 32, 64 or 128; grouped:
-                  aligned blocks of 16, 64 or 128 rows)                    */
+                  aligned blocks of 16, 64 or 128 rows.  Dense: skinny 16 x 16
+                  or 32; tiled 128 columns, or 128 x 256.  Fields that are
+                  given choose the kernel that has them, at every m)       */
   int tile_n;  /* skinny: columns per workgroup (16, 32, 64); tiled: 128, 256 */
   int waves;   /* wavefronts per workgroup                                 */
   int split_k; /* workgroups sharing one output tile along K (dense)     */
