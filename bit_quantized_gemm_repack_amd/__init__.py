@@ -21,6 +21,7 @@ import importlib
 import json
 import os
 import re
+import warnings
 from dataclasses import dataclass
 from typing import Optional
 
@@ -261,8 +262,8 @@ def lib():
 
 
 # The native form of the short calls (csrc/binding/calls.cpp), once the library
-# is loaded and if it is built; it answers None to anything but the ordinary
-# call, which the Python below then checks.
+# is loaded and if it is built and loads with this torch; it answers None to
+# anything but the ordinary call, which the Python below then checks.
 _calls = None
 
 
@@ -270,9 +271,15 @@ def _bind_calls(L):
     global _calls
     if not os.path.exists(CALLS_PATH):
         return
-    native = importlib.import_module("._calls", __package__)
-    native.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                  for f in (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes)))
+    try:
+        native = importlib.import_module("._calls", __package__)
+        if native.built_for != torch.__version__:
+            raise ImportError(f"built for torch {native.built_for}, this is {torch.__version__}")
+        native.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes)))
+    except Exception as e:  # a damaged file, another torch's: every call works without it
+        warnings.warn(f"{CALLS_PATH} is not used ({e}): short calls go through ctypes; build again to have it", RuntimeWarning)
+        return
     _calls = native
 
 
