@@ -267,11 +267,25 @@ def lib():
 _calls = None
 
 
+def _whole(path: str) -> bool:
+    """Whether an ELF file is as long as its header says: mapping one that was cut
+    short ends the process instead of raising."""
+    with open(path, "rb") as f:
+        h = f.read(64)
+    if len(h) < 64 or h[:4] != b"\x7fELF":
+        return False
+    at = int.from_bytes(h[40:48], "little")           # the section table, which comes last
+    size, count = (int.from_bytes(h[i:i + 2], "little") for i in (58, 60))
+    return os.path.getsize(path) >= at + size * count
+
+
 def _bind_calls(L):
     global _calls
     if not os.path.exists(CALLS_PATH):
         return
     try:
+        if not _whole(CALLS_PATH):
+            raise ImportError("the file is cut short")
         native = importlib.import_module("._calls", __package__)
         if native.built_for != torch.__version__:
             raise ImportError(f"built for torch {native.built_for}, this is {torch.__version__}")

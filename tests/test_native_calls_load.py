@@ -39,7 +39,10 @@ def test_first_call_without_the_native_part(tmp_path, kind):
     hq.lib()
     if kind == "cut short" and not os.path.exists(hq.CALLS_PATH):
         pytest.skip("the native calls are not built")
-    calls = {"damaged": b"\x7fELF damaged", "missing": None}.get(kind) if kind != "cut short" else open(hq.CALLS_PATH, "rb").read(4096)
+    calls = {"damaged": b"\x7fELF damaged", "missing": None}.get(kind)
+    if kind == "cut short":
+        with open(hq.CALLS_PATH, "rb") as f:
+            calls = f.read(4096)
     r = _package(tmp_path, calls)
     assert r.returncode == 0, r.stderr
     assert "kernel=" in r.stdout and "native False" in r.stdout
