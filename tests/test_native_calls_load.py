@@ -60,3 +60,19 @@ def test_native_part_of_another_torch_is_not_used(monkeypatch):
     with pytest.warns(RuntimeWarning, match="built for torch"):
         hq._bind_calls(L)
     assert hq._calls is None
+
+
+def test_build_goes_on_without_the_native_part(tmp_path, monkeypatch):
+    """No compiler for it, or headers that do not fit: a warning, and no file of an earlier build stays."""
+    from bit_quantized_gemm_repack_amd import build as b
+    monkeypatch.setattr(b, "CALLS", str(tmp_path / "_calls.so"))
+    no_headers = subprocess.CompletedProcess([], 1, "", "fatal error: ATen/core/Tensor.h: No such file or directory")
+
+    def no_compiler(*a, **kw):
+        raise FileNotFoundError("g++")
+    for run, what in ((no_compiler, r"g\+\+"), (lambda *a, **kw: no_headers, "Tensor.h")):
+        (tmp_path / "_calls.so").write_bytes(b"old")
+        monkeypatch.setattr(b.subprocess, "run", run)
+        with pytest.warns(RuntimeWarning, match=what):
+            assert b._build_calls_if_possible() is None
+        assert not (tmp_path / "_calls.so").exists()
