@@ -6,7 +6,8 @@
 // Each function takes the ordinary call: contiguous tensors of the right types
 // and sizes on the current device.  It returns None for any other and after any
 // error, and the Python function behind it then checks and calls again, with its
-// messages.  The library's entry points come in by address (bind), so nothing
+// messages.  Other Python threads run while it allocates and launches, which wait
+// where memory or the launch queue is full (as ctypes lets them).  The library's entry points come in by address (bind), so nothing
 // here links to it.
 #include <Python.h>
 
@@ -48,6 +49,12 @@ PyObject* pair(at::Tensor a, at::Tensor b) {
   return r;
 }
 
+// Python's lock given up for a scope, for what may wait and touches no Python object.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // f(), or None where it throws (an allocation that fails).
 template <typename F>
 PyObject* guarded(F&& f) {
@@ -67,11 +74,15 @@ PyObject* quantize_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int silu = PyObject_IsTrue(a[1]);
     const int64_t m = x->size(0), k = silu ? x->size(1) / 2 : x->size(1);
     if (silu < 0 || k % 128 || (silu && x->size(1) % 2)) return nullptr;
-    at::Tensor codes = at::empty({m, k}, x->options().dtype(at::kByte));
-    at::Tensor scales = at::empty({k / 128, m}, x->options().dtype(at::kFloat));
-    if (quantize_fn(m, k, (hq_dtype)act_type(*x), silu, x->data_ptr(), codes.data_ptr(), static_cast<float*>(scales.data_ptr()),
-                    stream(*x)) != HQ_OK)
-      return nullptr;
+    at::Tensor codes, scales;
+    {
+      const Unlocked unlocked;
+      codes = at::empty({m, k}, x->options().dtype(at::kByte));
+      scales = at::empty({k / 128, m}, x->options().dtype(at::kFloat));
+      if (quantize_fn(m, k, (hq_dtype)act_type(*x), silu, x->data_ptr(), codes.data_ptr(), static_cast<float*>(scales.data_ptr()),
+                      stream(*x)) != HQ_OK)
+        return nullptr;
+    }
     return pair(std::move(codes), std::move(scales));
   });
 }
@@ -85,11 +96,15 @@ PyObject* route_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t t = x->size(0), topk = PyLong_AsLongLong(a[1]);
     const int renorm = PyObject_IsTrue(a[2]);
     if (type < 0 || topk < 1 || topk > 64 || x->size(1) > 1024 || renorm < 0) return nullptr;
-    at::Tensor ids = at::empty({t, topk}, x->options().dtype(at::kInt));
-    at::Tensor w = at::empty({t, topk}, x->options().dtype(at::kFloat));
-    if (route_fn(t, (int)x->size(1), (int)topk, (hq_dtype)type, x->data_ptr(), renorm, static_cast<int32_t*>(ids.data_ptr()),
-                 static_cast<float*>(w.data_ptr()), stream(*x)) != HQ_OK)
-      return nullptr;
+    at::Tensor ids, w;
+    {
+      const Unlocked unlocked;
+      ids = at::empty({t, topk}, x->options().dtype(at::kInt));
+      w = at::empty({t, topk}, x->options().dtype(at::kFloat));
+      if (route_fn(t, (int)x->size(1), (int)topk, (hq_dtype)type, x->data_ptr(), renorm, static_cast<int32_t*>(ids.data_ptr()),
+                   static_cast<float*>(w.data_ptr()), stream(*x)) != HQ_OK)
+        return nullptr;
+    }
     return pair(std::move(ids), std::move(w));
   });
 }
@@ -110,13 +125,18 @@ PyObject* gemm_block(PyObject*, PyObject* const* v, Py_ssize_t count) {
     const int64_t m = a->size(0);
     if (s->scalar_type() != at::kFloat || s->dim() != 2 || s->size(0) != k / 128 || s->size(1) != m) return nullptr;
     if ((int64_t)w->nbytes() < n * k || (int64_t)meta->nbytes() < (n + 127) / 128 * (k / 128) * 4) return nullptr;
-    size_t need = 0;
-    if (workspace_fn(plan, m, &need) != HQ_OK) return nullptr;
-    at::Tensor out = at::empty({m, n}, a->options().dtype(PyObject_IsTrue(v[3]) ? at::kBFloat16 : at::kHalf)), ws;
-    if (need) ws = at::empty({(int64_t)need}, a->options().dtype(at::kByte));
-    if (gemm_fn(plan, m, a->data_ptr(), s->data_ptr(), w->data_ptr(), meta->data_ptr(), out.data_ptr(),
-                need ? ws.data_ptr() : nullptr, need, stream(*a)) != HQ_OK)
-      return nullptr;
+    const auto out_type = PyObject_IsTrue(v[3]) ? at::kBFloat16 : at::kHalf;
+    at::Tensor out, ws;
+    {
+      const Unlocked unlocked;
+      size_t need = 0;
+      if (workspace_fn(plan, m, &need) != HQ_OK) return nullptr;
+      out = at::empty({m, n}, a->options().dtype(out_type));
+      if (need) ws = at::empty({(int64_t)need}, a->options().dtype(at::kByte));
+      if (gemm_fn(plan, m, a->data_ptr(), s->data_ptr(), w->data_ptr(), meta->data_ptr(), out.data_ptr(),
+                  need ? ws.data_ptr() : nullptr, need, stream(*a)) != HQ_OK)
+        return nullptr;
+    }
     return THPVariable_Wrap(std::move(out));
   });
 }
