@@ -47,6 +47,18 @@ __device__ inline float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// e^d of a logit's difference d <= 0 from the largest: 2^(t + r), t the rounded
+// product d log2(e) and r what the rounding left, by the hardware's power (1 ulp)
+// and one multiply-add.  1.5 ulp whatever d, where 2^t alone is off by |d| 2^-24
+// (16383 x 160 bf16 in a graph 7.1 us, 6.8 that way, 7.8 with expf).  Below 2^-126
+// it is zero.
+__device__ inline float routing_exp(float d) {
+  constexpr float hi = 1.44269504f, lo = 1.92596299e-8f;  // log2(e)
+  d = fmaxf(d, -200.f);  // zero from here on
+  const float t = d * hi, r = fmaf(d, lo, fmaf(d, hi, -t)), p = __builtin_amdgcn_exp2f(t);
+  return fmaf(p, r * 0.693147181f, p);
+}
+
 // LT: 0 fp32, 1 bf16, 2 fp16
 template <int LT>
 __device__ inline float load_logit(const void* p, int64_t i) {
@@ -122,7 +134,7 @@ struct Logits {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (key[i]) s += expf(key_logit(key[i]) - top);
+      if (key[i]) s += routing_exp(key_logit(key[i]) - top);
     return wave_sum(s);
   }
 };
@@ -145,7 +157,7 @@ __global__ void __launch_bounds__(256) route_kernel(const void* __restrict__ log
     uint32_t k;
     const int e = x.take(lane, &k);
     if (e < 0) break;
-    const float v = expf(key_logit(k) - top);
+    const float v = routing_exp(key_logit(k) - top);
     if (renorm) sum += v;
     if (lane == j) {
       my_id = e;
@@ -221,8 +233,6 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict_
     for (int i = 1; i < NPL; ++i) m = max(m, key[i]);
     return m;
   };
-  // (weights below 2^-126 are zero)
-  auto exp_of = [](float d) { return __builtin_amdgcn_exp2f(d * 1.44269504f); };
   uint32_t head = largest();
   uint32_t best = b8_row_max(head);
   const float top = value(best);
@@ -230,7 +240,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict_
   if (!renorm) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (key[i]) sum += exp_of(value(key[i]) - top);
+      if (key[i]) sum += routing_exp(value(key[i]) - top);
     sum = row_sum(sum);
   }
   int my_id = -1;
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict_
 #pragma unroll
       for (int i = 0; i < NPL; ++i) key[i] = key[i] == m ? 0u : key[i];
     }
-    const float v = m ? exp_of(value(m) - top) : 0.f;
+    const float v = m ? routing_exp(value(m) - top) : 0.f;
     if (renorm) sum += v;
     if (lane == j && m) {
       my_id = e;
@@ -297,7 +307,7 @@ __device__ inline void few_write_routing(const B8FewArgs& p, int z, int lane) {
     uint32_t k;
     const int id = r.take(lane, &k);
     if (id < 0) break;
-    const float v = expf(key_logit(k) - top);
+    const float v = routing_exp(key_logit(k) - top);
     if (p.renorm) sum += v;
     if (j == z) {
       e = id;
@@ -766,10 +776,11 @@ int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits,
   const dim3 grid((unsigned)((t + 3) / 4)), block(256);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int ti = (int)t;
-  // 64 experts or fewer leave a wave per token nothing to gain; for more, a wave
+  // One token goes as the layer's gate_up routes it, whose weights are so the same
+  // bits.  64 experts or fewer leave a wave per token nothing to gain; for more, a wave
   // has the shorter chain and sixteen lanes the fewer instructions (256 experts,
   // top 8, fp32: 4096 tokens 6.0 us by waves, 6.5 by rows, 16383 15.6 and 11.0)
-  if (topk <= 16 && (E <= 64 || (E <= 256 && t >= 6144))) {
+  if (t > 1 && topk <= 16 && (E <= 64 || (E <= 256 && t >= 6144))) {
     const dim3 rows((unsigned)((t + 15) / 16));
     auto go = [&]<int LT>() -> int {
       if (E <= 64) return (int)launch_timed(route_rows_kernel<LT, 4>, rows, block, 0, s, logits, ti, E, topk, renorm, ids, w);

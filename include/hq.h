@@ -462,7 +462,8 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* plan, int64_t t, int topk, const vo
  * over the chosen ones' sum.  Logits of -inf (experts shut off) and NaN are
  * never chosen and add nothing to the softmax: a row with fewer than topk
  * others ends in ids of -1 with weight 0.  A logit of +inf gives unspecified
- * weights.  topk_ids int32 and topk_w fp32 [t, topk], fully overwritten, as
+ * weights; one below 2^-126 may be zero.  topk_ids int32 and topk_w fp32 [t,
+ * topk], fully overwritten, as
  * hq_moe_align / hq_moe_gemm take them.  num_experts <= 1024, topk <= 64,
  * t <= 2^24; t = 0 is a no-op.  The three are aligned to their elements (slices
  * of a batch may start at any row).  Honours hq_time_next_launch (one kernel). */
@@ -477,7 +478,8 @@ hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_typ
  * first; more tokens' is a kernel of its own before it.
  *   x         device [t, H] fp16 / bf16 (x_type)
  *   logits    device [t, num_experts]: topk_ids and topk_w (device [t, topk])
- *             are outputs, as hq_route_topk writes them; or NULL: they are
+ *             are outputs, bit for bit what hq_route_topk writes for these
+ *             logits; or NULL: they are
  *             inputs (ids outside [0, num_experts) contribute zero, an id may
  *             come twice in a row)
  *   out       device [t, H] in the down plan's out dtype

@@ -68,3 +68,45 @@ def test_route_every_kernel(t, e, topk, dt):
         wi, ww, far = _want(x, topk, renorm)
         assert torch.equal(ids.long(), wi)
         assert ((w.double() - ww).abs() <= _bound(ww, far, e)).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("t,e", [(1, 64), (5, 64), (5, 256), (6200, 256), (6200, 130)])
+def test_far_logits(t, e, dt):
+    """Differences that are exact in fp32, up to 80: the exponential's own rounding is all there is."""
+    x = -(torch.arange(e, device=DEV) * 0.5).clamp_max(80).repeat(t, 1)
+    x[:, 0] = 0
+    x = x[:, torch.randperm(e, generator=_gen(e), device=DEV)].to(dt).contiguous()
+    for renorm in (True, False):
+        ids, w = hq.route_topk(x, 16, renormalize=renorm)
+        torch.cuda.synchronize()
+        wi, ww, far = _want(x, 16, renorm)
+        assert torch.equal(ids.long(), wi)
+        assert ((w.double() - ww).abs() <= ww * (1 + 1 + 13 + 0.5) * 2.0 ** -23 * 1.01).all()
+    far = torch.full((t, e), -60.0, device=DEV, dtype=dt)
+    far[:, 3], far[:, 5] = 0.0, -40.0
+    ids, w = hq.route_topk(far, 3, renormalize=False)
+    torch.cuda.synchronize()
+    assert ids[:, 0].eq(3).all() and ids[:, 1].eq(5).all()
+    wi, ww, _ = _want(far, 3, False)
+    assert ((w.double() - ww).abs() <= ww * (1 + 1 + 13 + 0.5) * 2.0 ** -23 * 1.01).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("e,topk", [(8, 2), (40, 6), (64, 8), (65, 4), (128, 8), (200, 8), (256, 16), (300, 3), (700, 8)])
+def test_layer_writes_the_weights_of_routing(e, topk, dt, renorm):
+    """ids and weights of a layer from its logits are hq_route_topk's, bit for bit."""
+    g = _gen(e)
+    q = hq.w8a8_block()
+    gu, dn = hq.MoePlan(256, 128, q, e, 64, "silu_mul_qfp8"), hq.MoePlan(128, 128, q, e, 64, "topk_combine")
+    ones = lambda n, k: (torch.full((e, n, k), 0x38, dtype=torch.uint8, device=DEV), torch.full((e, n // 128, k // 128), 0.01, device=DEV))
+    wm = (*gu.repack(*ones(256, 128)), *dn.repack(*ones(128, 128)))
+    for t in (1, 2, 16, 24):
+        x = torch.randn(t, 128, generator=g, device=DEV, dtype=torch.bfloat16)
+        lg = (torch.randn(t, e, generator=g, device=DEV) * 4).to(dt)
+        lg[0, 1] = -math.inf
+        y, ids, w = hq.moe_layer_routed(gu, dn, x, lg, topk, *wm, renormalize=renorm)
+        ri, rw = hq.route_topk(lg, topk, renormalize=renorm)
+        torch.cuda.synchronize()
+        assert torch.equal(ids, ri) and torch.equal(w, rw)
