@@ -1322,7 +1322,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       }
       // down: column windows, each the GEMM and then the sum of its rows
       const int64_t win = down ? b8_window(p, t, topk) : 1;
-      b.rows16 = reinterpret_cast<int16_t*>(rows16);
+      b.rows16 = rows16;
       b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win) * 2));
       for (int64_t c = 0; down && c < N && err == hipSuccess; c += win) {
         b.col0 = (int)c;

@@ -44,9 +44,9 @@ struct B8Args {
   float* out_scale;        // gate_up: scales of the requantised rows [N/256][out_rows]
   int out_rows;
   // down: this launch's columns [col0, col0 + ncol) of N, col0 a multiple of
-  // 256; the slots' rows as 16-bit integers with a scale per 64 columns
+  // 256; the slots' rows with a scale per 64 columns
   int col0, ncol;
-  int16_t* rows16;         // [n_slots][ncol]
+  uint16_t* rows16;        // [n_slots][ncol] fp16
   float* row_scale;        // [n_slots][ncol / 64]
   int cols_wg;             // short K: columns a workgroup walks
 };

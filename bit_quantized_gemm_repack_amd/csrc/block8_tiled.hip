@@ -142,12 +142,15 @@ __device__ __forceinline__ void b8_rows16(uint8_t* buf, int lane, V&& value, S&&
   __builtin_amdgcn_wave_barrier();
 }
 
-// A slot's weighted row of the down GEMM, 64 columns a wave: the fp32 sums o
-// as 16-bit integers q = o / 2^e with the one 2^e that brings the largest to
-// 15 bits, and topk_w * 2^e as their scale.  Half the bytes of fp32 rows, each
-// off by at most half a unit (one at the very top), 2^-15 of the 64 columns'
-// largest; bf16 rows are off by 2^-9 of each value.  A value that is not finite
-// makes the scale NaN, and so the 64 columns.
+// A slot's row of the down GEMM, 64 columns a wave, on its way into the sum over
+// the token's experts: fp16 values o / 2^e, with the 2^e that brings the 64 columns'
+// largest finite one to [2^14, 2^15), and topk_w * 2^e as their scale.  Half the
+// bytes of fp32 rows, which are a third of the layer's traffic (4096 tokens with
+// fp16 outputs: 980 us with fp32 rows, 739 with these).  Each value is off by at most
+// 2^-11 of itself down to 2^-29 of the largest, and below that by 2^-39 of the
+// largest: an eighth of bf16's rounding, and as much as fp16's own.  (Integers of
+// one step for the 64 columns were finer beside a large column and lost the others.)
+// What is not finite stays in its column.
 template <int MB>
 __device__ __forceinline__ void b8_store_rows(const B8Args& p, const int32_t* ids, const float* tw, uint8_t* buf, int col,
                                               int lane, const f4_t (&acc)[MB][4]) {
@@ -158,7 +161,10 @@ __device__ __forceinline__ void b8_store_rows(const B8Args& p, const int32_t* id
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) top = max(top, b8_mag(acc[mb][j][q]));
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t m = b8_mag(acc[mb][j][q]);
+        top = max(top, m < 0x7F800000u ? m : 0u);
+      }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     const int e = max((int)(top >> 23) - 127 - 14, -126);  // the largest is below 2^(e + 15)
@@ -169,18 +175,16 @@ __device__ __forceinline__ void b8_store_rows(const B8Args& p, const int32_t* id
     b8_rows16<4>(
         buf, lane,
         [&](int j) {
-          int v[4];
+          uint32_t v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            v[q] = (int)__builtin_amdgcn_fmed3f(__builtin_rintf(acc[mb][j][q] * inv), 32767.f, -32767.f);
-          return uint2{((uint32_t)v[0] & 0xFFFFu) | ((uint32_t)v[1] << 16), ((uint32_t)v[2] & 0xFFFFu) | ((uint32_t)v[3] << 16)};
+          for (int q = 0; q < 4; ++q) v[q] = float_to_f16_bits(acc[mb][j][q] * inv);
+          return uint2{v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
         },
         [&](int byte, uint4 v) {
           if (live) *reinterpret_cast<uint4*>(o + byte) = v;
         });
     if (live && lane < 16)
-      p.row_scale[(int64_t)id * (p.ncol / 64) + (col - p.col0) / 64] =
-          top < 0x7F800000u ? tw[16 * mb + c16] * __builtin_amdgcn_ldexpf(1.f, e) : __builtin_nanf("");
+      p.row_scale[(int64_t)id * (p.ncol / 64) + (col - p.col0) / 64] = tw[16 * mb + c16] * __builtin_amdgcn_ldexpf(1.f, e);
   }
 }
 
@@ -640,11 +644,11 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
 #endif
 }
 
-// y[t][col0 + c] = RNE(sum over the token's topk slots of q * scale), in slot
-// order; eight columns a thread.  Bound by reading the rows: a window of 4096
-// tokens, 235 MB, 43 us, 6.1 TB/s with its output.  The rows are done with once
-// read: loads that do not keep them leave the cache to the next window's (a layer
-// of 4096 tokens 648 us against 661).
+// y[t][col0 + c] = RNE(sum over the token's topk slots of row * scale), in slot
+// order; eight columns a thread, the rows as b8_store_rows leaves them.  Bound by
+// reading the rows: a window of 4096 tokens, 235 MB, 43 us, 6.1 TB/s with its output.
+// The rows are done with once read: loads that do not keep them leave the cache to
+// the next window's (a layer of 4096 tokens 648 us against 661).
 __global__ void __launch_bounds__(256) b8_combine_kernel(const u4_t* __restrict__ rows, const float* __restrict__ scale,
                                                          int topk, int n, int col0, int ncol, int64_t elems,
                                                          uint4* __restrict__ y, int out_bf16) {
@@ -656,9 +660,8 @@ __global__ void __launch_bounds__(256) b8_combine_kernel(const u4_t* __restrict_
     for (int j = 0; j < topk; ++j) {
       const u4_t w = __builtin_nontemporal_load(rows + (t * topk + j) * ncol8 + c);
       const float f = scale[(t * topk + j) * strips + c / 8];
-      const uint32_t u[4] = {w[0], w[1], w[2], w[3]};
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = fmaf((float)(int16_t)(u[q >> 1] >> (16 * (q & 1))), f, v[q]);
+      for (int q = 0; q < 8; ++q) v[q] = fmaf(f16_bits_to_float((w[q >> 1] >> (16 * (q & 1))) & 0xFFFFu), f, v[q]);
     }
     uint32_t o[4];
 #pragma unroll

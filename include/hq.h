@@ -399,7 +399,11 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  *                             intermediate of slot sorted_ids[r];
  *                             out = y [t, n] (plan out dtype),
  *                             y[tok] = sum_j topk_w[tok, j] * (a_row . W_e^T):
- *                             each slot's weighted row, rounded to bf16, goes
+ *                             each slot's weighted row, rounded to bf16
+ *                             (W8A8-BLOCK: to fp16 with a power of two per 64
+ *                             columns, each value off by at most 2^-11 of itself
+ *                             down to 2^-29 of the 64 columns' largest, and below
+ *                             by 2^-39 of that one), goes
  *                             to the workspace, then a second kernel sums a
  *                             token's topk rows in fp32 in slot order and
  *                             rounds once, so the result is deterministic.
