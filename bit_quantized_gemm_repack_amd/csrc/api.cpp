@@ -226,8 +226,9 @@ static const hq_tuning* tuned_for(const hq_plan* p, int64_t m) {
 }
 
 // fp8 x fp8 with 128-block scales (block8.h).  The rules follow a sweep on
-// MI355X of every shape and K split over 1 .. 2048 rows and (N, K) = (576,
-// 7168), (2112, 7168), (4096, 7168), (7168, 2048), (14336, 4096), (4096, 14336),
+// MI355X of the shapes and K splits (tiles under 64 rows up to 256 rows only: their
+// use beyond, with N under 2048, is the rule carried on) over 1 .. 2048 rows and (N,
+// K) = (576, 7168), (2112, 7168), (4096, 7168), (7168, 2048), (14336, 4096), (4096, 14336),
 // (24576, 1536), (1024, 1024), weights from memory: their choice took 1.2 %
 // more than the best one on the geometric mean, 19 % at most.
 static Exec choose_exec_b8(const hq_plan* p, int64_t m, const hq_tuning& u) {

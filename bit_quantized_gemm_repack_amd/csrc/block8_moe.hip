@@ -14,13 +14,16 @@
 // slots of an expert from the logits in every workgroup took 9 us of 8 tokens'
 // 76, the launch takes 4.
 //
-// 256 experts, top 8, H = 7168, I = 256, in a graph, and the experts' bytes over
-// a streaming read's 6 TB/s: 1 token 17.3 us (7.3), 2 29 (15), 4 45 (28), 8 67
-// (49), 13 92 (71), 16 102 (80); 24 tokens 154, where the aligned path takes 128.
+// 256 experts, top 8, H = 7168, I = 256, in a graph over four sets of inputs, and
+// the bytes of the experts that those hit over a streaming read's 6 TB/s: 1 token 18.3
+// us (7.3), 2 29.2 (14.5), 4 42.9 (27), 8 64 (47), 13 90 (67), 16 97 (76); 24 tokens
+// 150 (96), where the aligned path takes 117 (16 tokens 106).  With fewer experts
+// the two paths cross earlier: 64 experts, top 8, H = 2048, I = 768 at 4 tokens (8
+// tokens 68 us against 51), 8 and 16 experts, top 2, H = 4096 between 10 and 16.
 // More than one token's weights are read past the caches (4 tokens 42 us against
 // 45, 13 88.6 against 93); one token's may stay there (17.3 against 18.4).
 // About 9 us are the two kernels' launches and their chains of dependent loads
-// (ids, weights); the rest runs at 5.6 TB/s.
+// (ids, weights); the rest runs at 4.5 .. 5 TB/s.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -187,7 +190,8 @@ __device__ inline float row_sum(float v) {
 // over 16 lanes for four tokens.  Lane l keeps experts l, l + 16, ...  16-bit
 // logits carry their expert in the key's low half (the lower the larger), which
 // makes the keys unique and a choice one comparison per key.  Bound by
-// instructions: 16383 x 160 bf16 top 6, 6.0 us (a wave per token 12), 6 MB.
+// instructions: 16383 x 160 bf16 top 6, 7.1 us in a graph (a wave per token about
+// twice that), 6 MB.
 template <int LT, int NPL>
 __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict__ logits, int t, int E, int topk, int renorm,
                                                          int32_t* __restrict__ ids, float* __restrict__ w) {
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(256) route_rows_kernel(const void* __restrict_
 //           once, more with 4.
 //   wide    128 outputs a workgroup, 16 a wave over all of K: no sums to join,
 //           and the workgroup holds a whole scale block, so that it writes
-//           codes and scales.  13 tokens 57 us, 5.5 TB/s.
+//           codes and scales.  13 tokens 57 us, 4.8 TB/s (272 MB).
 // The products go through fp16 (b8_mfma_exact): their sums are quantised again.
 // One more row of workgroups writes the routing where there are logits, and
 // otherwise the units that the down kernel walks.
@@ -607,8 +611,8 @@ __global__ void __launch_bounds__(64 * NW) few_gate_up(B8FewArgs p) {
 // ---------------------------------------------------------------------------
 // down + combine: grid (16-column blocks, tiles of 16 tokens).  The tile's
 // activation rows lie quantised in LDS (as many 128-k groups at a time as
-// fit); the waves take the (expert, group) steps in turn.  One token 6.0 us
-// (14.7 MB), 13 tokens 32 us (141 MB).
+// fit); the waves take the (expert, group) steps in turn.  One token 6.0 .. 6.5 us
+// (14.7 MB), 13 tokens 30 us (136 MB).
 // ---------------------------------------------------------------------------
 template <bool WIDE, bool ONE, int ST>
 __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(4))) few_down(B8FewArgs p) {
@@ -779,7 +783,10 @@ int launch_route(int64_t t, int E, int topk, int logit_type, const void* logits,
   // One token goes as the layer's gate_up routes it, whose weights are so the same
   // bits.  64 experts or fewer leave a wave per token nothing to gain; for more, a wave
   // has the shorter chain and sixteen lanes the fewer instructions (256 experts,
-  // top 8, fp32: 4096 tokens 6.0 us by waves, 6.5 by rows, 16383 15.6 and 11.0)
+  // top 8, fp32: 4096 tokens 6.0 us by waves, 6.5 by rows, 16383 15.6 and 11.0).
+  // The border was set for 256 experts; fewer would cross earlier (6143 tokens by
+  // waves and 6144 by rows: 128 experts 6.4 and 4.2 us, 160 6.7 and 5.2, 192 7.1 and
+  // 6.0, 256 7.1 both).
   if (t > 1 && topk <= 16 && (E <= 64 || (E <= 256 && t >= 6144))) {
     const dim3 rows((unsigned)((t + 15) / 16));
     auto go = [&]<int LT>() -> int {

@@ -10,8 +10,9 @@
 // run along the rows, so that memory sees runs of 1 KiB (16 rows of one column:
 // 5 % more).  Ordinary loads: what the kernel before has left in the last-level
 // cache is found there (4096 x 7168 15.9 us against 19.6 with loads that pass it
-// by).  One token of 7168: 2.2 us, a launch; SiLU of 8191 x 2048, 84 MB: 18.9 us a
-// call, 4.4 TB/s (a large copy reaches 4.9); 4096 x 7168, 88 MB: 5.5 TB/s.
+// by).  One token of 7168: 2.6 us in a graph, a launch; SiLU of 8191 x 2048, 84 MB:
+// 18.9 .. 20.8 us a call, 4.0 .. 4.4 TB/s (a large copy reaches 4.9); 4096 x 7168, 88
+// MB: 15.9 us with x in the last-level cache, 18.5 in a layer of that many tokens.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -10,9 +10,9 @@
 //
 // P_g over the 128 k of group g is one matrix instruction; the promotion to fp32
 // is four multiply-adds a lane and free beside the loads.  One row of (4096,
-// 7168), 29.4 MB: 7.0 us as a kernel, of which about 2 are the launch and the
-// first loads' latency, 5.9 TB/s over the rest; 33 rows of (576, 7168) with three
-// row blocks 7.8 us, latency alone.
+// 7168), 29.4 MB: 7.0 .. 7.8 us as a kernel, of which about 2 are the launch and the
+// first loads' latency; 33 rows of (576, 7168) with three row blocks 7.8 us, latency
+// alone: a wave's 14 groups come in two rings of loads.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 

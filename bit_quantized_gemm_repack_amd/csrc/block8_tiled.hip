@@ -7,11 +7,12 @@
 // per lane are one token's, so the promotion to the fp32 accumulator is four
 // fused multiply-adds with one factor sa * sw.
 //
-// What bounds it: 4096 x 4096 x 7168 takes 104 us, 2320 TFLOP/s (the library's
+// What bounds it: 4096 x 4096 x 7168 takes 104 .. 106 us, 2320 TFLOP/s (the library's
 // product with one scale per tensor takes 83, the instruction alone would take
 // 53): the operand reads from LDS beside the matrix and vector instructions, and
 // the clock, which the same product of zeros keeps higher (88 us).  200 x 14336
-// x 4096 takes 22.6 us: without its loads 17, without its products 21.  Up to 64
+// x 4096 takes 22.6 us, 30 with its weight from memory: every row tile reads the
+// weight again; without its loads 17, without its products 21.  Up to 64
 // rows an expert the grouped products read weights at 5.0 .. 5.8 TB/s.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
@@ -533,8 +534,8 @@ __global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((a
 // the workgroup walks its column tiles in one stream of weight loads, with no
 // barrier and no refill between tiles (with two or four groups of K per tile
 // the loads' latency at each tile's start would cost as much as its math).
-// 256 experts, top 8, H = 7168, I = 256: 509 tokens 105 us (470 MB of weights and
-// 58 of rows, 5.0 TB/s), 4096 tokens two windows of 115 us (5 TB/s).
+// 256 experts, top 8, H = 7168, I = 256: 509 tokens 105 us (444 MB of weights and
+// 58 of rows, 4.8 TB/s), 4096 tokens two windows of 118 us (5 TB/s).
 template <int MB>
 __device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int m0, int64_t ex, int c0, int c1) {
 #if defined(__HIP_DEVICE_COMPILE__)
