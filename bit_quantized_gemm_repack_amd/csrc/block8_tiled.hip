@@ -13,7 +13,7 @@
 // the clock, which the same product of zeros keeps higher (88 us).  200 x 14336
 // x 4096 takes 22.6 us, 30 with its weight from memory: every row tile reads the
 // weight again; without its loads 17, without its products 21.  Up to 64
-// rows an expert the grouped products read weights at 5.0 .. 5.8 TB/s.
+// rows an expert the grouped products read weights at 4.8 .. 5.3 TB/s.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
