@@ -38,6 +38,7 @@ F16, BF16, F32, FP8_E4M3, INT8, U4, FP4_E2M1, E8M0, I32, U8, U2, U3, I4 = range(
 ZP_NONE, ZP_FIXED, ZP_PER_GROUP_U4 = range(3)
 ASCALE_NONE, ASCALE_PER_TOKEN_F32, ASCALE_MX_E8M0, ASCALE_BLOCK_F32 = range(4)
 GEMM_DENSE, GEMM_GROUPED = range(2)
+NORM_SAME, NORM_FP8, NORM_INT8, NORM_FP8_BLOCK, NORM_MXFP4 = range(5)
 EPI_NONE, EPI_SILU_MUL, EPI_SILU_MUL_QFP8, EPI_TOPK_COMBINE, EPI_I32_ACC = range(5)
 PEAK_F16, PEAK_BF16, PEAK_FP8, PEAK_FP8_FP4, PEAK_FP4, PEAK_INT8 = range(6)
 MFMA_AUTO, MFMA_F16, MFMA_BF16, MFMA_FP8, MFMA_INT8, MFMA_FP8_FP4, MFMA_FP4 = range(7)
@@ -45,6 +46,7 @@ _MFMA = {None: MFMA_AUTO, "auto": MFMA_AUTO, "f16": MFMA_F16, "bf16": MFMA_BF16,
          "int8": MFMA_INT8, "fp8xfp4": MFMA_FP8_FP4, "fp4": MFMA_FP4}
 
 _DT = {"f16": F16, "bf16": BF16, "fp8": FP8_E4M3, "int8": INT8}
+_NORM = {None: NORM_SAME, "fp8": NORM_FP8, "int8": NORM_INT8, "fp8_block": NORM_FP8_BLOCK, "mxfp4": NORM_MXFP4}
 _EPI = {"none": EPI_NONE, "silu_mul": EPI_SILU_MUL, "silu_mul_qfp8": EPI_SILU_MUL_QFP8,
         "topk_combine": EPI_TOPK_COMBINE, "i32_acc": EPI_I32_ACC}
 
@@ -218,6 +220,9 @@ _SIGS = {
                          [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
     "hq_quantize_blocks": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int] +
                            [ctypes.c_void_p] * 4),
+    "hq_rms_norm": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                   ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_int,
+                                   ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 3),
     "hq_plan_autotune": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 6 +
                          [ctypes.c_size_t, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p,
                           ctypes.POINTER(AutotuneResult)]),
@@ -816,6 +821,69 @@ def quantize_blocks(x: torch.Tensor, silu_mul: bool = False, codes: Optional[tor
     _run(dev, lib().hq_quantize_blocks, m, k, BF16 if x.dtype == torch.bfloat16 else F16, 1 if silu_mul else 0,
          x.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return codes, scales
+
+
+def _norm_rows(t, name, x, m, k):
+    """A [m, k] operand of rms_norm beside x: rows of any stride, contiguous inside."""
+    if not isinstance(t, torch.Tensor) or t.device != x.device or t.dtype != x.dtype or t.shape != (m, k):
+        raise ValueError(f"{name} must be {x.dtype} [{m}, {k}] on x's device")
+    if k > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             out: Optional[str] = None, residual_out: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of fp16 / bf16 rows x [m, k], or of h = x + residual
+    (rounded to x's type), times weight [k] (x's type or float32), in one kernel
+    (see hq_rms_norm).  out: None gives y in x's type; "fp8" or "int8" (codes
+    uint8 / int8 [m, k], scales float32 [m]), "fp8_block" (codes uint8 [m, k], scales
+    float32 [k/128, m]) and "mxfp4" (codes uint8 [m, k/2], e8m0 uint8 [k/128, m, 4])
+    the (a, a_scale) of the products that take them, quantised from the fp32 norm.
+    x, residual and residual_out may be slices of columns of wider tensors.
+    Returns y, or (codes, scales); with a residual h comes last: (y, h) or (codes,
+    scales, h), written into residual_out where that is given (which may be x or
+    the residual)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16) or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be fp16 / bf16 [m, k] with contiguous rows")
+    if out not in _NORM:
+        raise ValueError(f"out must be None or one of {sorted(o for o in _NORM if o)}")
+    m, k = x.shape
+    if not isinstance(weight, torch.Tensor) or weight.shape != (k,) or weight.dtype not in (x.dtype, torch.float32) or \
+            not _same_device(x.device, weight):
+        raise ValueError(f"weight must be {x.dtype} or float32 [{k}], contiguous and on x's device")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out goes with a residual")
+    else:
+        _norm_rows(residual, "residual", x, m, k)
+        if residual_out is None:
+            residual_out = x.new_empty((m, k))
+        else:
+            _norm_rows(residual_out, "residual_out", x, m, k)
+    scales = None
+    if out is None:
+        y = x.new_empty((m, k))
+    elif out == "mxfp4":
+        y = x.new_empty((m, k // 2), dtype=torch.uint8)
+        scales = x.new_empty((k // 128, m, 4), dtype=torch.uint8)
+    else:
+        y = x.new_empty((m, k), dtype=torch.int8 if out == "int8" else torch.uint8)
+        scales = x.new_empty((k // 128, m) if out == "fp8_block" else (m,), dtype=torch.float32)
+
+    def stride(t):  # of one row it says nothing
+        return 0 if t is None else (t.stride(0) if m > 1 else k)
+
+    dt = BF16 if x.dtype == torch.bfloat16 else F16
+    _run(x.device, lib().hq_rms_norm, m, k, dt, _ptr(x), stride(x), _ptr(residual), stride(residual),
+         F32 if weight.dtype == torch.float32 else dt, _ptr(weight), float(eps), _NORM[out], _ptr(residual_out),
+         stride(residual_out), _ptr(y), _ptr(scales))
+    r = (y,) if scales is None else (y, scales)
+    if residual is not None:
+        r += (residual_out,)
+    return r if len(r) > 1 else y
 
 
 def mx_scales_group_major(e8m0_rows: torch.Tensor) -> torch.Tensor:

@@ -20,6 +20,7 @@
 #include "block8.h"
 #include "hq_internal.h"
 #include "jit.h"
+#include "norm.h"
 
 namespace {
 
@@ -1784,6 +1785,49 @@ hq_status hq_quantize_mxfp4(int64_t m, int64_t k, hq_dtype in, const void* x, vo
   const int err = hq::launch_quantize_mx(m, k, in == HQ_BF16, x, codes, e8m0, stream);
   hq::arm_timing({nullptr, nullptr});
   if (err != hipSuccess) return fail(HQ_ERR_HIP, "quantize launch: %s", hipGetErrorString((hipError_t)err));
+  return ok();
+}
+
+hq_status hq_rms_norm(int64_t m, int64_t k, hq_dtype x_type, const void* x, int64_t x_stride, const void* residual,
+                      int64_t r_stride, hq_dtype w_type, const void* weight, float eps, hq_norm_kind kind, void* h,
+                      int64_t h_stride, void* out, void* scale, void* stream) {
+  const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
+  if (x_type != HQ_F16 && x_type != HQ_BF16) return fail(HQ_ERR_UNSUPPORTED, "x must be fp16 or bf16");
+  if (w_type != x_type && w_type != HQ_F32) return fail(HQ_ERR_UNSUPPORTED, "weight must be of x's type or fp32");
+  if (kind < HQ_NORM_SAME || kind > HQ_NORM_MXFP4) return fail(HQ_ERR_INVALID_ARG, "unknown output kind %d", (int)kind);
+  const bool blocks = kind == HQ_NORM_FP8_BLOCK || kind == HQ_NORM_MXFP4;
+  if (m < 0 || m > (int64_t(1) << 24)) return fail(HQ_ERR_INVALID_ARG, "m out of range [0, 2^24]");
+  if (k < 8 || k % 8) return fail(HQ_ERR_INVALID_ARG, "k must be a multiple of 8");
+  if (blocks && k % 128) return fail(HQ_ERR_INVALID_ARG, "k must be a multiple of 128 for a scale per block");
+  if (k > 65536) return fail(HQ_ERR_UNSUPPORTED, "k above 65536");
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(HQ_ERR_INVALID_ARG, "eps must be a finite number of at least 0");
+  if (m == 0) return ok();
+  if (!x || !weight || !out) return fail(HQ_ERR_INVALID_ARG, "null device pointer");
+  if ((residual == nullptr) != (h == nullptr)) return fail(HQ_ERR_INVALID_ARG, "a residual and h go together");
+  if ((kind == HQ_NORM_SAME) != (scale == nullptr)) return fail(HQ_ERR_INVALID_ARG, "scale goes with a quantised output");
+  if (x_stride < 0 || x_stride % 8 || (residual && (r_stride < 0 || r_stride % 8 || h_stride % 8)))
+    return fail(HQ_ERR_INVALID_ARG, "row strides must be multiples of 8 elements");
+  if (h && h_stride < k) return fail(HQ_ERR_INVALID_ARG, "the rows of h overlap");
+  for (const void* p : {x, residual, weight, (const void*)h, (const void*)out, (const void*)scale})
+    if (!aligned16(p)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  hq::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.h = h;
+  a.out = out;
+  a.scale = scale;
+  a.x_stride = x_stride / 8;
+  a.r_stride = r_stride / 8;
+  a.h_stride = h_stride / 8;
+  a.m = (int)m;
+  a.k8 = (int)(k / 8);
+  a.eps = eps;
+  a.w_f32 = w_type == HQ_F32;
+  hq::arm_timing(ev);
+  const int err = hq::launch_rms_norm(x_type == HQ_BF16, (int)kind, a, stream);
+  hq::arm_timing({nullptr, nullptr});
+  if (err != hipSuccess) return fail(HQ_ERR_HIP, "norm launch: %s", hipGetErrorString((hipError_t)err));
   return ok();
 }
 

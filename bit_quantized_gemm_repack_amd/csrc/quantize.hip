@@ -31,6 +31,7 @@
 #include "device_common.h"
 #include "hq_internal.h"
 #include "launch.h"
+#include "mx4_device.h"
 
 namespace hq {
 
@@ -129,25 +130,6 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const u4_t* __restr
 // (2 = the largest E2M1 exponent), clamped to [-127, 127], X = 0 for an
 // all-zero block; elements RNE_E2M1(v / 2^X) saturated to +-6.  The scaling by
 // 2^-X is exact (ldexp), so every decision is an exact comparison.
-
-// Round-to-nearest-even fp32 -> E2M1 code, saturating at 6; -0 gives code 0.
-// Below 1 the spacing is 0.5 (code = rint(2|x|)); above, the 23-bit mantissa
-// is rounded to 1 bit (a carry moves into the exponent field).
-__device__ inline uint32_t e2m1_code_rne(float x) {
-  const uint32_t sign = (__float_as_uint(x) >> 28) & 0x8u;
-  const float a = fminf(fabsf(x), 6.f);
-  uint32_t code;
-  if (a < 1.f) {
-    code = (uint32_t)__builtin_rintf(a * 2.f);
-  } else {
-    const uint32_t bits = __float_as_uint(a);
-    const uint32_t e = (bits >> 23) - 127u + 1u;  // exponent field, bias 1
-    const uint32_t mant = bits & 0x7FFFFFu;
-    const uint32_t r = (mant + 0x1FFFFFu + ((mant >> 22) & 1u)) >> 22;  // 0..2
-    code = (e << 1) + r;
-  }
-  return code == 0 ? 0u : (sign | code);
-}
 
 // One thread per 32-element block: 64 input bytes in, 16 code bytes and one
 // E8M0 byte out (consecutive threads, consecutive blocks of a row).  The

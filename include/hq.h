@@ -568,6 +568,45 @@ hq_status hq_quantize_blocks(int64_t m, int64_t k, hq_dtype in, int silu_mul, co
 hq_status hq_quantize_mxfp4(int64_t m, int64_t k, hq_dtype in, const void* x, void* codes, uint8_t* e8m0,
                             void* stream);
 
+/* Root-mean-square norm with the residual's addition, in 16 bits or quantised
+ * for the product that reads it:
+ *   h[r, j] = x[r, j] + residual[r, j], rounded to x's type (x itself where
+ *             residual is NULL)
+ *   y[r, j] = h[r, j] weight[j] / sqrt(mean_j(h[r, j]^2) + eps), formed in fp32
+ * and, by `kind`,
+ *   HQ_NORM_SAME       out = y rounded to x's type, [m, k]; scale NULL
+ *   HQ_NORM_FP8        out, scale = y by row as hq_quantize_per_token gives e4m3
+ *   HQ_NORM_INT8       the same with int8 codes
+ *   HQ_NORM_FP8_BLOCK  out, scale = y by row and 128 columns as
+ *                      hq_quantize_blocks gives them
+ *   HQ_NORM_MXFP4      out, scale = y by 32 columns as hq_quantize_mxfp4 gives them
+ * (y is not rounded to 16 bits first; a negative value that rounds to zero may
+ * give e4m3's code of -0.)
+ *   x, residual  device [m, k] fp16 / bf16 (x_type), rows x_stride / r_stride
+ *                elements apart (slices of columns of a wider tensor; 0 repeats a
+ *                row)
+ *   weight       device [k] in x_type or fp32 (w_type)
+ *   h            device [m, k] in x_type, rows h_stride elements apart; with a
+ *                residual only, else NULL.  It may be x or the residual themselves
+ *                (the same pointer and stride), no other overlap
+ * A row (HQ_NORM_FP8, _INT8) or block (the others) of y that holds an infinity or
+ * a NaN gets the scale NaN, and unspecified codes, so that the product's row is
+ * NaN.  The squares are summed in fp32: a row whose sum is past fp32's range gives
+ * zeros or NaN.
+ * k must be a multiple of 8 (128 for _FP8_BLOCK and _MXFP4) up to 65536, the
+ * strides multiples of 8, the pointers 16-byte aligned, m at most 2^24, eps at least 0;
+ * m = 0 is a no-op.  Honours hq_time_next_launch (one kernel). */
+typedef enum hq_norm_kind {
+  HQ_NORM_SAME = 0,
+  HQ_NORM_FP8 = 1,
+  HQ_NORM_INT8 = 2,
+  HQ_NORM_FP8_BLOCK = 3,
+  HQ_NORM_MXFP4 = 4
+} hq_norm_kind;
+hq_status hq_rms_norm(int64_t m, int64_t k, hq_dtype x_type, const void* x, int64_t x_stride, const void* residual,
+                      int64_t r_stride, hq_dtype w_type, const void* weight, float eps, hq_norm_kind kind, void* h,
+                      int64_t h_stride, void* out, void* scale, void* stream);
+
 /* ---- Autotuning (dense plans) ----------------------------------------
  * The heuristic maps (format, n, k, m) to an execution choice by rules taken
  * from sweeps; the pages list that rule-based selection among the
