@@ -38,6 +38,27 @@ __device__ inline uint32_t mx4_scale(uint32_t top_bits) {
 // elements either way).
 __device__ inline float mx4_scaled(float v, uint32_t scale) { return __builtin_amdgcn_ldexpf(v, 127 - (int)scale); }
 
+// Eight values of a block -> a word of codes, the first in the lowest bits: the
+// hardware conversion, which agrees with e2m1_code_rne(mx4_scaled()) for every value
+// that a block's scale leaves below 8 (checked exhaustively) but for the codes of -0,
+// and a quarter of its instructions.  Blocks at the exponents' end go the long way.
+__device__ inline uint32_t mx4_word(const float (&v)[8], uint32_t scale) {
+  uint32_t w = 0u;
+  if (scale == 0u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w |= e2m1_code_rne(mx4_scaled(v[j], 0u)) << (4 * j);
+    return w;
+  }
+#if defined(__HIP_DEVICE_COMPILE__)
+  const float s = __uint_as_float(scale << 23);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
+#endif
+  return w & (0x77777777u | (((w & 0x77777777u) + 0x77777777u) & 0x88888888u));
+}
+
 // Maximum over the four lanes that share lane / 4, in each of them.
 __device__ inline uint32_t quad_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));  // quad_perm 1 0 3 2

@@ -13,7 +13,10 @@
 // maxima need one pass over registers and one meeting of the row's threads.  h w
 // is exact for 16-bit weights, so y rounds once more than the factor.
 //
-// Bound by memory: x, r and h are moved once.
+// Bound by memory: x, r and h are moved once.  bf16 with residual, in a graph: 8191
+// x 4096 to e4m3 by row 44.6 us, 5.3 TB/s (a large copy reaches 5.0), 8191 x 7168 to
+// MXFP4 70 us, 5.5 TB/s; one row of 7168 to MXFP4 3.1 us, a launch and a chain of
+// loads, sums and codes.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -182,9 +185,10 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_kernel(NormArgs p)
     for (int i = 0; i < C; ++i) {
       const int c = lane + T * i;
       const uint32_t s = mx4_scale(b8_mag(__uint_as_float(quad_max(top[i])) * f));
-      uint32_t word = 0u;
+      float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) word |= e2m1_code_rne(mx4_scaled(t[i][j] * f, s)) << (4 * j);
+      for (int j = 0; j < 8; ++j) y[j] = t[i][j] * f;
+      const uint32_t word = mx4_word(y, s);
       // the four blocks' bytes of 128 columns, in their first lane
       uint32_t all = s;
 #pragma unroll
@@ -204,12 +208,23 @@ int launch_out(const NormArgs& a, hipStream_t s) {
     constexpr int ROWS = T < 256 ? 256 / T : 1;
     return (int)launch_timed(rms_norm_kernel<BF16, OUT, T, C>, dim3((unsigned)((a.m + ROWS - 1) / ROWS)), dim3(T < 256 ? 256 : T), 0, s, a);
   };
+  // The shape that leaves the fewest threads idle, with the more threads the fewer
+  // rows there are (us, bf16 with residual, to 16 bits / e4m3 by row / MXFP4):
+  //   k = 7168, 1 row: 512 threads of two chunks 3.0 / 3.5 / 3.1, 256 of four 3.4 /
+  //   4.3 / 3.7, 64 of fourteen 5.8 / 9.1 / 7.4; 8191 rows: 82 / 74 / 70, 82 / 74 / 70,
+  //   91 / 121 / 80
+  //   k = 4096, 1 row: 512 of one 2.5 / 3.0 / 2.6, 256 of two 2.8 / 3.3 / 2.9; 8191
+  //   rows: 46 / 48 / 40, 47 / 45 / 41
+  //   k = 256, 33 rows: 64 of one 2.4 / 2.8 / 2.5, 16 of two 2.6 / 3.2 / 2.9; 100000
+  //   rows: 40 / 59 / 40, 39 / 35 / 33
   const int k8 = a.k8;
   if (k8 <= 16) return go.template operator()<16, 1>();
+  if (k8 <= 32 && a.m >= 2048) return go.template operator()<16, 2>();
   if (k8 <= 64) return go.template operator()<64, 1>();
+  if (k8 <= 128) return go.template operator()<64, 2>();
   if (k8 <= 256) return go.template operator()<256, 1>();
-  if (k8 <= 512) return go.template operator()<256, 2>();
-  if (k8 <= 1024) return go.template operator()<256, 4>();
+  if (k8 <= 512) return a.m <= 256 ? go.template operator()<512, 1>() : go.template operator()<256, 2>();
+  if (k8 <= 1024) return go.template operator()<512, 2>();
   if (k8 <= 2048) return go.template operator()<1024, 2>();
   if (k8 <= 4096) return go.template operator()<1024, 4>();
   if (k8 <= 8192) return go.template operator()<1024, 8>();
