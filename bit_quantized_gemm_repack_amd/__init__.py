@@ -38,6 +38,7 @@ F16, BF16, F32, FP8_E4M3, INT8, U4, FP4_E2M1, E8M0, I32, U8, U2, U3, I4 = range(
 ZP_NONE, ZP_FIXED, ZP_PER_GROUP_U4 = range(3)
 ASCALE_NONE, ASCALE_PER_TOKEN_F32, ASCALE_MX_E8M0, ASCALE_BLOCK_F32 = range(4)
 GEMM_DENSE, GEMM_GROUPED = range(2)
+SCORE_SIGMOID, SCORE_SOFTMAX = range(2)
 NORM_SAME, NORM_FP8, NORM_INT8, NORM_FP8_BLOCK, NORM_MXFP4 = range(5)
 EPI_NONE, EPI_SILU_MUL, EPI_SILU_MUL_QFP8, EPI_TOPK_COMBINE, EPI_I32_ACC = range(5)
 PEAK_F16, PEAK_BF16, PEAK_FP8, PEAK_FP8_FP4, PEAK_FP4, PEAK_INT8 = range(6)
@@ -46,6 +47,7 @@ _MFMA = {None: MFMA_AUTO, "auto": MFMA_AUTO, "f16": MFMA_F16, "bf16": MFMA_BF16,
          "int8": MFMA_INT8, "fp8xfp4": MFMA_FP8_FP4, "fp4": MFMA_FP4}
 
 _DT = {"f16": F16, "bf16": BF16, "fp8": FP8_E4M3, "int8": INT8}
+_SCORE = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
 _NORM = {None: NORM_SAME, "fp8": NORM_FP8, "int8": NORM_INT8, "fp8_block": NORM_FP8_BLOCK, "mxfp4": NORM_MXFP4}
 _EPI = {"none": EPI_NONE, "silu_mul": EPI_SILU_MUL, "silu_mul_qfp8": EPI_SILU_MUL_QFP8,
         "topk_combine": EPI_TOPK_COMBINE, "i32_acc": EPI_I32_ACC}
@@ -213,6 +215,9 @@ _SIGS = {
     "hq_quantize_mxfp4": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p] * 4),
     "hq_route_topk": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                      ctypes.c_int] + [ctypes.c_void_p] * 3),
+    "hq_route_experts": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+                                        ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_float] + [ctypes.c_void_p] * 3),
     "hq_moe_few_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_size_t)]),
     "hq_moe_layer_few": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
@@ -1095,6 +1100,30 @@ def route_topk(logits: torch.Tensor, topk: int, renormalize: bool = True):
     w = logits.new_empty((t, topk), dtype=torch.float32)
     _run(logits.device, lib().hq_route_topk, t, experts, topk, _LOGITS[logits.dtype], logits.data_ptr(),
          1 if renormalize else 0, ids.data_ptr(), w.data_ptr())
+    return ids, w
+
+
+def route_experts(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, scoring: str = "sigmoid",
+                  groups: int = 1, group_topk: int = 1, group_best: int = 2, renormalize: bool = True, scale: float = 1.0):
+    """The topk experts of each row of logits [t, experts] (fp32, fp16 or bf16) by
+    score + bias, and their weights (see hq_route_experts).  scoring: "sigmoid" or
+    "softmax"; bias float32 [experts] counts for the choice only.  With groups > 1
+    only experts of the group_topk best groups are chosen, a group's score being the
+    sum of its group_best (1 or 2) best.  Returns (ids int32 [t, topk], weights
+    float32 [t, topk]), the (topk_ids, topk_w) of moe_layer."""
+    _dev(logits, "logits")
+    if logits.dim() != 2 or logits.dtype not in _LOGITS:
+        raise ValueError("logits must be fp32 / fp16 / bf16 [t, experts]")
+    if scoring not in _SCORE:
+        raise ValueError(f"scoring must be one of {sorted(_SCORE)}")
+    t, experts = logits.shape
+    if bias is not None and (not _same_device(logits.device, bias) or bias.dtype != torch.float32 or bias.shape != (experts,)):
+        raise ValueError(f"bias must be float32 [{experts}], contiguous and on the logits' device")
+    topk = int(topk)
+    ids = logits.new_empty((t, max(topk, 0)), dtype=torch.int32)
+    w = logits.new_empty((t, max(topk, 0)), dtype=torch.float32)
+    _run(logits.device, lib().hq_route_experts, t, experts, topk, _LOGITS[logits.dtype], logits.data_ptr(), _SCORE[scoring], _ptr(bias),
+         int(groups), int(group_topk), int(group_best), 1 if renormalize else 0, float(scale), ids.data_ptr(), w.data_ptr())
     return ids, w
 
 

@@ -21,6 +21,7 @@
 #include "hq_internal.h"
 #include "jit.h"
 #include "norm.h"
+#include "route.h"
 
 namespace {
 
@@ -1619,6 +1620,50 @@ hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_typ
     return fail(HQ_ERR_INVALID_ARG, "logits, topk_ids and topk_w must be aligned to their elements");
   hq::arm_timing(ev);
   const int err = hq::launch_route(t, num_experts, topk, lt, logits, renormalize, topk_ids, topk_w, stream);
+  hq::arm_timing({nullptr, nullptr});
+  if (err != hipSuccess) return fail(HQ_ERR_HIP, "route launch: %s", hipGetErrorString((hipError_t)err));
+  return ok();
+}
+
+hq_status hq_route_experts(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, hq_score scoring,
+                           const float* bias, int groups, int group_topk, int group_best, int renormalize, float scale,
+                           int32_t* topk_ids, float* topk_w, void* stream) {
+  const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
+  const int lt = logit_type_of(logit_type);
+  if (lt < 0) return fail(HQ_ERR_UNSUPPORTED, "logits must be fp32, fp16 or bf16");
+  if (scoring != HQ_SCORE_SIGMOID && scoring != HQ_SCORE_SOFTMAX) return fail(HQ_ERR_INVALID_ARG, "unknown scoring %d", (int)scoring);
+  if (t < 0 || t > (int64_t(1) << 24)) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, 2^24]");
+  if (num_experts < 1) return fail(HQ_ERR_INVALID_ARG, "num_experts must be >= 1");
+  if (num_experts > 1024) return fail(HQ_ERR_UNSUPPORTED, "routing covers up to 1024 experts");
+  if (groups < 1 || num_experts % groups) return fail(HQ_ERR_INVALID_ARG, "groups must divide the experts");
+  if (groups > 64) return fail(HQ_ERR_UNSUPPORTED, "routing covers up to 64 groups");
+  if (group_topk < 1 || group_topk > groups) return fail(HQ_ERR_INVALID_ARG, "group_topk must be 1..groups");
+  if (group_best != 1 && group_best != 2) return fail(HQ_ERR_INVALID_ARG, "group_best must be 1 or 2");
+  if (topk < 1 || topk > 64 || topk > group_topk * (num_experts / groups))
+    return fail(HQ_ERR_INVALID_ARG, "topk must be 1..64, at most the experts of group_topk groups");
+  if (renormalize != 0 && renormalize != 1) return fail(HQ_ERR_INVALID_ARG, "renormalize must be 0 or 1");
+  if (!std::isfinite(scale)) return fail(HQ_ERR_INVALID_ARG, "scale must be finite");
+  if (t == 0) return ok();
+  if (!logits || !topk_ids || !topk_w) return fail(HQ_ERR_INVALID_ARG, "null device pointer");
+  if (!aligned_logits(logits, lt) || !aligned4(bias) || !aligned4(topk_ids) || !aligned4(topk_w))
+    return fail(HQ_ERR_INVALID_ARG, "logits, bias, topk_ids and topk_w must be aligned to their elements");
+  hq::RouteArgs a{};
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.logit_type = lt;
+  a.t = (int)t;
+  a.E = num_experts;
+  a.topk = topk;
+  a.softmax = scoring == HQ_SCORE_SOFTMAX;
+  a.groups = groups;
+  a.group_topk = group_topk;
+  a.group_best = group_best;
+  a.renorm = renormalize;
+  a.scale = scale;
+  hq::arm_timing(ev);
+  const int err = hq::launch_route_experts(a, stream);
   hq::arm_timing({nullptr, nullptr});
   if (err != hipSuccess) return fail(HQ_ERR_HIP, "route launch: %s", hipGetErrorString((hipError_t)err));
   return ok();

@@ -480,6 +480,32 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* plan, int64_t t, int topk, const vo
 hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, int renormalize,
                         int32_t* topk_ids, float* topk_w, void* stream);
 
+/* Routing by scores, with a bias for balance and a choice of groups first.  For each
+ * row of logits [t, num_experts] (fp32, fp16 or bf16):
+ *   s    = sigmoid(logit), or softmax over the row (HQ_SCORE_SOFTMAX), as the
+ *          nearest fp32 number
+ *   key  = s + bias, in fp32 (bias: device fp32 [num_experts], or NULL)
+ *   the experts lie in `groups` groups of num_experts / groups neighbours; a group's
+ *   score is its largest key (group_best = 1), or the fp32 sum of its two largest
+ *   (group_best = 2; of one, where the group has only one), and the group_topk
+ *   groups of largest score stay (groups = 1: no such choice)
+ *   of their experts the topk of largest key are chosen, in falling order
+ *   weight = s (without the bias), with renormalize = 1 over the chosen ones' sum
+ *          (where that is not zero), times scale
+ * Ties go to the lowest index, of groups and of experts.  Experts of logit -inf or
+ * NaN, or of key -inf or NaN, are shut off: never chosen, nothing to a group's score
+ * (a row with fewer than topk others ends in ids of -1 with weight 0), and logits of
+ * -inf and NaN add nothing to the softmax.  A logit of +inf gives unspecified ids and
+ * weights under the softmax, an infinite bias is allowed.  topk_ids int32 and topk_w
+ * fp32 [t, topk], fully overwritten, as hq_moe_align / hq_moe_gemm take them.
+ * num_experts <= 1024, groups <= 64, topk <= 64 and at most the experts of
+ * group_topk groups, t <= 2^24; t = 0 is a no-op.  The tensors are aligned to their
+ * elements.  Honours hq_time_next_launch (one kernel). */
+typedef enum hq_score { HQ_SCORE_SIGMOID = 0, HQ_SCORE_SOFTMAX = 1 } hq_score;
+hq_status hq_route_experts(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, hq_score scoring,
+                           const float* bias, int groups, int group_topk, int group_best, int renormalize, float scale,
+                           int32_t* topk_ids, float* topk_w, void* stream);
+
 /* A whole experts' layer of fp8 weights with block scales (W8A8-BLOCK plans:
  * gate_up [2 I, H] with SILU_MUL_QFP8, down [H, I] with TOPK_COMBINE, the same
  * experts) for a few tokens, in two kernels: the block quantisation of x,
