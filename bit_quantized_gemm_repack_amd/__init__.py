@@ -40,7 +40,7 @@ ASCALE_NONE, ASCALE_PER_TOKEN_F32, ASCALE_MX_E8M0, ASCALE_BLOCK_F32 = range(4)
 GEMM_DENSE, GEMM_GROUPED = range(2)
 SCORE_SIGMOID, SCORE_SOFTMAX = range(2)
 NORM_SAME, NORM_FP8, NORM_INT8, NORM_FP8_BLOCK, NORM_MXFP4 = range(5)
-EPI_NONE, EPI_SILU_MUL, EPI_SILU_MUL_QFP8, EPI_TOPK_COMBINE, EPI_I32_ACC = range(5)
+EPI_NONE, EPI_SILU_MUL, EPI_SILU_MUL_QFP8, EPI_TOPK_COMBINE, EPI_I32_ACC, EPI_SILU_MUL_QMX4 = range(6)
 PEAK_F16, PEAK_BF16, PEAK_FP8, PEAK_FP8_FP4, PEAK_FP4, PEAK_INT8 = range(6)
 MFMA_AUTO, MFMA_F16, MFMA_BF16, MFMA_FP8, MFMA_INT8, MFMA_FP8_FP4, MFMA_FP4 = range(7)
 _MFMA = {None: MFMA_AUTO, "auto": MFMA_AUTO, "f16": MFMA_F16, "bf16": MFMA_BF16, "fp8": MFMA_FP8,
@@ -50,7 +50,7 @@ _DT = {"f16": F16, "bf16": BF16, "fp8": FP8_E4M3, "int8": INT8}
 _SCORE = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
 _NORM = {None: NORM_SAME, "fp8": NORM_FP8, "int8": NORM_INT8, "fp8_block": NORM_FP8_BLOCK, "mxfp4": NORM_MXFP4}
 _EPI = {"none": EPI_NONE, "silu_mul": EPI_SILU_MUL, "silu_mul_qfp8": EPI_SILU_MUL_QFP8,
-        "topk_combine": EPI_TOPK_COMBINE, "i32_acc": EPI_I32_ACC}
+        "silu_mul_qmxfp4": EPI_SILU_MUL_QMX4, "topk_combine": EPI_TOPK_COMBINE, "i32_acc": EPI_I32_ACC}
 
 
 class HQError(RuntimeError):
@@ -448,6 +448,7 @@ class Plan:
                              f"{_DT_NAME[q16.act]} activations")
         self._h = handle
         self._block8 = self.quant.act_scale == ASCALE_BLOCK_F32
+        self._mx4_grouped = kind != "dense" and self.quant.act == FP4_E2M1
         self._ws_need = {}  # rows -> workspace bytes of a block-scaled GEMM
         self._few_need = {}  # (tokens, topk, down's k) -> workspace bytes of a layer of a few tokens
         self._ws = {}
@@ -502,6 +503,15 @@ class Plan:
                 scales.numel() != self.num_experts * blocks[0] * blocks[1]:
             raise ValueError(f"scales must be float32, {self.num_experts} x [{blocks[0]}, {blocks[1]}]")
 
+    def _check_mx4_weight(self, codes, e8m0):
+        if not self._mx4_grouped:
+            return
+        e, n, k = self.num_experts, self.n, self.k
+        if codes.nbytes != e * n * (k // 2) or codes.is_floating_point() or codes.shape[-2] != n:
+            raise ValueError(f"codes must hold {e} x [{n}, {k // 2}] bytes of packed E2M1 codes")
+        if e8m0 is None or e8m0.element_size() != 1 or e8m0.numel() != e * n * (k // 32) or e8m0.shape[-2:] != (n, k // 32):
+            raise ValueError(f"e8m0 must be uint8, {e} x [{n}, {k // 32}]")
+
     def _repack_outputs(self, device):
         wb, mb = self.repacked_bytes()
         w = torch.empty(wb, dtype=torch.uint8, device=device)
@@ -516,6 +526,7 @@ class Plan:
             if t is not None:
                 _dev(t, nm)
         self._check_block_weight(codes, scales)
+        self._check_mx4_weight(codes, e8m0)
         w, meta = self._repack_outputs(codes.device)
         zx = e8m0 if e8m0 is not None else zeros
         _run(codes.device, lib().hq_repack, self._h, _ptr(codes), _ptr(scales), _ptr(zx), _ptr(w), _ptr(meta))
@@ -530,6 +541,7 @@ class Plan:
                 raise ValueError("repack_host takes CPU tensors")
         codes, scales, zeros, e8m0 = ts
         self._check_block_weight(codes, scales)
+        self._check_mx4_weight(codes, e8m0)
         w, meta = self._repack_outputs("cpu")
         zx = e8m0 if e8m0 is not None else zeros
         _check(lib().hq_repack_host(self._h, _ptr(codes), _ptr(scales), _ptr(zx), _ptr(w), _ptr(meta)))
@@ -914,8 +926,7 @@ def quantize_mxfp4(x: torch.Tensor, codes: Optional[torch.Tensor] = None, e8m0: 
     if codes.numel() * codes.element_size() != m * (k // 2) or e8m0.numel() != m * (k // 32) or \
             e8m0.dtype != torch.uint8:
         raise ValueError("codes must hold [m, k/2] bytes and e8m0 be uint8 [k/128, m, 4]")
-    _check(lib().hq_quantize_mxfp4(m, k, BF16 if x.dtype == torch.bfloat16 else F16, _ptr(x), _ptr(codes),
-                                   _ptr(e8m0), _stream_ptr(x.device)))
+    _run(x.device, lib().hq_quantize_mxfp4, m, k, BF16 if x.dtype == torch.bfloat16 else F16, _ptr(x), _ptr(codes), _ptr(e8m0))
     return codes, e8m0
 
 
@@ -945,7 +956,8 @@ def moe_align(topk_ids: torch.Tensor, num_experts: int, block_m: int):
 
 class MoePlan(Plan):
     """A grouped plan: num_experts weights of [n, k]; epi one of 'silu_mul',
-    'silu_mul_qfp8' (gate_up), 'topk_combine' (down) or 'none'."""
+    'silu_mul_qfp8', 'silu_mul_qmxfp4' (gate_up; the last for w4a4_mxfp4),
+    'topk_combine' (down) or 'none'."""
 
     def __init__(self, n: int, k: int, quant: QuantDesc, num_experts: int, max_t: int, epi: str,
                  tuning: Optional[dict] = None, mfma_in: Optional[str] = None, fallback: bool = False):
@@ -986,6 +998,9 @@ class MoePlan(Plan):
             raise ValueError(f"sorted_ids / block_expert are smaller than an alignment with block_m={bm} "
                              f"for t={t}, topk={topk} needs ({need}, {need // bm}); align with block_m(t, topk)")
         mp = sorted_ids.numel()
+        if self._mx4_grouped:
+            return self._moe_gemm_mx4(a, int(t), int(topk), need, sorted_ids, block_expert, num_padded, w, meta, a_scale, topk_w, out,
+                                      out_scale, ws)
         if out is None:
             if self.epi == EPI_TOPK_COMBINE:
                 out = torch.empty((t, self.n), dtype=_TORCH_OUT[self.quant.out], device=dev)
@@ -1031,6 +1046,51 @@ class MoePlan(Plan):
              _ptr(block_expert), _ptr(num_padded), _ptr(topk_w), _ptr(w), _ptr(meta), _ptr(out), _ptr(out_scale),
              _ptr(ws), ws_bytes)
         return (out, out_scale) if self.epi == EPI_SILU_MUL_QFP8 else out
+
+    def _check_mx4_layout(self, w, meta):
+        if w.nbytes < self.num_experts * self.n * (self.k // 2) or meta.nbytes < self.num_experts * self.n * (self.k // 32):
+            raise ValueError("w and meta must be what repack returned for this plan")
+
+    def _moe_gemm_mx4(self, a, t, topk, mp, sorted_ids, block_expert, num_padded, w, meta, a_scale, topk_w, out, out_scale, ws):
+        """moe_gemm of a w4a4_mxfp4 plan; the slot rows live in a workspace of the
+        call's own unless one is given."""
+        dev, down, k, n = a.device, self.epi == EPI_TOPK_COMBINE, self.k, self.n
+        rows = mp if down else t
+        if sorted_ids.numel() != mp:
+            raise ValueError(f"sorted_ids must hold {mp} ids: the block scales are laid out for that many rows")
+        if a.shape != (rows, k // 2) or a.element_size() != 1 or a.is_floating_point() or a_scale is None or a_scale.dtype != torch.uint8 or \
+                a_scale.shape != (k // 128, rows, 4):
+            raise ValueError(f"a must hold [{rows}, {k // 2}] bytes of packed E2M1 codes and a_scale be uint8 [{k // 128}, {rows}, 4]")
+        self._check_mx4_layout(w, meta)
+        _block_ws(ws, dev)
+        if any(v.dtype != torch.int32 for v in (sorted_ids, block_expert, num_padded)):
+            raise ValueError("sorted_ids, block_expert and num_padded must be int32")
+        if down:
+            if topk_w is None or topk_w.dtype != torch.float32 or topk_w.numel() != t * topk:
+                raise ValueError(f"topk_w must be float32 [{t}, {topk}]")
+            if out is None:
+                out = a.new_empty((t, n), dtype=_TORCH_OUT[self.quant.out])
+            elif out.dtype != _TORCH_OUT[self.quant.out] or out.shape != (t, n):
+                raise ValueError(f"out must be {_TORCH_OUT[self.quant.out]} [{t}, {n}]")
+            if ws is None:
+                b = ctypes.c_size_t()
+                _check(lib().hq_moe_workspace_bytes(self._h, t, topk, ctypes.byref(b)))
+                ws = a.new_empty(b.value, dtype=torch.uint8)
+        else:
+            if out is None:
+                out = a.new_empty((mp, n // 4), dtype=torch.uint8)
+            elif out.dtype != torch.uint8 or out.shape != (mp, n // 4):
+                raise ValueError(f"out must be uint8 [{mp}, {n // 4}]")
+            if out_scale is None:
+                out_scale = a.new_empty((n // 256, mp, 4), dtype=torch.uint8)
+            elif out_scale.dtype != torch.uint8 or out_scale.shape != (n // 256, mp, 4):
+                raise ValueError(f"out_scale must be uint8 [{n // 256}, {mp}, 4]")
+        if not _same_device(dev, a, a_scale, sorted_ids, block_expert, num_padded, w, meta, out, topk_w if down else out_scale):
+            raise ValueError("the tensors of a w4a4_mxfp4 GEMM must be contiguous and on a's device")
+        _run(dev, lib().hq_moe_gemm, self._h, t, topk, a.data_ptr(), a_scale.data_ptr(), sorted_ids.data_ptr(), block_expert.data_ptr(),
+             num_padded.data_ptr(), _ptr(topk_w) if down else None, w.data_ptr(), meta.data_ptr(), out.data_ptr(),
+             None if down else out_scale.data_ptr(), _ptr(ws), 0 if ws is None else ws.nbytes)
+        return out if down else (out, out_scale)
 
     def moe_gemm_by_slot(self, a: torch.Tensor, t: int, topk: int, topk_ids: torch.Tensor, w: torch.Tensor,
                          meta: torch.Tensor, a_scale=None, topk_w=None, out=None, out_scale=None, ws=None):
@@ -1141,11 +1201,11 @@ def _uses_few(gate_up: "MoePlan", down: "MoePlan", t: int, topk: int) -> bool:
 def _check_layer_plans(gate_up: "MoePlan", down: "MoePlan"):
     """Both plans of a layer index one set of experts, and down takes gate_up's
     rows: a plan of another shape would read past its weights."""
-    if down.epi != EPI_TOPK_COMBINE or gate_up.epi not in (EPI_SILU_MUL, EPI_SILU_MUL_QFP8):
-        raise ValueError("moe_layer takes a gate_up plan (silu_mul / silu_mul_qfp8) and a topk_combine plan")
-    if gate_up._block8 != down._block8:
-        raise ValueError("gate_up and down must both be w8a8_block plans, or neither")
-    if down.num_experts < gate_up.num_experts or (gate_up._block8 and down.num_experts != gate_up.num_experts):
+    if down.epi != EPI_TOPK_COMBINE or gate_up.epi not in (EPI_SILU_MUL, EPI_SILU_MUL_QFP8, EPI_SILU_MUL_QMX4):
+        raise ValueError("moe_layer takes a gate_up plan (silu_mul / silu_mul_qfp8 / silu_mul_qmxfp4) and a topk_combine plan")
+    if gate_up._block8 != down._block8 or gate_up._mx4_grouped != down._mx4_grouped:
+        raise ValueError("gate_up and down must both be w8a8_block plans, or both w4a4_mxfp4 plans, or neither")
+    if down.num_experts < gate_up.num_experts or ((gate_up._block8 or gate_up._mx4_grouped) and down.num_experts != gate_up.num_experts):
         raise ValueError(f"gate_up has {gate_up.num_experts} experts, down {down.num_experts}")
     if gate_up.n != 2 * down.k:
         raise ValueError(f"gate_up gives rows of {gate_up.n // 2}, down takes {down.k}")
@@ -1176,6 +1236,24 @@ def _moe_few(gate_up, down, x, topk, ids, w, logits, renormalize, w1, m1, w2, m2
     return out
 
 
+def _moe_mx4(gate_up, down, x, x_scale, ids, w, w1, m1, w2, m2):
+    """moe_layer of w4a4_mxfp4 plans: 16-bit x (quantised here), or the codes and powers
+    of two of quantize_mxfp4 or rms_norm."""
+    t, topk = ids.shape
+    if t == 0:
+        return x.new_empty((0, down.n), dtype=_TORCH_OUT[down.quant.out])
+    if x_scale is None:
+        if x.dtype not in (torch.float16, torch.bfloat16) or x.shape != (t, gate_up.k):
+            raise ValueError(f"x must be fp16 / bf16 [{t}, {gate_up.k}], or MXFP4 codes with x_scale")
+        x, x_scale = quantize_mxfp4(x)
+    bm = gate_up.block_m(t, topk)
+    if down.block_m(t, topk) != bm:
+        raise ValueError("the gate_up and down plans must share one alignment block size (equal tuning)")
+    sid, bex, npad = moe_align(ids, gate_up.num_experts, bm)
+    act, scale = gate_up.moe_gemm(x, t, topk, sid, bex, npad, w1, m1, a_scale=x_scale)
+    return down.moe_gemm(act, t, topk, sid, bex, npad, w2, m2, a_scale=scale, topk_w=w)
+
+
 def moe_layer_routed(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, logits: torch.Tensor, topk: int,
                      w1: torch.Tensor, m1: torch.Tensor, w2: torch.Tensor, m2: torch.Tensor, renormalize: bool = True):
     """An MoE layer from the router's logits [t, experts] on: (y [t, n_down],
@@ -1203,11 +1281,16 @@ def moe_layer(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, topk_ids: to
     decode-sized calls (moe_uses_by_slot) and the aligned path otherwise;
     `by_slot` forces one.  w8a8_block plans take 16-bit x (quantised here, or
     inside the two kernels that few tokens run in) or the codes and scales of
-    quantize_blocks, and always the aligned path beyond.  x: [t, k] activations (fp8 codes with x_scale for
+    quantize_blocks, and always the aligned path beyond; w4a4_mxfp4 plans 16-bit x or
+    the codes and scales of quantize_mxfp4 or rms_norm.  x: [t, k] activations (fp8 codes with x_scale for
     W4A8); topk_ids int32 / topk_w fp32 [t, topk] on the GPU."""
     t, topk = topk_ids.shape
     _check_layer_plans(gate_up, down)
     fp8 = gate_up.epi == EPI_SILU_MUL_QFP8
+    if gate_up._mx4_grouped:
+        if by_slot:
+            raise ValueError("w4a4_mxfp4 layers have no by-slot path")
+        return _moe_mx4(gate_up, down, x, x_scale, topk_ids, topk_w, w1, m1, w2, m2)
     if gate_up._block8:
         if by_slot:
             raise ValueError("w8a8_block layers have no by-slot path")

@@ -20,6 +20,7 @@
 #include "block8.h"
 #include "hq_internal.h"
 #include "jit.h"
+#include "mx4.h"
 #include "norm.h"
 #include "route.h"
 
@@ -589,6 +590,7 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
         break;
       case HQ_EPI_SILU_MUL:
       case HQ_EPI_SILU_MUL_QFP8:
+      case HQ_EPI_SILU_MUL_QMX4:
       case HQ_EPI_TOPK_COMBINE:
         if (compute->kind != HQ_GEMM_GROUPED)
           return fail(HQ_ERR_UNSUPPORTED, "grouped epilogues are not available on dense plans");
@@ -597,16 +599,22 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
         return fail(HQ_ERR_INVALID_ARG, "unknown epilogue");
     }
     if (compute->kind == HQ_GEMM_GROUPED) {
-      if (fmt != hq::FMT_W16F16 && fmt != hq::FMT_W16BF16 && fmt != hq::FMT_Q8 && fmt != hq::FMT_B8)
-        return fail(HQ_ERR_UNSUPPORTED, "grouped GEMM supports INT4 weights with fp16/bf16/fp8 activations, and fp8 "
-                                        "weights with block scales");
-      if (fmt == hq::FMT_B8) {
-        if (compute->epi != HQ_EPI_SILU_MUL_QFP8 && compute->epi != HQ_EPI_TOPK_COMBINE)
-          return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers are gate_up with the fp8 requant, or down with the combine");
-        if (compute->epi == HQ_EPI_SILU_MUL_QFP8 && layer->n % 256)
-          return fail(HQ_ERR_UNSUPPORTED, "fp8 block gate_up needs n (gate + up) a multiple of 256");
+      if (fmt != hq::FMT_W16F16 && fmt != hq::FMT_W16BF16 && fmt != hq::FMT_Q8 && !hq::block_grouped(fmt))
+        return fail(HQ_ERR_UNSUPPORTED, "grouped GEMM supports INT4 weights with fp16/bf16/fp8 activations, fp8 weights "
+                                        "with block scales, and MXFP4 weights with MXFP4 activations");
+      if (compute->epi == HQ_EPI_SILU_MUL_QMX4 && fmt != hq::FMT_F44)
+        return fail(HQ_ERR_UNSUPPORTED, "the MXFP4 requant goes with MXFP4 weights and activations");
+      if (hq::block_grouped(fmt)) {
+        const bool mx = fmt == hq::FMT_F44;
+        const hq_epilogue requant = mx ? HQ_EPI_SILU_MUL_QMX4 : HQ_EPI_SILU_MUL_QFP8;
+        if (compute->epi != requant && compute->epi != HQ_EPI_TOPK_COMBINE)
+          return fail(HQ_ERR_UNSUPPORTED, "grouped %s layers are gate_up with the %s requant, or down with the combine",
+                      mx ? "MXFP4" : "fp8 block", mx ? "MXFP4" : "fp8");
+        if (compute->epi == requant && layer->n % 256)
+          return fail(HQ_ERR_UNSUPPORTED, "%s gate_up needs n (gate + up) a multiple of 256", mx ? "MXFP4" : "fp8 block");
         if (tuning && (tuning->kernel == hq::KER_SKINNY || tuning->tile_m == 32 || (tuning->tile_n && tuning->tile_n != 256)))
-          return fail(HQ_ERR_UNSUPPORTED, "grouped fp8 block layers run 16-, 64- or 128-row blocks of 256 columns");
+          return fail(HQ_ERR_UNSUPPORTED, "grouped %s layers run 16-, 64- or 128-row blocks of 256 columns",
+                      mx ? "MXFP4" : "fp8 block");
       }
       if ((compute->epi == HQ_EPI_SILU_MUL || compute->epi == HQ_EPI_SILU_MUL_QFP8) && layer->n % 32)
         return fail(HQ_ERR_UNSUPPORTED, "SiLU * mul needs n (gate + up) a multiple of 32");
@@ -618,7 +626,7 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
           return fail(HQ_ERR_UNSUPPORTED, "grouped tile_m must be 16 or 32 (skinny), 64 or 128 (tiled)");
         if (tuning->kernel == hq::KER_SKINNY && tm > 32)
           return fail(HQ_ERR_UNSUPPORTED, "the skinny grouped kernel uses 16- or 32-row blocks");
-        if (tuning->kernel == hq::KER_TILED && (tm == 16 || tm == 32) && fmt != hq::FMT_B8)
+        if (tuning->kernel == hq::KER_TILED && (tm == 16 || tm == 32) && !hq::block_grouped(fmt))
           return fail(HQ_ERR_UNSUPPORTED, "the tiled grouped kernel uses 64- or 128-row blocks");
         if (tn != 0 && tn != 16 && tn != 32 && tn != 64 && tn != 128 && tn != 256)
           return fail(HQ_ERR_UNSUPPORTED, "grouped tile_n must be 128 or 256 (tiled), 16, 32 or 64 (by slot)");
@@ -1048,7 +1056,7 @@ static MoeChoice moe_choice(const hq_plan* p, int64_t t, int topk) {
   const hq_tuning& u = p->user;
   const int64_t N = p->layer.n;
   const double per_expert = (double)t * topk / p->layer.num_experts;
-  if (p->fmt == hq::FMT_B8) {
+  if (hq::block_grouped(p->fmt)) {
     c.tiled = true;
     // blocks a little taller than what lands on an expert: a block is run with
     // as many rows as it holds, but one more block reads the weights again
@@ -1185,16 +1193,16 @@ static int64_t moe_down_cols(const hq_plan* p, int64_t t, int topk, int bm) {
   return std::min(c, N);
 }
 
-// Columns of a down launch of fp8 block layers: windows whose slot rows fit the
+// Columns of a down launch of fp8 block and MXFP4 layers: windows whose slot rows fit the
 // last-level cache, so that the sum reads them from there and the workspace
 // stays small (4096 tokens, top 8, H = 7168: windows of 60 / 120 / 160 / 240 MiB
 // 424 / 355 / 328 / 311 us, one of 448 309).
-static constexpr int64_t kB8WindowBytes = int64_t(240) << 20;
+static constexpr int64_t kBlockWindowBytes = int64_t(240) << 20;
 
-static int64_t b8_window(const hq_plan* p, int64_t t, int topk) {
+static int64_t block_window(const hq_plan* p, int64_t t, int topk) {
   const int64_t N = p->layer.n, per = std::max<int64_t>(1, t * topk * 2);
-  if (N * per <= kB8WindowBytes) return N;
-  const int64_t n = cdiv(N, std::max<int64_t>(256, kB8WindowBytes / per / 256 * 256));  // windows
+  if (N * per <= kBlockWindowBytes) return N;
+  const int64_t n = cdiv(N, std::max<int64_t>(256, kBlockWindowBytes / per / 256 * 256));  // windows
   return cdiv(cdiv(N, n), 256) * 256;
 }
 
@@ -1207,8 +1215,8 @@ static MoeWs moe_ws(const hq_plan* p, int64_t t, int topk) {
   const int64_t mp = moe_max_padded(t, topk, p->layer.num_experts, moe_choice(p, t, topk).bm);
   // (the fp8 block gate_up requantises inside its tile: no fp32 rows)
   if (p->compute.epi == HQ_EPI_SILU_MUL_QFP8 && p->fmt != hq::FMT_B8) w.act32 = align256((size_t)mp * (size_t)(p->layer.n / 2) * 4);
-  if (p->compute.epi == HQ_EPI_TOPK_COMBINE && p->fmt == hq::FMT_B8) {
-    const int64_t win = b8_window(p, t, topk);
+  if (p->compute.epi == HQ_EPI_TOPK_COMBINE && hq::block_grouped(p->fmt)) {
+    const int64_t win = block_window(p, t, topk);
     w.rows = align256((size_t)(t * topk * win) * 2) + align256((size_t)(t * topk * (win / 64)) * 4);
   } else if (p->compute.epi == HQ_EPI_TOPK_COMBINE)
     w.rows = align256((size_t)t * topk * (size_t)moe_down_cols(p, t, topk, moe_choice(p, t, topk).bm) * 2);
@@ -1224,9 +1232,9 @@ hq_status hq_moe_workspace_bytes(const hq_plan* p, int64_t t, int topk, size_t* 
   return ok();
 }
 
-hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, const float* a_scale,
+hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, const void* a_scale,
                       const int32_t* sorted_ids, const int32_t* block_expert, const int32_t* num_padded,
-                      const float* topk_w, const void* w, const void* meta, void* out, float* out_scale, void* ws,
+                      const float* topk_w, const void* w, const void* meta, void* out, void* out_scale, void* ws,
                       size_t ws_bytes, void* stream) {
   const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
   try {
@@ -1239,12 +1247,15 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       return fail(HQ_ERR_INVALID_ARG, "null device pointer");
     if (!aligned16(a) || !aligned16(w) || !aligned16(meta) || !aligned16(out))
       return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
-    const bool act8 = p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_B8;
+    const bool act8 = p->fmt == hq::FMT_Q8 || p->fmt == hq::FMT_B8, act4 = p->fmt == hq::FMT_F44;
     if (act8 && !a_scale) return fail(HQ_ERR_INVALID_ARG, "8-bit activations need a_scale");
-    if (!act8 && a_scale) return fail(HQ_ERR_INVALID_ARG, "16-bit activations take no a_scale");
+    if (act4 && !a_scale) return fail(HQ_ERR_INVALID_ARG, "MXFP4 activations need their E8M0 scales in a_scale");
+    if (act4 && !aligned16(a_scale)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+    if (!act8 && !act4 && a_scale) return fail(HQ_ERR_INVALID_ARG, "16-bit activations take no a_scale");
     const int epi = p->compute.epi;
     if (epi == HQ_EPI_TOPK_COMBINE && !topk_w) return fail(HQ_ERR_INVALID_ARG, "the combine needs topk_w");
-    if (epi == HQ_EPI_SILU_MUL_QFP8 && !out_scale) return fail(HQ_ERR_INVALID_ARG, "fp8 requant needs out_scale");
+    if ((epi == HQ_EPI_SILU_MUL_QFP8 || epi == HQ_EPI_SILU_MUL_QMX4) && !out_scale)
+      return fail(HQ_ERR_INVALID_ARG, "the requant needs out_scale");
     const MoeWs mw = moe_ws(p, t, topk);
     if (mw.total > 0) {
       if (!ws) return fail(HQ_ERR_WORKSPACE, "this call needs %zu workspace bytes", mw.total);
@@ -1258,9 +1269,9 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     {
       // the kernels address A (token rows for gate_up, aligned rows for the
       // down GEMM) and one expert's W through 32-bit buffer ranges
-      const int64_t act_bytes = (p->fmt == hq::FMT_W16F16 || p->fmt == hq::FMT_W16BF16) ? 2 : 1;
+      const int64_t act_bytes2 = (p->fmt == hq::FMT_W16F16 || p->fmt == hq::FMT_W16BF16) ? 4 : (act4 ? 1 : 2);
       const int64_t a_rows = epi == HQ_EPI_TOPK_COMBINE ? mp : t;
-      if (a_rows * K * act_bytes >= (int64_t(1) << 31) || (int64_t)p->w_bytes_per_expert >= (int64_t(1) << 31))
+      if (a_rows * K * act_bytes2 / 2 >= (int64_t(1) << 31) || (int64_t)p->w_bytes_per_expert >= (int64_t(1) << 31))
         return fail(HQ_ERR_UNSUPPORTED, "activations and one expert's weights must each stay below 2 GiB");
     }
     const uint32_t* zeros = p->layer.q.zp == HQ_ZP_PER_GROUP_U4
@@ -1275,6 +1286,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     switch (epi) {
       case HQ_EPI_NONE: gepi = hq::GEPI_PLAIN; break;
       case HQ_EPI_SILU_MUL: gepi = hq::GEPI_SILU; break;
+      case HQ_EPI_SILU_MUL_QMX4: break;
       case HQ_EPI_SILU_MUL_QFP8:
         gepi = hq::GEPI_SILU_F32;
         f32_out = reinterpret_cast<float*>(wsb);
@@ -1291,11 +1303,61 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     const int64_t blocks = std::min<int64_t>(mp / bm, t * topk);
     const int n_slots = (int)(t * topk);
     int err;
+    if (p->fmt == hq::FMT_F44) {
+      const bool down = epi == HQ_EPI_TOPK_COMBINE;
+      hq::Mx4Args b{};
+      b.a = static_cast<const uint8_t*>(a);
+      b.a_scale = static_cast<const uint32_t*>(a_scale);
+      b.w = static_cast<const uint8_t*>(w);
+      b.w_scale = static_cast<const uint8_t*>(meta);
+      b.out = out;
+      b.N = (int)N;
+      b.K = (int)K;
+      b.G = (int)G;
+      b.a_rows = (int)(down ? mp : t);
+      b.sorted_ids = sorted_ids;
+      b.block_expert = block_expert;
+      b.num_padded = num_padded;
+      b.topk_w = topk_w;
+      b.topk = topk;
+      b.n_slots = n_slots;
+      b.experts = p->layer.num_experts;
+      b.w_expert = (int64_t)p->w_bytes_per_expert;
+      b.s_expert = (int64_t)p->meta_bytes_per_expert;
+      b.out_scale = static_cast<uint8_t*>(out_scale);
+      b.out_rows = (int)mp;
+      err = hipSuccess;
+      if (!down) {
+        hq::arm_timing(ev);
+        err = hq::launch_mx4_grouped(hq::MX4_GATE_UP, bm, b, blocks, stream);
+      }
+      // down: column windows, each the GEMM and then the sum of its rows
+      const int64_t win = down ? block_window(p, t, topk) : 1;
+      hq::B8Args sum{};
+      sum.rows16 = b.rows16 = rows16;
+      sum.row_scale = b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win) * 2));
+      sum.topk = topk;
+      sum.N = (int)N;
+      sum.out = out;
+      sum.out_bf16 = p->layer.q.out == HQ_BF16;
+      for (int64_t c = 0; down && c < N && err == hipSuccess; c += win) {
+        sum.col0 = b.col0 = (int)c;
+        sum.ncol = b.ncol = (int)std::min(win, N - c);
+        hq::arm_timing({c == 0 ? ev.start : nullptr, nullptr});
+        err = hq::launch_mx4_grouped(hq::MX4_DOWN, bm, b, blocks, stream);
+        if (err != hipSuccess) break;
+        hq::arm_timing({nullptr, c + win >= N ? ev.stop : nullptr});
+        err = hq::launch_b8_combine(sum, t, stream);
+      }
+      hq::arm_timing({nullptr, nullptr});
+      if (err != hipSuccess) return fail(HQ_ERR_HIP, "grouped gemm launch: %s", hipGetErrorString((hipError_t)err));
+      return ok();
+    }
     if (p->fmt == hq::FMT_B8) {
       const bool down = epi == HQ_EPI_TOPK_COMBINE;
       hq::B8Args b{};
       b.a = static_cast<const uint8_t*>(a);
-      b.a_scale = a_scale;
+      b.a_scale = static_cast<const float*>(a_scale);
       b.w = static_cast<const uint8_t*>(w);
       b.w_scale = static_cast<const float*>(meta);
       b.out = out;
@@ -1314,7 +1376,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.experts = p->layer.num_experts;
       b.w_expert = (int64_t)p->w_bytes_per_expert;
       b.s_expert = (int64_t)(p->meta_bytes_per_expert / 4);
-      b.out_scale = out_scale;
+      b.out_scale = static_cast<float*>(out_scale);
       b.out_rows = (int)mp;
       b.out_bf16 = p->layer.q.out == HQ_BF16;
       b.once = 2 * t * topk <= (int64_t)bm * p->layer.num_experts;
@@ -1324,7 +1386,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
         err = hq::launch_b8_grouped(hq::B8_GATE_UP, bm, b, blocks, stream);
       }
       // down: column windows, each the GEMM and then the sum of its rows
-      const int64_t win = down ? b8_window(p, t, topk) : 1;
+      const int64_t win = down ? block_window(p, t, topk) : 1;
       b.rows16 = rows16;
       b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win) * 2));
       for (int64_t c = 0; down && c < N && err == hipSuccess; c += win) {
@@ -1348,7 +1410,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     if (smallk) {
       hq::SkinnyArgs s{};
       s.a = a;
-      s.a_scale = a_scale;
+      s.a_scale = static_cast<const float*>(a_scale);
       s.w = w;
       s.scales = meta;
       s.zeros = zeros;
@@ -1392,7 +1454,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     } else if (mc.tiled) {
       hq::TiledArgs s{};
       s.a = a;
-      s.a_scale = a_scale;
+      s.a_scale = static_cast<const float*>(a_scale);
       s.w = w;
       s.scales = meta;
       s.zeros = zeros;
@@ -1422,7 +1484,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     } else {
       hq::SkinnyArgs s{};
       s.a = a;
-      s.a_scale = a_scale;
+      s.a_scale = static_cast<const float*>(a_scale);
       s.w = w;
       s.scales = meta;
       s.zeros = zeros;
@@ -1455,7 +1517,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     if (err == hipSuccess && epi == HQ_EPI_SILU_MUL_QFP8)
       err = hq::launch_moe_requant(f32_out, sorted_ids, num_padded, n_slots, (int)(N / 2),
                                    std::min<int64_t>(mp, (int64_t)bm * t * topk), static_cast<uint8_t*>(out),
-                                   out_scale, stream);
+                                   static_cast<float*>(out_scale), stream);
     if (err == hipSuccess && epi == HQ_EPI_TOPK_COMBINE)
       err = hq::launch_moe_combine(rows16, topk, t, N, 0, N, out, p->layer.q.out == HQ_BF16, stream);
     hq::arm_timing({nullptr, nullptr});
@@ -1475,6 +1537,7 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* p, int64_t t, int topk, const void*
     if (p->compute.kind != HQ_GEMM_GROUPED) return fail(HQ_ERR_INVALID_ARG, "hq_moe_gemm_by_slot needs a grouped plan");
     if (p->fmt == hq::FMT_B8)
       return fail(HQ_ERR_UNSUPPORTED, "fp8 block layers run few tokens through hq_moe_layer_few");
+    if (p->fmt == hq::FMT_F44) return fail(HQ_ERR_UNSUPPORTED, "MXFP4 layers have no by-slot path");
     if (t < 0 || t > p->max_m) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, max_m]");
     if (topk < 1 || topk > 64) return fail(HQ_ERR_INVALID_ARG, "topk must be 1..64");
     if (t == 0) return ok();

@@ -22,6 +22,7 @@
 
 #include "block8.h"
 #include "block8_device.h"
+#include "grouped_device.h"
 #include "launch.h"
 #include "qgemm_tiled_kernel.h"
 
@@ -122,103 +123,6 @@ __device__ __forceinline__ void b8_step_exact(const uint8_t* at, const float* st
 #endif
 }
 
-// Sixteen rows of 16 NB 16-bit values from the operand layout (lane (c16, kq),
-// fragment j: columns 16 j + 4 kq .. + 3 of row c16) to 16 bytes a lane, so
-// that a store instruction covers whole 64-byte runs of its rows; through the
-// wave's own 16 x (32 NB + 16) bytes of LDS.  Stored 8 bytes a lane straight
-// from the operand layout, the rows of the down GEMM took 129 us of 4096
-// tokens' 340.
-constexpr int b8_rows_lds(int NB) { return 16 * (32 * NB + 16); }
-
-template <int NB, typename V, typename S>
-__device__ __forceinline__ void b8_rows16(uint8_t* buf, int lane, V&& value, S&& store) {
-  const int c16 = lane & 15, kq = lane >> 4;
-  constexpr int PITCH = 32 * NB + 16;
-#pragma unroll
-  for (int j = 0; j < NB; ++j) *reinterpret_cast<uint2*>(buf + c16 * PITCH + 32 * j + 8 * kq) = value(j);
-  __builtin_amdgcn_wave_barrier();
-#pragma unroll
-  for (int h = 0; h < NB / 2; ++h)
-    store(64 * h + 16 * kq, *reinterpret_cast<const uint4*>(buf + c16 * PITCH + 64 * h + 16 * kq));
-  __builtin_amdgcn_wave_barrier();
-}
-
-// A slot's row of the down GEMM, 64 columns a wave, on its way into the sum over
-// the token's experts: fp16 values o / 2^e, with the 2^e that brings the 64 columns'
-// largest finite one to [2^14, 2^15), and topk_w * 2^e as their scale.  Half the
-// bytes of fp32 rows, which are a third of the layer's traffic (4096 tokens with
-// fp16 outputs: 980 us with fp32 rows, 739 with these).  Each value is off by at most
-// 2^-11 of itself down to 2^-29 of the largest, and below that by 2^-39 of the
-// largest: an eighth of bf16's rounding, and as much as fp16's own.  (Integers of
-// one step for the 64 columns were finer beside a large column and lost the others.)
-// What is not finite stays in its column.
-template <int MB>
-__device__ __forceinline__ void b8_store_rows(const B8Args& p, const int32_t* ids, const float* tw, uint8_t* buf, int col,
-                                              int lane, const f4_t (&acc)[MB][4]) {
-  const int c16 = lane & 15;
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    uint32_t top = 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t m = b8_mag(acc[mb][j][q]);
-        top = max(top, m < 0x7F800000u ? m : 0u);
-      }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    const int e = max((int)(top >> 23) - 127 - 14, -126);  // the largest is below 2^(e + 15)
-    const float inv = __builtin_amdgcn_ldexpf(1.f, -e);    // (exact: e is at most 113)
-    const int id = ids[16 * mb + c16];
-    const bool live = id < p.n_slots;
-    char* o = reinterpret_cast<char*>(p.rows16 + (int64_t)(live ? id : 0) * p.ncol + (col - p.col0));
-    b8_rows16<4>(
-        buf, lane,
-        [&](int j) {
-          uint32_t v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = float_to_f16_bits(acc[mb][j][q] * inv);
-          return uint2{v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
-        },
-        [&](int byte, uint4 v) {
-          if (live) *reinterpret_cast<uint4*>(o + byte) = v;
-        });
-    if (live && lane < 16)
-      p.row_scale[(int64_t)id * (p.ncol / 64) + (col - p.col0) / 64] = tw[16 * mb + c16] * __builtin_amdgcn_ldexpf(1.f, e);
-  }
-}
-
-// Slots and top-k weights of a block's rows, into LDS.
-__device__ inline void b8_load_slots(const B8Args& p, int m0, int rows, int32_t* ids, float* tw, int tid, int threads) {
-  for (int i = tid; i < rows; i += threads) {
-    const int id = p.sorted_ids[m0 + i];
-    ids[i] = id;
-    tw[i] = id < p.n_slots ? p.topk_w[id] : 0.f;
-  }
-}
-
-// The rows of slots whose expert id is out of range: zeros, columns [c0, c1).
-__device__ inline void b8_zero_rows(const B8Args& p, int m0, int rows, int c0, int c1, int tid, int threads) {
-  const int n = (c1 - c0) / 64;  // strips
-  for (int i = tid; i < rows * n * 16; i += threads) {
-    const int s = i >> 4, r = s / n, strip = s - r * n;
-    const int id = p.sorted_ids[m0 + r];
-    if (id >= p.n_slots) continue;
-    const int col = c0 + 64 * strip - p.col0;
-    *reinterpret_cast<uint2*>(p.rows16 + (int64_t)id * p.ncol + col + 4 * (i & 15)) = uint2{0u, 0u};
-    if ((i & 15) == 0) p.row_scale[(int64_t)id * (p.ncol / 64) + col / 64] = 0.f;
-  }
-}
-
-// Rows of the aligned block from m0 on that hold a slot: a prefix of it.
-__device__ inline int b8_block_rows(const B8Args& p, int m0, int bm, int lane) {
-  int n = 0;
-  for (int b = 0; b < bm; b += 64)
-    n += __popcll(__ballot(b + lane < bm && p.sorted_ids[m0 + min(b + lane, bm - 1)] < p.n_slots));
-  return n;
-}
-
 // A workgroup of WV waves computes BM = 16 MB rows by BN = 16 NB WV columns,
 // each wave all the rows and 16 NB columns, so that every weight is read once a
 // tile, straight to registers.
@@ -233,31 +137,9 @@ struct B8Cfg {
   static constexpr int SROWS = BM < 64 ? 64 : BM;  // row scales per step (whole 64-lane loads)
   static constexpr int STAGE = BM * 128 + SROWS * 4;
   // the ring, or what the epilogues keep in its place
-  static constexpr int EPI = BM * 16 + WAVES * b8_rows_lds(4);
+  static constexpr int EPI = BM * 16 + WAVES * rows_lds(4);
   static constexpr int LDS = ST * STAGE > EPI ? ST * STAGE : EPI;
 };
-
-// Workgroup ids are dealt round-robin to the 8 XCDs, each with an L2 of its own:
-// the id'th of n workgroups takes this logical tile, so that every XCD runs a
-// consecutive run of them.
-__device__ __forceinline__ int b8_xcd_order(int id, int n) {
-  const int xcd = id & 7, each = n >> 3, over = n & 7;
-  return xcd * each + min(xcd, over) + (id >> 3);
-}
-
-// The tile of a grouped launch (row block tm, column tile tn), or false past the
-// padded rows.  The column tiles of a row block and the row blocks of an expert
-// follow each other on one XCD, so that its L2 fetches the rows and the expert's
-// weights once where they keep pace (4096 tokens, 256 experts, top 8, H = 7168,
-// I = 256: gate_up 303 us against 325 with ids in order).
-__device__ __forceinline__ bool b8_grouped_place(const B8Args& p, int bm, int& tm, int& tn) {
-  const int n = *p.num_padded / bm * p.tiles_n;
-  if ((int)blockIdx.x >= n) return false;
-  const int lid = b8_xcd_order(blockIdx.x, n);
-  tm = lid / p.tiles_n;
-  tn = lid - tm * p.tiles_n;
-  return true;
-}
 
 // One tile: rows m0 .. m0 + C::BM - 1, column tile tn.
 template <int MB, int NB, int ST, int MODE, int WV = 4, bool ONCE = false>
@@ -443,10 +325,10 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     int32_t* lid = reinterpret_cast<int32_t*>(lds);
     float* ltw = reinterpret_cast<float*>(lid + C::BM);
     __syncthreads();  // every wave is done with the stage ring
-    b8_load_slots(p, m0, C::BM, lid, ltw, tid, C::THREADS);
+    load_slots(p, m0, C::BM, lid, ltw, tid, C::THREADS);
     __syncthreads();
-    uint8_t* buf = lds + C::BM * 8 + wave * b8_rows_lds(4);
-    if (col < p.col0 + p.ncol) b8_store_rows<MB>(p, lid, ltw, buf, col, lane, acc);
+    uint8_t* buf = lds + C::BM * 8 + wave * rows_lds(4);
+    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid, ltw, buf, col, lane, acc);
   } else if (p.part) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -459,13 +341,13 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     }
   } else {
     __syncthreads();  // every wave is done with the stage ring
-    uint8_t* buf = lds + wave * b8_rows_lds(NB);
+    uint8_t* buf = lds + wave * rows_lds(NB);
     const int col = nblk(0) * 16, cols = min(16 * NB, N - col);
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       const int m = m0 + 16 * mb + c16;
       char* o = reinterpret_cast<char*>(static_cast<uint16_t*>(p.out) + (int64_t)m * N + col);
-      b8_rows16<NB>(
+      rows16_out<NB>(
           buf, lane,
           [&](int j) {
             auto cv = [&](float x) -> uint32_t { return p.out_bf16 ? float_to_bf16_bits(x) : float_to_f16_bits(x); };
@@ -485,7 +367,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // logical tiles run in groups of group_m row tiles, column by column
-  const int lid = b8_xcd_order(blockIdx.x, gridDim.x);
+  const int lid = xcd_order(blockIdx.x, gridDim.x);
   const int per = p.group_m * p.tiles_n;
   const int grp = lid / per, first = grp * p.group_m;
   const int gsz = min(p.tiles_m - first, p.group_m);
@@ -518,15 +400,15 @@ __global__ void __launch_bounds__(64 * b8_grouped_waves(EXACT)) __attribute__((a
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int tm, tn;
-  if (!b8_grouped_place(p, 16 * MB, tm, tn)) return;
+  if (!grouped_place(p, 16 * MB, tm, tn)) return;
   const int m0 = tm * 16 * MB;
   const int64_t ex = p.block_expert[tm];
   if (ex < 0 || ex >= p.experts) {
     if constexpr (MODE == B8_DOWN)
-      b8_zero_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
+      zero_slot_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
     return;
   }
-  b8_grouped_tile<MB, MODE, EXACT, ONCE>(p, lds, m0, ex, tn, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+  b8_grouped_tile<MB, MODE, EXACT, ONCE>(p, lds, m0, ex, tn, block_rows(p, m0, 16 * MB, threadIdx.x & 63));
 #endif
 }
 
@@ -564,8 +446,8 @@ __device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int
   }
   int32_t* lid = reinterpret_cast<int32_t*>(ls + G * ROWS);
   float* ltw = reinterpret_cast<float*>(lid + ROWS);
-  b8_load_slots(p, m0, ROWS, lid, ltw, tid, 256);
-  uint8_t* buf = reinterpret_cast<uint8_t*>(ltw + ROWS) + wave * b8_rows_lds(4);
+  load_slots(p, m0, ROWS, lid, ltw, tid, 256);
+  uint8_t* buf = reinterpret_cast<uint8_t*>(ltw + ROWS) + wave * rows_lds(4);
 
   u4_t braw[2][4][2];
   float sw[2][1];
@@ -603,7 +485,7 @@ __device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int
     __builtin_amdgcn_sched_barrier(0);
     b8_step<MB, 4, 1>(lds + g * ROWS * 128 + c16 * 128, ls + g * ROWS + c16, c16, kq, braw[slot], sw[slot], acc);
     if (++g == G) {
-      if (col < c1) b8_store_rows<MB>(p, lid, ltw, buf, col, lane, acc);
+      if (col < c1) store_slot_rows<MB>(p, lid, ltw, buf, col, lane, acc);
       zero();
       g = 0;
       col += 256;
@@ -633,20 +515,20 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int tm, tn;
-  if (!b8_grouped_place(p, 16 * MB, tm, tn)) return;
+  if (!grouped_place(p, 16 * MB, tm, tn)) return;
   const int m0 = tm * 16 * MB;
   const int64_t ex = p.block_expert[tm];
   const int c0 = p.col0 + tn * p.cols_wg, c1 = min(c0 + p.cols_wg, p.col0 + p.ncol);
   if (ex < 0 || ex >= p.experts) {
-    b8_zero_rows(p, m0, 16 * MB, c0, c1, threadIdx.x, 256);
+    zero_slot_rows(p, m0, 16 * MB, c0, c1, threadIdx.x, 256);
     return;
   }
-  b8_down_dispatch<MB>(p, lds, m0, ex, c0, c1, b8_block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+  b8_down_dispatch<MB>(p, lds, m0, ex, c0, c1, block_rows(p, m0, 16 * MB, threadIdx.x & 63));
 #endif
 }
 
 // y[t][col0 + c] = RNE(sum over the token's topk slots of row * scale), in slot
-// order; eight columns a thread, the rows as b8_store_rows leaves them.  Bound by
+// order; eight columns a thread, the rows as store_slot_rows leaves them.  Bound by
 // reading the rows: a window of 4096 tokens, 235 MB, 43 us, 6.1 TB/s with its output.
 // The rows are done with once read: loads that do not keep them leave the cache to
 // the next window's (a layer of 4096 tokens 648 us against 661).
@@ -727,7 +609,7 @@ constexpr int kShortLds = 72 * 1024;  // two workgroups a CU
 template <int MB>
 hipError_t launch_short(const B8Args& a, dim3 grid, hipStream_t s) {
   const hipError_t e = allow_lds<b8_down_short<MB>>(kShortLds);
-  return e != hipSuccess ? e : launch_timed(b8_down_short<MB>, grid, dim3(256), (size_t)(16 * MB * (a.G * 132 + 8) + 4 * b8_rows_lds(4)), s, a);
+  return e != hipSuccess ? e : launch_timed(b8_down_short<MB>, grid, dim3(256), (size_t)(16 * MB * (a.G * 132 + 8) + 4 * rows_lds(4)), s, a);
 }
 
 }  // namespace
@@ -750,7 +632,7 @@ int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* s
   if (a.G < 1 || a.gps != a.G || a.N % (mode == B8_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
   if (mode == B8_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
   B8Args b = a;
-  const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) + 4 * b8_rows_lds(4) <= kShortLds;
+  const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) + 4 * rows_lds(4) <= kShortLds;
   if (whole) {
     // column tiles a workgroup walks: two where there are plenty (they share
     // the rows' staging; more leave the last workgroups a long tail).  256

@@ -113,6 +113,9 @@ HQ_HD constexpr inline int frag_bytes(int fmt) {
   return (w8_weights(fmt) || fmt == FMT_B8) ? 2048 : (w2_weights(fmt) ? 512 : (w3_weights(fmt) ? 768 : 1024));
 }
 
+// Grouped layers of aligned 16-, 64- or 128-row blocks whose activations have scales per
+// block of a row (block8_tiled.hip, mx4_tiled.hip).
+HQ_HD constexpr inline bool block_grouped(int fmt) { return fmt == FMT_B8 || fmt == FMT_F44; }
 // MXFP4 weights (E2M1 codes in natural order + E8M0 block scales).
 HQ_HD constexpr inline bool mx_weights(int fmt) { return fmt == FMT_F4 || fmt == FMT_F44; }
 // Metadata is one region of byte scales (E8M0 for MXFP4 / MXINT4, E4M3 for

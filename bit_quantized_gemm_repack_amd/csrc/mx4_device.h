@@ -65,4 +65,13 @@ __device__ inline uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));  // quad_perm 2 3 0 1
 }
 
+// The scale bytes of the four blocks that 16 neighbouring lanes hold (four lanes each), as
+// a word in each of them.
+__device__ inline uint32_t mx4_scale_word(uint32_t s) {
+  uint32_t all = 0u;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) all |= (uint32_t)__shfl((int)s, ((int)threadIdx.x & 48) + 4 * b, 64) << (8 * b);
+  return all;
+}
+
 }  // namespace hq

@@ -189,10 +189,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_kernel(NormArgs p)
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = t[i][j] * f;
       const uint32_t word = mx4_word(y, s);
-      // the four blocks' bytes of 128 columns, in their first lane
-      uint32_t all = s;
-#pragma unroll
-      for (int b = 1; b < 4; ++b) all |= (uint32_t)__shfl((int)s, (tid & 48) + 4 * b, 64) << (8 * b);
+      const uint32_t all = mx4_scale_word(s);
       if (c < k8) {
         static_cast<uint32_t*>(p.out)[row * k8 + c] = word;
         if ((lane & 15) == 0) static_cast<uint32_t*>(p.scale)[(int64_t)(c >> 4) * p.m + row] = all;

@@ -129,51 +129,45 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const u4_t* __restr
 // conversion of a 32-element block: shared exponent X = floor(log2 max|v|) - 2
 // (2 = the largest E2M1 exponent), clamped to [-127, 127], X = 0 for an
 // all-zero block; elements RNE_E2M1(v / 2^X) saturated to +-6.  The scaling by
-// 2^-X is exact (ldexp), so every decision is an exact comparison.
-
-// One thread per 32-element block: 64 input bytes in, 16 code bytes and one
-// E8M0 byte out (consecutive threads, consecutive blocks of a row).  The
-// scales are stored group-major: byte j of word (g, row) is block 4 g + j of
-// the row, so that the GEMM's 16 rows of one operand read 64 contiguous bytes.
+// 2^-X is exact, so every decision is an exact comparison.  A block with an
+// infinity or a NaN gets E8M0's NaN.
+//
+// Eight values a lane, so four lanes a block and sixteen a word of four blocks'
+// scales; a workgroup takes 4 rows by 4 words.  The scales are stored group-major:
+// byte j of word (g, row) is block 4 g + j of the row, so that the GEMM's 16 rows of
+// one operand read 64 contiguous bytes.
 template <bool BF16>
-__global__ void __launch_bounds__(256) quantize_mx_kernel(const u4_t* __restrict__ x, int64_t nblk, int64_t m,
-                                                          int64_t kb, u4_t* __restrict__ codes,
-                                                          uint8_t* __restrict__ e8m0) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= nblk) return;
-  const int64_t row = i / kb, b = i - row * kb;
-  u4_t v[4];
+__global__ void __launch_bounds__(256) quantize_mx_kernel(const u4_t* __restrict__ x, uint32_t m, uint32_t k8,
+                                                          uint32_t* __restrict__ codes, uint32_t* __restrict__ e8m0) {
+  const uint32_t G = k8 / 16, quads = (G + 3) / 4, rq = blockIdx.x / quads;
+  const uint32_t g = (blockIdx.x - rq * quads) * 4 + (threadIdx.x >> 6), row = rq * 4 + ((threadIdx.x >> 4) & 3);
+  if (g >= G || row >= m) return;
+  const int64_t at = (int64_t)row * k8 + g * 16 + (threadIdx.x & 15);
+  const u4_t raw = x[at];
+  float v[8];
+  uint32_t top = 0u;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) v[c] = __builtin_nontemporal_load(x + 4 * i + c);
-  float amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) amax = fmaxf(amax, chunk_absmax<BF16>(v[c]));
-  // floor(log2 amax) from the exponent field (a subnormal amax clamps to -127)
-  const int X = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23) - 127 - 2, -127) : 0;
-  uint32_t w[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {  // chunk c: elements 8c .. 8c + 7 -> word c, low nibble first
-    uint32_t word = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      word |= e2m1_code_rne(__builtin_amdgcn_ldexpf(elem<BF16>(v[c][j >> 1], j & 1), -X)) << (4 * j);
-    w[c] = word;
+  for (int j = 0; j < 8; ++j) {
+    v[j] = elem<BF16>(raw[j >> 1], j & 1);
+    top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
   }
-  codes[i] = u4_t{w[0], w[1], w[2], w[3]};
-  e8m0[((b >> 2) * m + row) * 4 + (b & 3)] = (uint8_t)(X + 127);
+  const uint32_t s = mx4_scale(quad_max(top));
+  codes[at] = mx4_word(v, s);
+  const uint32_t all = mx4_scale_word(s);
+  if ((threadIdx.x & 15) == 0) e8m0[(int64_t)g * m + row] = all;
 }
 
 }  // namespace
 
 int launch_quantize_mx(int64_t m, int64_t k, int in_bf16, const void* x, void* codes, uint8_t* e8m0, void* stream) {
-  const int64_t nblk = m * (k / 32);
-  const dim3 grid((unsigned)((nblk + 255) / 256)), block(256);
+  const dim3 grid((unsigned)((k / 128 + 3) / 4 * ((m + 3) / 4))), block(256);
   const auto xs = static_cast<const u4_t*>(x);
-  const auto cs = static_cast<u4_t*>(codes);
+  const auto cs = static_cast<uint32_t*>(codes);
+  const auto es = reinterpret_cast<uint32_t*>(e8m0);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t kb = k / 32;
-  return in_bf16 ? (int)launch_timed(quantize_mx_kernel<true>, grid, block, 0, s, xs, nblk, m, kb, cs, e8m0)
-                 : (int)launch_timed(quantize_mx_kernel<false>, grid, block, 0, s, xs, nblk, m, kb, cs, e8m0);
+  const uint32_t mu = (uint32_t)m, k8 = (uint32_t)(k / 8);
+  return in_bf16 ? (int)launch_timed(quantize_mx_kernel<true>, grid, block, 0, s, xs, mu, k8, cs, es)
+                 : (int)launch_timed(quantize_mx_kernel<false>, grid, block, 0, s, xs, mu, k8, cs, es);
 }
 
 int launch_quantize_rows(int64_t m, int64_t k, int in_bf16, int out_fp8, const void* x, void* codes, float* scales,

@@ -150,9 +150,10 @@ typedef enum hq_ascale_mode {
  *   W4A8-MXFP4 w_elem FP4_E2M1, group 32, scale E8M0, zp NONE,
  *              act FP8_E4M3, act_scale PER_TOKEN_F32, out F16|BF16
  *   W4A4-MXFP4 w_elem FP4_E2M1, group 32, scale E8M0, zp NONE,
- *              act FP4_E2M1, act_scale MX_E8M0, out F16|BF16 (dense only;
- *              W4A4 and MXFP4 are among the supported combinations and
- *              formats of cocoloop.cn, format section)
+ *              act FP4_E2M1, act_scale MX_E8M0, out F16|BF16 (W4A4 and
+ *              MXFP4 are among the supported combinations and formats of
+ *              cocoloop.cn, format section); dense, and grouped as
+ *              SILU_MUL_QMX4 / TOPK_COMBINE
  *   W8A8-BLOCK w_elem FP8_E4M3 (w_bits 8), group 128, scale F32 (one per
  *              128 n x 128 k), zp NONE, act FP8_E4M3, act_scale BLOCK_F32
  *              (one per row and 128 k), out F16|BF16; dense, and grouped as
@@ -184,7 +185,8 @@ typedef enum hq_epilogue {
   HQ_EPI_SILU_MUL = 1,      /* grouped gate_up: SiLU(h[:, :N/2]) * h[:, N/2:] */
   HQ_EPI_SILU_MUL_QFP8 = 2, /* as above, then per-row fp8 e4m3 requant    */
   HQ_EPI_TOPK_COMBINE = 3,  /* grouped down: * topk weight, sum per token  */
-  HQ_EPI_I32_ACC = 4        /* W4A8-INT debug: per-group int32 accumulators */
+  HQ_EPI_I32_ACC = 4,       /* W4A8-INT debug: per-group int32 accumulators */
+  HQ_EPI_SILU_MUL_QMX4 = 5  /* W4A4-MXFP4 grouped gate_up: as SILU_MUL, then MXFP4 requant */
 } hq_epilogue;
 
 /* Operand type of the matrix instruction a plan runs on.  The quantisation
@@ -401,12 +403,21 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  *                             of the codes (exact) and summed in fp32, but for
  *                             128-row blocks of plans with outputs of bf16,
  *                             which take the fp8 instruction (see hq_gemm).
+ *   epi HQ_EPI_SILU_MUL_QMX4  W4A4-MXFP4 plans: SiLU * mul in fp32, requantised
+ *                             inside the GEMM's tile by the rule of
+ *                             hq_quantize_mxfp4 (a block of 32 outputs that holds an
+ *                             infinity or a NaN gets E8M0's NaN, so that its
+ *                             products are NaN): out = uint8 codes [max_padded,
+ *                             n/4], out_scale = E8M0 words uint8 [n/256]
+ *                             [max_padded][4], no workspace; a_scale is uint8
+ *                             [k/128][t][4] for gate_up, [k/128][max_padded][4]
+ *                             for down.
  *   epi HQ_EPI_TOPK_COMBINE   down: row r of `a` [max_padded, k] is the
  *                             intermediate of slot sorted_ids[r];
  *                             out = y [t, n] (plan out dtype),
  *                             y[tok] = sum_j topk_w[tok, j] * (a_row . W_e^T):
  *                             each slot's weighted row, rounded to bf16
- *                             (W8A8-BLOCK: to fp16 with a power of two per 64
+ *                             (W8A8-BLOCK, W4A4: to fp16 with a power of two per 64
  *                             columns, each value off by at most 2^-11 of itself
  *                             down to 2^-29 of the 64 columns' largest, and below
  *                             by 2^-39 of that one), goes
@@ -420,7 +431,7 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  *   epi HQ_EPI_NONE           gate_up rows without the activation: out
  *                             [max_padded, n] (plan out dtype).
  * a_scale: per-row fp32 scales of 8-bit activations (per token for gate_up,
- * per aligned row for down), else NULL.  topk_w: device fp32 [t, topk]
+ * per aligned row for down) or E8M0 words (W4A4), else NULL.  topk_w: device fp32 [t, topk]
  * (TOPK_COMBINE only).  Rows of padding slots (and, for gate_up, of slots
  * with an out-of-range expert id) are left unwritten.  ws: the workspace of
  * hq_moe_workspace_bytes (the fp8 requant's fp32 rows, or the combine's
@@ -430,9 +441,9 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  * hq_gemm, activations or one expert's weights of 2 GiB or more are
  * HQ_ERR_UNSUPPORTED. */
 hq_status hq_moe_workspace_bytes(const hq_plan* plan, int64_t t, int topk, size_t* bytes);
-hq_status hq_moe_gemm(const hq_plan* plan, int64_t t, int topk, const void* a, const float* a_scale,
+hq_status hq_moe_gemm(const hq_plan* plan, int64_t t, int topk, const void* a, const void* a_scale,
                       const int32_t* sorted_ids, const int32_t* block_expert, const int32_t* num_padded,
-                      const float* topk_w, const void* w, const void* meta, void* out, float* out_scale,
+                      const float* topk_w, const void* w, const void* meta, void* out, void* out_scale,
                       void* ws, size_t ws_bytes, void* stream);
 
 /* The same grouped GEMMs without the alignment, for decode-sized t: the rows
@@ -584,7 +595,9 @@ hq_status hq_quantize_blocks(int64_t m, int64_t k, hq_dtype in, int silu_mul, co
  * clamped to [-127, 127], with X = 0 for an all-zero block; each element is
  * v / 2^X (exact) rounded to E2M1, nearest with ties to even, saturated to
  * +-6; a value that rounds to zero gives code 0.
- *   x      device [m, k] fp16 / bf16 (in = HQ_F16 / HQ_BF16), finite values
+ * A block that holds an infinity or a NaN gets E8M0's NaN (255) and unspecified
+ * codes, so that the GEMM's row is NaN.
+ *   x      device [m, k] fp16 / bf16 (in = HQ_F16 / HQ_BF16)
  *   codes  device [m, k/2] bytes: E2M1 codes two per byte along k, low
  *          nibble first (the `a` of a W4A4 hq_gemm), fully overwritten
  *   e8m0   device bytes, X + 127 per block, in the group-major word layout
