@@ -1048,7 +1048,7 @@ class MoePlan(Plan):
         return (out, out_scale) if self.epi == EPI_SILU_MUL_QFP8 else out
 
     def _check_mx4_layout(self, w, meta):
-        if w.nbytes < self.num_experts * self.n * (self.k // 2) or meta.nbytes < self.num_experts * self.n * (self.k // 32):
+        if w.nbytes < self.num_experts * self.n * self.k * 17 // 32:
             raise ValueError("w and meta must be what repack returned for this plan")
 
     def _moe_gemm_mx4(self, a, t, topk, mp, sorted_ids, block_expert, num_padded, w, meta, a_scale, topk_w, out, out_scale, ws):

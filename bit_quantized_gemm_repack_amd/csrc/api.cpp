@@ -622,7 +622,7 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
         return fail(HQ_ERR_UNSUPPORTED, "the combining down GEMM needs n a multiple of 64");
       if (tuning) {
         const int tm = tuning->tile_m, tn = tuning->tile_n;
-        if (tm != 0 && tm != 16 && tm != 32 && tm != 64 && tm != 128)
+        if (tm != 0 && tm != 16 && tm != 32 && tm != 64 && tm != 128 && !(tm == 256 && fmt == hq::FMT_F44))
           return fail(HQ_ERR_UNSUPPORTED, "grouped tile_m must be 16 or 32 (skinny), 64 or 128 (tiled)");
         if (tuning->kernel == hq::KER_SKINNY && tm > 32)
           return fail(HQ_ERR_UNSUPPORTED, "the skinny grouped kernel uses 16- or 32-row blocks");
@@ -656,6 +656,10 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
       p->scale_region_bytes = (size_t)(N * G * 2);
       p->meta_bytes_per_expert = p->scale_region_bytes;
       if (layer->q.zp == HQ_ZP_PER_GROUP_U4) p->meta_bytes_per_expert += (size_t)((N / 16) * G * 8);
+    }
+    if (hq::mx4_layout(p)) {
+      p->w_bytes_per_expert = (size_t)hq::mx4_weight_bytes(N, K);
+      p->meta_bytes_per_expert = 0;
     }
     hq::Exec e = hq::choose_exec(p, max_m > 0 ? max_m : 1);
     s = compute->kind == HQ_GEMM_GROUPED ? HQ_OK : check_exec(p, e);
@@ -738,8 +742,9 @@ hq_status hq_repack(const hq_plan* p, const void* codes, const void* scales, con
     if (s != HQ_OK) return s;
     if (!aligned16(codes) || !aligned16(w_out) || !aligned16(meta_out))
       return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
-    int err = p->fmt == hq::FMT_B8 ? hq::launch_b8_repack(p->layer.n, p->layer.k, p->layer.num_experts, codes, scales,
-                                                          w_out, meta_out, stream)
+    const int64_t N = p->layer.n, K = p->layer.k, E = p->layer.num_experts;
+    int err = p->fmt == hq::FMT_B8 ? hq::launch_b8_repack(N, K, E, codes, scales, w_out, meta_out, stream)
+              : hq::mx4_layout(p)  ? hq::launch_mx4_repack(N, K, E, p->compute.epi != HQ_EPI_TOPK_COMBINE, codes, zx, w_out, stream)
                                    : hq::launch_repack(p, codes, scales, zx, w_out, meta_out, stream);
     if (err != hipSuccess) return fail(HQ_ERR_HIP, "repack launch: %s", hipGetErrorString((hipError_t)err));
     return ok();
@@ -761,6 +766,15 @@ hq_status hq_repack_host(const hq_plan* p, const void* codes, const void* scales
       for (int64_t e = 0; e < E; ++e)
         for (int64_t i = 0; i < wpe; ++i) wo[e * wpe + i] = hq::repack_word_b8(cb + e * N * K, K, i);
       std::memcpy(meta_out, scales, p->meta_bytes_per_expert * (size_t)E);
+      return ok();
+    }
+    if (hq::mx4_layout(p)) {
+      const bool paired = p->compute.epi != HQ_EPI_TOPK_COMBINE;
+      const int64_t per = hq::mx4_weight_bytes(N, K) / 16;  // chunks of 16 bytes
+      const uint8_t *cb = static_cast<const uint8_t*>(codes), *sb = static_cast<const uint8_t*>(zx);
+      for (int64_t e = 0; e < E; ++e)
+        for (int64_t i = 0; i < per; ++i)
+          hq::mx4_repack_chunk(cb + e * N * (K / 2), sb + e * N * (K / 32), N, K, paired, i, static_cast<uint8_t*>(w_out) + (e * per + i) * 16);
       return ok();
     }
     if (hq::w3_weights(p->fmt)) {
@@ -1273,6 +1287,8 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       const int64_t a_rows = epi == HQ_EPI_TOPK_COMBINE ? mp : t;
       if (a_rows * K * act_bytes2 / 2 >= (int64_t(1) << 31) || (int64_t)p->w_bytes_per_expert >= (int64_t(1) << 31))
         return fail(HQ_ERR_UNSUPPORTED, "activations and one expert's weights must each stay below 2 GiB");
+      if (epi == HQ_EPI_TOPK_COMBINE && hq::block_grouped(p->fmt) && t * topk * block_window(p, t, topk) * 2 >= (int64_t)hq::kSlotRowsMost)
+        return fail(HQ_ERR_UNSUPPORTED, "the slots' rows must stay below 4 GiB");
     }
     const uint32_t* zeros = p->layer.q.zp == HQ_ZP_PER_GROUP_U4
                                 ? reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(meta) +
@@ -1309,7 +1325,6 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.a = static_cast<const uint8_t*>(a);
       b.a_scale = static_cast<const uint32_t*>(a_scale);
       b.w = static_cast<const uint8_t*>(w);
-      b.w_scale = static_cast<const uint8_t*>(meta);
       b.out = out;
       b.N = (int)N;
       b.K = (int)K;
@@ -1323,7 +1338,6 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       b.n_slots = n_slots;
       b.experts = p->layer.num_experts;
       b.w_expert = (int64_t)p->w_bytes_per_expert;
-      b.s_expert = (int64_t)p->meta_bytes_per_expert;
       b.out_scale = static_cast<uint8_t*>(out_scale);
       b.out_rows = (int)mp;
       err = hipSuccess;

@@ -17,6 +17,7 @@
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -137,7 +138,7 @@ struct B8Cfg {
   static constexpr int SROWS = BM < 64 ? 64 : BM;  // row scales per step (whole 64-lane loads)
   static constexpr int STAGE = BM * 128 + SROWS * 4;
   // the ring, or what the epilogues keep in its place
-  static constexpr int EPI = BM * 16 + WAVES * rows_lds(4);
+  static constexpr int EPI = std::max(BM * 16, WAVES * rows_lds(NB));
   static constexpr int LDS = ST * STAGE > EPI ? ST * STAGE : EPI;
 };
 
@@ -327,8 +328,7 @@ __device__ __forceinline__ void b8_tile(const B8Args& p, uint8_t* lds, int m0, i
     __syncthreads();  // every wave is done with the stage ring
     load_slots(p, m0, C::BM, lid, ltw, tid, C::THREADS);
     __syncthreads();
-    uint8_t* buf = lds + C::BM * 8 + wave * rows_lds(4);
-    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid, ltw, buf, col, lane, acc);
+    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid, ltw, col, lane, acc);
   } else if (p.part) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -447,7 +447,6 @@ __device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int
   int32_t* lid = reinterpret_cast<int32_t*>(ls + G * ROWS);
   float* ltw = reinterpret_cast<float*>(lid + ROWS);
   load_slots(p, m0, ROWS, lid, ltw, tid, 256);
-  uint8_t* buf = reinterpret_cast<uint8_t*>(ltw + ROWS) + wave * rows_lds(4);
 
   u4_t braw[2][4][2];
   float sw[2][1];
@@ -485,7 +484,7 @@ __device__ __forceinline__ void b8_down_tiles(const B8Args& p, uint8_t* lds, int
     __builtin_amdgcn_sched_barrier(0);
     b8_step<MB, 4, 1>(lds + g * ROWS * 128 + c16 * 128, ls + g * ROWS + c16, c16, kq, braw[slot], sw[slot], acc);
     if (++g == G) {
-      if (col < c1) store_slot_rows<MB>(p, lid, ltw, buf, col, lane, acc);
+      if (col < c1) store_slot_rows<MB>(p, lid, ltw, col, lane, acc);
       zero();
       g = 0;
       col += 256;
@@ -604,12 +603,12 @@ hipError_t launch_grouped(int mode, const B8Args& a, dim3 grid, hipStream_t s) {
   return launch_grouped_k<MB, B8_GATE_UP, true>(a, grid, s);
 }
 
-constexpr int kShortLds = 72 * 1024;  // two workgroups a CU
+constexpr int kShortLds = 63 * 1024;  // two workgroups a CU
 
 template <int MB>
 hipError_t launch_short(const B8Args& a, dim3 grid, hipStream_t s) {
   const hipError_t e = allow_lds<b8_down_short<MB>>(kShortLds);
-  return e != hipSuccess ? e : launch_timed(b8_down_short<MB>, grid, dim3(256), (size_t)(16 * MB * (a.G * 132 + 8) + 4 * rows_lds(4)), s, a);
+  return e != hipSuccess ? e : launch_timed(b8_down_short<MB>, grid, dim3(256), (size_t)(16 * MB * (a.G * 132 + 8)), s, a);
 }
 
 }  // namespace
@@ -632,7 +631,7 @@ int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* s
   if (a.G < 1 || a.gps != a.G || a.N % (mode == B8_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
   if (mode == B8_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
   B8Args b = a;
-  const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) + 4 * rows_lds(4) <= kShortLds;
+  const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) <= kShortLds;
   if (whole) {
     // column tiles a workgroup walks: two where there are plenty (they share
     // the rows' staging; more leave the last workgroups a long tail).  256

@@ -5,6 +5,7 @@
 #pragma once
 
 #include "block8_device.h"
+#include "hq_internal.h"
 
 namespace hq {
 
@@ -29,6 +30,23 @@ __device__ __forceinline__ void rows16_out(uint8_t* buf, int lane, V&& value, S&
   __builtin_amdgcn_wave_barrier();
 }
 
+// Maximum over the lanes that differ in bit D (16, 32) of their number, in each of them.
+template <int D>
+__device__ __forceinline__ float lanes_max(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t b = __float_as_uint(v);
+  if constexpr (D == 16) {
+    const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  } else {
+    const auto x = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  }
+#else
+  return v;
+#endif
+}
+
 // A slot's row of the down GEMM, 64 columns a wave, on its way into the sum over
 // the token's experts: fp16 values o / 2^e, with the 2^e that brings the 64 columns'
 // largest finite one to [2^14, 2^15), and topk_w * 2^e as their scale.  Half the
@@ -39,40 +57,62 @@ __device__ __forceinline__ void rows16_out(uint8_t* buf, int lane, V&& value, S&
 // one step for the 64 columns were finer beside a large column and lost the others.)
 // What is not finite stays in its column.
 template <int MB, typename Args>
-__device__ __forceinline__ void store_slot_rows(const Args& p, const int32_t* ids, const float* tw, uint8_t* buf, int col,
-                                              int lane, const f4_t (&acc)[MB][4]) {
-  const int c16 = lane & 15;
+__device__ __forceinline__ void store_slot_rows(const Args& p, const int32_t* ids, const float* tw, int col, int lane, const f4_t (&acc)[MB][4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int c16 = lane & 15, kq = lane >> 4;
+  // Rows without a slot are stored past the end, which writes nothing: with a branch
+  // around them the next loads' wait would cover these stores, each block's in turn.
+  const auto rows = __builtin_amdgcn_make_buffer_rsrc(p.rows16, (short)0, (int)((uint32_t)p.n_slots * (uint32_t)(2 * p.ncol)), 0x00020000);
+  const auto scales = __builtin_amdgcn_make_buffer_rsrc(p.row_scale, (short)0, (int)((uint32_t)p.n_slots * (uint32_t)(p.ncol / 16)), 0x00020000);
+  const uint32_t at = 2 * (col - p.col0) + (kq & 1) * 32 + (kq >> 1) * 16;
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) {
-    uint32_t top = 0u;
+    float top = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t m = b8_mag(acc[mb][j][q]);
-        top = max(top, m < 0x7F800000u ? m : 0u);
-      }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    const int e = max((int)(top >> 23) - 127 - 14, -126);  // the largest is below 2^(e + 15)
-    const float inv = __builtin_amdgcn_ldexpf(1.f, -e);    // (exact: e is at most 113)
+      for (int q = 0; q < 4; q += 2) top = fmaxf(fmaxf(fabsf(acc[mb][j][q]), fabsf(acc[mb][j][q + 1])), top);
+    if (__ballot(top == __builtin_inff())) {  // the largest finite one
+      top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float m = fabsf(acc[mb][j][q]);
+          top = m < __builtin_inff() ? fmaxf(top, m) : top;
+        }
+    }
+    top = lanes_max<16>(top);
+    top = lanes_max<32>(top);
+    const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 14, -126);  // the largest is below 2^(e + 15)
+    const float inv = __builtin_amdgcn_ldexpf(1.f, -e);                     // (exact: e is at most 113)
     const int id = ids[16 * mb + c16];
     const bool live = id < p.n_slots;
-    char* o = reinterpret_cast<char*>(p.rows16 + (int64_t)(live ? id : 0) * p.ncol + (col - p.col0));
-    rows16_out<4>(
-        buf, lane,
-        [&](int j) {
-          uint32_t v[4];
+    const uint32_t row = live ? (uint32_t)id * (uint32_t)(2 * p.ncol) + at : kSlotRowsMost;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = float_to_f16_bits(acc[mb][j][q] * inv);
-          return uint2{v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
-        },
-        [&](int byte, uint4 v) {
-          if (live) *reinterpret_cast<uint4*>(o + byte) = v;
-        });
-    if (live && lane < 16)
-      p.row_scale[(int64_t)id * (p.ncol / 64) + (col - p.col0) / 64] = tw[16 * mb + c16] * __builtin_amdgcn_ldexpf(1.f, e);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const f4_t& a = acc[mb][2 * h + j];
+          v[j][q] = (uint32_t)float_to_f16_bits(a[2 * q] * inv) | ((uint32_t)float_to_f16_bits(a[2 * q + 1] * inv) << 16);
+        }
+      // lanes of odd kq give their first four columns for their neighbour's second four
+      u4_t o;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const auto x = __builtin_amdgcn_permlane16_swap(v[0][q], v[1][q], false, false);
+        o[q] = x[0];
+        o[2 + q] = x[1];
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(o, rows, row, 64 * h, 0);
+    }
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tw[16 * mb + c16] * __builtin_amdgcn_ldexpf(1.f, e)), scales,
+                                          live && kq == 0 ? (uint32_t)id * (uint32_t)(p.ncol / 16) + (col - p.col0) / 16 : kSlotRowsMost, 0, 0);
   }
+#endif
 }
 
 // Slots and top-k weights of a block's rows, into LDS.

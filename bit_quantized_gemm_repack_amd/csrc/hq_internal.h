@@ -116,6 +116,8 @@ HQ_HD constexpr inline int frag_bytes(int fmt) {
 // Grouped layers of aligned 16-, 64- or 128-row blocks whose activations have scales per
 // block of a row (block8_tiled.hip, mx4_tiled.hip).
 HQ_HD constexpr inline bool block_grouped(int fmt) { return fmt == FMT_B8 || fmt == FMT_F44; }
+// Most bytes of a launch's slot rows, which the kernels address with 32 bits.
+constexpr uint32_t kSlotRowsMost = 0xFFFFF000u;
 // MXFP4 weights (E2M1 codes in natural order + E8M0 block scales).
 HQ_HD constexpr inline bool mx_weights(int fmt) { return fmt == FMT_F4 || fmt == FMT_F44; }
 // Metadata is one region of byte scales (E8M0 for MXFP4 / MXINT4, E4M3 for

@@ -4,10 +4,18 @@
 // Activations and weights are E2M1 codes with one power of two per 32 k, which the
 // scaled matrix instruction takes as they are: a product needs no promotion.
 //
-// Device weight layout: codes as the dense plans have them (hq_internal.h: fragments of
-// 16 columns x 128 k, 1 KiB, lane l the 32 codes of column l % 16 and block l / 16),
-// powers of two [N/16][K/128][64 lanes] bytes.  Activation codes are row-major, their
-// powers of two words [K/128][rows] of four blocks.
+// Device weight layout, a private one of the grouped plans: strips of 64 columns, what one
+// wave multiplies, each along K without a gap, so that a wave reads one stream (in the dense
+// plans' order, 16 columns a stream and the powers of two apart, gate_up of 256 experts by
+// 16 rows ran at 4.5 TB/s for 5.6).  A strip is four fragments of 16 columns; gate_up's
+// holds 32 columns of gate and the 32 of up that belong to the same outputs.  It goes in
+// steps of q groups of 128 k, q = 2 where K/128 is even, else 1, each
+//   codes           [q][fragment 4][lane 64][16 bytes]: lane l has the 32 codes of column l %
+//                   16 and block l / 16
+//   powers of two   [lane 64][q][fragment 4] bytes, a fragment's by the matrix instruction's
+//                   selector
+// and all of it lies in the codes' buffer; the metadata is empty.
+// Activation codes are row-major, their powers of two words [K/128][rows] of four blocks.
 #pragma once
 
 #include "hq_internal.h"
@@ -18,7 +26,6 @@ struct Mx4Args {
   const uint8_t* a;          // codes, K / 2 bytes a row
   const uint32_t* a_scale;   // [G][a_rows]
   const uint8_t* w;
-  const uint8_t* w_scale;
   void* out;                 // gate_up: codes [rows][N / 4]
   int N, K, G;
   int a_rows;                // rows of a and of each scale group
@@ -29,8 +36,7 @@ struct Mx4Args {
   const float* topk_w;
   int topk, n_slots;
   int experts;               // a block_expert outside [0, experts) is no expert
-  int64_t w_expert;          // code bytes per expert
-  int64_t s_expert;          // powers of two per expert
+  int64_t w_expert;          // bytes per expert
   uint8_t* out_scale;        // gate_up: [N / 256][out_rows][4]
   int out_rows;
   // down: this launch's columns [col0, col0 + ncol) of N, col0 a multiple of
@@ -38,10 +44,40 @@ struct Mx4Args {
   int col0, ncol;
   uint16_t* rows16;          // [n_slots][ncol] fp16
   float* row_scale;          // [n_slots][ncol / 64]
-  int cols_wg;               // short K: columns a workgroup walks
 };
 
 enum Mx4Mode : int { MX4_GATE_UP = 0, MX4_DOWN = 1 };
+
+// Groups of 128 k a step, and a step's bytes.
+HQ_HD constexpr inline int mx4_groups(int64_t G) { return G % 2 ? 1 : 2; }
+constexpr int kMx4GroupBytes = 4 * kFragBytes + 256;
+HQ_HD constexpr inline int64_t mx4_weight_bytes(int64_t N, int64_t K) { return N / 64 * (K / kFragK) * kMx4GroupBytes; }
+// Column of fragment j, lane column c of a strip.
+HQ_HD inline int64_t mx4_column(int64_t N, bool paired, int64_t strip, int j, int c) {
+  return paired ? (j < 2 ? 0 : N / 2) + strip * 32 + (j & 1) * 16 + c : strip * 64 + j * 16 + c;
+}
+// The 16 bytes that are chunk `at` of an expert's device weight <- canonical codes [N][K/2]
+// and E8M0 [N][K/32].
+HQ_HD inline void mx4_repack_chunk(const uint8_t* codes, const uint8_t* e8m0, int64_t N, int64_t K, bool paired, int64_t at, uint8_t* out) {
+  const int64_t G = K / kFragK;
+  const int q = mx4_groups(G), per = q * (kMx4GroupBytes / 16), c = (int)(at % per);
+  const int64_t step = at / per, g0 = step % (G / q) * q, strip = step / (G / q);
+  if (c < q * 256) {
+    const int lane = c & 63, j = (c >> 6) & 3, u = c >> 8;
+    const uint8_t* from = codes + mx4_column(N, paired, strip, j, lane & 15) * (K / 2) + (g0 + u) * 64 + (lane >> 4) * 16;
+    for (int i = 0; i < 16; ++i) out[i] = from[i];
+    return;
+  }
+  for (int i = 0; i < 16; ++i) {
+    const int b = (c - q * 256) * 16 + i, j = b & 3, u = (b >> 2) % q, lane = (b >> 2) / q;
+    out[i] = e8m0[mx4_column(N, paired, strip, j, lane & 15) * (K / 32) + 4 * (g0 + u) + (lane >> 4)];
+  }
+}
+#ifndef __HIPCC_RTC__
+// Whether a plan's weights have this layout.
+inline bool mx4_layout(const hq_plan* p) { return p->fmt == FMT_F44 && p->compute.kind == HQ_GEMM_GROUPED; }
+#endif
+int launch_mx4_repack(int64_t N, int64_t K, int64_t E, bool paired, const void* codes, const void* e8m0, void* w_out, void* stream);
 
 // Aligned blocks of bm rows (16, 64, 128) by 256 columns.
 int launch_mx4_grouped(int mode, int bm, const Mx4Args& a, int64_t blocks, void* stream);

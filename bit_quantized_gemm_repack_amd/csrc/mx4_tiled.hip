@@ -24,58 +24,83 @@ namespace hq {
 namespace {
 
 // acc += W . A^T over 128 k: the weight is the first operand, so a lane (token l % 16)
-// holds four consecutive columns.  sw, sa: the power of two of this lane's 32 k of its
-// weight column and of its activation row, in the lowest byte.
+// holds four consecutive columns.  Byte J of sw and byte 0 of sa: the powers of two of this
+// lane's 32 k of its weight column and of its activation row.
+template <int J>
 __device__ __forceinline__ f4_t mx4_mfma(u4_t w, u4_t a, f4_t acc, uint32_t sw, uint32_t sa) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const i8_t wv = i8_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
   const i8_t av = i8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 4, 0, (int)sw, 0, (int)sa);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, acc, 4, 4, J, (int)sw, 0, (int)sa);
 #else
   return acc;
 #endif
 }
+// The four fragments of a strip.
+__device__ __forceinline__ void mx4_strip(const u4_t (&w)[4], u4_t a, f4_t (&acc)[4], uint32_t sw, uint32_t sa) {
+  acc[0] = mx4_mfma<0>(w[0], a, acc[0], sw, sa);
+  acc[1] = mx4_mfma<1>(w[1], a, acc[1], sw, sa);
+  acc[2] = mx4_mfma<2>(w[2], a, acc[2], sw, sa);
+  acc[3] = mx4_mfma<3>(w[3], a, acc[3], sw, sa);
+}
 
-// A workgroup of 4 waves computes BM = 16 MB rows by 256 columns, each wave all the rows
-// and 64 columns, so that every weight is read once a tile, straight to registers.
+// A workgroup of 4 H waves computes BM = 16 MB H rows by 256 columns: each wave MB row
+// blocks and a strip of 64 columns, whose weights go straight to registers; with H = 2 two
+// waves share a strip, and the second finds it in the first-level cache.  A step covers Q
+// groups of 128 k: with two, an activation row is a whole 128-byte line.
 constexpr int kWaves = 4;
-template <int MB, int ST>
+template <int MB, int H, int ST, int Q>
 struct Mx4Cfg {
-  static constexpr int BM = 16 * MB;
-  static constexpr int SEGW = MB > kWaves ? MB / kWaves : 1;  // 1 KiB loads of 16 rows a wave and step
-  static constexpr int SROWS = BM < 64 ? 64 : BM;             // row scales per step (whole 64-lane loads)
-  static constexpr int STAGE = BM * 64 + SROWS * 4;
-  static constexpr int EPI = BM * 8 + kWaves * rows_lds(4);   // what down's epilogue keeps in the ring's place
-  static constexpr int LDS = ST * STAGE > EPI ? ST * STAGE : EPI;
+  static constexpr int WAVES = kWaves * H;
+  static constexpr int BM = 16 * MB * H;
+  static constexpr int CHUNKS = 4 * Q;                                    // 16-byte chunks of a row
+  static constexpr int SEG_ROWS = 64 / CHUNKS;                            // rows of a 1 KiB load
+  static constexpr int SEGS = BM / SEG_ROWS;
+  static constexpr int SEGW = SEGS > WAVES ? SEGS / WAVES : 1;            // such loads a wave
+  static constexpr int SROWS = BM < 64 ? 64 : BM;                         // row scales a group (whole 64-lane loads)
+  static constexpr int SCALES = BM * 64 * Q;                              // where they lie in a stage
+  static constexpr int STAGE = SCALES + Q * SROWS * 4;
+  static constexpr int LDS = ST * STAGE;                                  // (more than the slots of down's epilogue)
 };
 
 __device__ inline __amdgpu_buffer_rsrc_t mx4_rsrc(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
+// The powers of two of the step at byte `at`: a word a group.
+template <int Q>
+struct Mx4Scales {
+  uint32_t v[Q];
+  template <int AUX>
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int lane, int at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (Q == 2) {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, at + 8192, AUX);
+      v[0] = x[0];
+      v[1] = x[1];
+    } else {
+      v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, lane * 4, at + 4096, AUX);
+    }
+#endif
+  }
+};
+
 // One tile: rows m0 .. m0 + 16 MB - 1, column tile tn.
-template <int MB, int ST, int MODE>
+template <int MB, int H, int ST, int Q, int MODE, int AUX>
 __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using C = Mx4Cfg<MB, ST>;
-  constexpr int NB = 4;
+  using C = Mx4Cfg<MB, H, ST, Q>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kq = lane >> 4;
-  const int N = p.N, G = p.G, kb = p.K / 2;
-
-  // 16-column block of this wave's fragment j: gate_up takes two of gate and the two of up
-  // that belong to the same 32 outputs, one block of the intermediate
-  const int nblocks = N / 16;
-  auto nblk = [&](int j) -> int {
-    if constexpr (MODE == MX4_GATE_UP) return (j < 2 ? 0 : nblocks / 2) + tn * 8 + wave * 2 + (j & 1);
-    return p.col0 / 16 + tn * 16 + wave * 4 + j;
-  };
+  const int N = p.N, G = p.G, kb = p.K / 2, steps = G / Q;
+  const int sw = wave % kWaves, r0 = H > 1 ? wave / kWaves * 16 * MB : 0;  // strip of the tile, first row of this wave's
+  const int strip = (MODE == MX4_DOWN ? p.col0 / 64 : 0) + tn * 4 + sw;
+  const int first = __builtin_amdgcn_readfirstlane(min(strip, N / 64 - 1) * steps * Q * kMx4GroupBytes);  // past N: loaded again, not stored
 
   const auto ra = mx4_rsrc(p.a, (int64_t)p.a_rows * kb);
   const auto rs = mx4_rsrc(p.a_scale, (int64_t)G * p.a_rows * 4);
   const auto rw = mx4_rsrc(p.w + ex * p.w_expert, p.w_expert);
-  const auto rws = mx4_rsrc(p.w_scale + ex * p.s_expert, p.s_expert);
 
   auto row_of = [&](int r) -> int {
     if constexpr (MODE == MX4_GATE_UP) {
@@ -84,86 +109,82 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
     }
     return m0 + r;
   };
-  // activation rows: segment seg holds rows 16 seg .. 16 seg + 15, lane l writes physical
-  // chunk l % 4 of row 16 seg + l / 4 (waves beyond the segments repeat one, so that every
-  // wave has the same loads in flight)
+  // activation rows: lane l of segment seg writes physical chunk l % CHUNKS of row
+  // SEG_ROWS seg + l / CHUNKS (waves beyond the segments repeat one, so that every wave has
+  // the same loads in flight)
   int aoff[C::SEGW], alds[C::SEGW];
 #pragma unroll
   for (int s = 0; s < C::SEGW; ++s) {
-    const int seg = (wave + kWaves * s) % MB;
-    const int r = seg * 16 + (lane >> 2);
-    aoff[s] = row_of(r) * kb + swz<4>(r, lane & 3) * 16;
+    const int seg = (wave + C::WAVES * s) % C::SEGS;
+    const int r = seg * C::SEG_ROWS + lane / C::CHUNKS;
+    aoff[s] = row_of(r) * kb + swz<C::CHUNKS>(r, lane % C::CHUNKS) * 16;
     alds[s] = seg * 1024;
   }
-  const int sseg = wave % (C::SROWS / 64);
-  const int soff = row_of(min(sseg * 64 + lane, C::BM - 1)) * 4;
-  int wfrag[NB];  // columns past N read the last block (their results are not stored)
-#pragma unroll
-  for (int j = 0; j < NB; ++j) wfrag[j] = __builtin_amdgcn_readfirstlane(min(nblk(j), nblocks - 1) * G);
+  constexpr int HALVES = C::SROWS / 64;
+  const int sgroup = wave / HALVES % Q, shalf = wave % HALVES;
+  const int soff = row_of(min(shalf * 64 + lane, C::BM - 1)) * 4;
+  const int slds = C::SCALES + sgroup * C::SROWS * 4 + shalf * 256;
 
-  u4_t braw[ST][NB];
-  uint32_t sraw[ST][NB];
-  constexpr int LPS = C::SEGW + 1 + 2 * NB;
+  u4_t braw[ST][Q][4];
+  Mx4Scales<Q> sraw[ST];
+  constexpr int LPS = C::SEGW + 1 + 4 * Q + 1;
   static_assert(LPS * (ST - 2) < 64, "loads in flight exceed the wait counter");
 
-  auto issue = [&](auto slot_c, int g) {
+  auto issue = [&](auto slot_c, int s) {
     constexpr int slot = decltype(slot_c)::value;
 #pragma unroll
-    for (int s = 0; s < C::SEGW; ++s)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(lds + slot * C::STAGE + alds[s]), 16, aoff[s], g * 64, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(lds + slot * C::STAGE + C::BM * 64 + sseg * 256), 4, soff,
-                                             g * p.a_rows * 4, 0, 0);
+    for (int i = 0; i < C::SEGW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(lds + slot * C::STAGE + alds[i]), 16, aoff[i], s * 64 * Q, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(lds + slot * C::STAGE + slds), 4, soff, (s * Q + sgroup) * p.a_rows * 4, 0, 0);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      braw[slot][j] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16, (wfrag[j] + g) * 1024, 0));
-      sraw[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(rws, lane & ~3, (wfrag[j] + g) * 64, 0);
-    }
+    for (int u = 0; u < Q; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        braw[slot][u][j] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + j * 1024, first + s * Q * kMx4GroupBytes + u * 4096, AUX));
+    sraw[slot].template load<AUX>(rw, lane, first + s * Q * kMx4GroupBytes);
   };
 
-  f4_t acc[MB][NB];
+  f4_t acc[MB][4];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) acc[mb][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 4; ++j) acc[mb][j] = f4_t{0.f, 0.f, 0.f, 0.f};
 
   auto compute = [&](auto slot_c) {
     constexpr int slot = decltype(slot_c)::value;
-    const uint8_t* at = lds + slot * C::STAGE + c16 * 64 + swz<4>(c16, kq) * 16;
-    const uint8_t* st = lds + slot * C::STAGE + C::BM * 64 + c16 * 4 + kq;
-    uint32_t sw[NB];
+    const uint8_t* at = lds + slot * C::STAGE + (r0 + c16) * 64 * Q;
+    const uint8_t* st = lds + slot * C::STAGE + C::SCALES + (r0 + c16) * 4 + kq;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) sw[j] = sraw[slot][j] >> (8 * (lane & 3));
+    for (int u = 0; u < Q; ++u)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const u4_t av = *reinterpret_cast<const u4_t*>(at + mb * 1024);
-      const uint32_t sa = st[mb * 64];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[mb][j] = mx4_mfma(braw[slot][j], av, acc[mb][j], sw[j], sa);
-    }
+      for (int mb = 0; mb < MB; ++mb)
+        mx4_strip(braw[slot][u], *reinterpret_cast<const u4_t*>(at + mb * 1024 * Q + swz<C::CHUNKS>(c16, 4 * u + kq) * 16), acc[mb],
+                  sraw[slot].v[u], st[u * C::SROWS * 4 + mb * 64]);
   };
 
-  auto gclamp = [&](int g) { return g < G ? g : G - 1; };
-  auto step = [&](auto slot_c, int g) {
+  auto sclamp = [&](int s) { return s < steps ? s : steps - 1; };
+  auto step = [&](auto slot_c, int s) {
     constexpr int cur = decltype(slot_c)::value;
     using Ahead = std::integral_constant<int, (cur + ST - 1) % ST>;
     __builtin_amdgcn_sched_barrier(0);
-    wait_vm_lds<LPS*(ST - 2)>();  // this wave's loads of step g have landed
+    wait_vm_lds<LPS*(ST - 2)>();  // this wave's loads of step s have landed
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      pin(braw[cur][j]);
-      pin(sraw[cur][j]);
+    for (int u = 0; u < Q; ++u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pin(braw[cur][u][j]);
+      pin(sraw[cur].v[u]);
     }
-    issue(Ahead{}, gclamp(g + ST - 1));  // into the slot every wave finished with at step g - 1
-    if (g < G) compute(slot_c);
+    issue(Ahead{}, sclamp(s + ST - 1));  // into the slot every wave finished with at step s - 1
+    if (s < steps) compute(slot_c);
   };
   [&]<int... I>(std::integer_sequence<int, I...>) {
-    ((issue(std::integral_constant<int, I>{}, gclamp(I)), __builtin_amdgcn_sched_barrier(0)), ...);
+    ((issue(std::integral_constant<int, I>{}, sclamp(I)), __builtin_amdgcn_sched_barrier(0)), ...);
   }(std::make_integer_sequence<int, ST - 1>{});
-  for (int g = 0; g < G; g += ST) {
+  for (int s = 0; s < steps; s += ST) {
     [&]<int... I>(std::integer_sequence<int, I...>) {
-      (step(std::integral_constant<int, I>{}, g + I), ...);
+      (step(std::integral_constant<int, I>{}, s + I), ...);
     }(std::make_integer_sequence<int, ST>{});
   }
   __builtin_amdgcn_s_waitcnt(0);  // no load into LDS may outlive its use here
@@ -190,227 +211,194 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
       const uint32_t give = kq & 1 ? word & 0xFFFFu : word >> 16;
       const uint32_t got = (uint32_t)__shfl_xor((int)give, 16, 64);
       const uint32_t codes = kq & 1 ? got | (word & 0xFFFF0000u) : (word & 0xFFFFu) | (got << 16);
-      const int row = m0 + 16 * mb + c16;
+      const int row = m0 + r0 + 16 * mb + c16;
       if (p.sorted_ids[row] >= p.n_slots) continue;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (int64_t)row * (N / 4) + tn * 64 + wave * 16 + (kq & 1) * 8 + (kq >> 1) * 4) = codes;
-      if (kq == 0) p.out_scale[((int64_t)tn * p.out_rows + row) * 4 + wave] = (uint8_t)s;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (int64_t)row * (N / 4) + tn * 64 + sw * 16 + (kq & 1) * 8 + (kq >> 1) * 4) = codes;
+      if (kq == 0) p.out_scale[((int64_t)tn * p.out_rows + row) * 4 + sw] = (uint8_t)s;
     }
   } else {
-    const int col = nblk(0) * 16;
+    const int col = strip * 64;
     // the rows' slots and weights, into LDS first: a load per row block between
     // the stores would wait for each in turn
     int32_t* lid = reinterpret_cast<int32_t*>(lds);
     float* ltw = reinterpret_cast<float*>(lid + C::BM);
     __syncthreads();  // every wave is done with the stage ring
-    load_slots(p, m0, C::BM, lid, ltw, tid, 64 * kWaves);
+    load_slots(p, m0, C::BM, lid, ltw, tid, 64 * C::WAVES);
     __syncthreads();
-    uint8_t* buf = lds + C::BM * 8 + wave * rows_lds(4);
-    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid, ltw, buf, col, lane, acc);
+    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid + r0, ltw + r0, col, lane, acc);
   }
 #endif
 }
 
-constexpr int mx4_stages(int MB) { return MB <= 4 ? 4 : 3; }
+constexpr int mx4_stages(int MB, int H) { return MB <= 4 || H > 1 ? 3 : 2; }
 
 // An aligned block is run with as many row blocks (a power of two) as hold slots, so that
 // the half-empty blocks that end each expert's segment cost what they hold.
-template <int MB, int MODE>
+template <int MB, int H, int Q, int MODE, int AUX>
 __device__ __forceinline__ void mx4_tile_rows(const Mx4Args& p, uint8_t* lds, int m0, int64_t ex, int tn, int rows) {
   if constexpr (MB > 1) {
-    if (rows <= 8 * MB) {
-      mx4_tile_rows<MB / 2, MODE>(p, lds, m0, ex, tn, rows);
+    if (rows <= 8 * MB * H) {
+      mx4_tile_rows<MB / 2, H, Q, MODE, AUX>(p, lds, m0, ex, tn, rows);
       return;
     }
   }
-  mx4_tile<MB, mx4_stages(MB), MODE>(p, lds, m0, ex, tn);
+  mx4_tile<MB, H, mx4_stages(MB, H), Q, MODE, AUX>(p, lds, m0, ex, tn);
 }
 
-template <int MB, int MODE>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) mx4_grouped(Mx4Args p) {
+template <int MB, int H, int Q, int MODE>
+__global__ void __launch_bounds__(64 * kWaves * H) __attribute__((amdgpu_waves_per_eu(2))) mx4_grouped(Mx4Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int tm, tn;
-  if (!grouped_place(p, 16 * MB, tm, tn)) return;
-  const int m0 = tm * 16 * MB;
+  if (!grouped_place(p, 16 * MB * H, tm, tn)) return;
+  const int m0 = tm * 16 * MB * H;
   const int64_t ex = p.block_expert[tm];
   if (ex < 0 || ex >= p.experts) {
     if constexpr (MODE == MX4_DOWN)
-      zero_slot_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 256);
+      zero_slot_rows(p, m0, 16 * MB * H, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 64 * kWaves * H);
     return;
   }
-  mx4_tile_rows<MB, MODE>(p, lds, m0, ex, tn, block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+  const int rows = block_rows(p, m0, 16 * MB * H, threadIdx.x & 63);
+  // weights that no other block reads go past the caches
+  const bool alone = (tm == 0 || p.block_expert[tm - 1] != ex) && ((tm + 1) * 16 * MB * H >= *p.num_padded || p.block_expert[tm + 1] != ex);
+  if (alone)
+    mx4_tile_rows<MB, H, Q, MODE, kReadOnce>(p, lds, m0, ex, tn, rows);
+  else
+    mx4_tile_rows<MB, H, Q, MODE, 0>(p, lds, m0, ex, tn, rows);
 #endif
 }
 
-// The down product with short K: the block's activation rows lie in LDS whole, and the
-// workgroup walks its column tiles in one stream of weight loads, with no barrier and no
-// refill between tiles.
-constexpr int short_lds(int rows, int G) { return rows * (G * 68 + 8) + kWaves * rows_lds(4); }
-constexpr int kShortLds = 72 * 1024;  // two workgroups a CU
+// The down product with short K (G groups, up to kShortGroups): each wave keeps its strip's
+// weights in registers whole, the block's activation rows lie in LDS, and sixteen of them
+// at a time are multiplied and stored.  Past its start a wave loads nothing more: loads and
+// stores return in one order, so that a load's wait would cover the stores before it (rows
+// straight from memory, a ring of three: 105 us a window of 4096 tokens).
+constexpr int kShortGroups = 8;
+constexpr int short_lds(int bm, int G) { return bm * (G * 68 + 8); }
 
-template <int MB>
-__device__ __forceinline__ void mx4_down_tiles(const Mx4Args& p, uint8_t* lds, int m0, int64_t ex, int c0, int c1) {
+template <int G>
+__global__ void __launch_bounds__(64 * kWaves) mx4_down_short(Mx4Args p, int bm) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int ROWS = 16 * MB, ST = 3;
+  constexpr int Q = mx4_groups(G), CHUNKS = 4 * Q, SEG_ROWS = 64 / CHUNKS;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // rows [G / Q][bm][64 Q], chunks swizzled
+  int tm, tn;
+  if (!grouped_place(p, bm, tm, tn)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kq = lane >> 4;
-  const int G = p.G, kb = p.K / 2;
-  const auto ra = mx4_rsrc(p.a, (int64_t)p.a_rows * kb);
-  const auto rw = mx4_rsrc(p.w + ex * p.w_expert, p.w_expert);
-  const auto rws = mx4_rsrc(p.w_scale + ex * p.s_expert, p.s_expert);
-  // rows: group g at g * ROWS * 64, chunks swizzled; their powers of two [G][ROWS] behind
-  uint32_t* ls = reinterpret_cast<uint32_t*>(lds + G * ROWS * 64);
-  for (int s = wave; s < G * MB; s += kWaves) {
-    const int g = s / MB, seg = s - g * MB;
-    const int r = seg * 16 + (lane >> 2);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(lds + s * 1024), 16, (m0 + r) * kb + swz<4>(r, lane & 3) * 16, g * 64, 0, 0);
-  }
-  for (int i = tid; i < G * ROWS; i += 64 * kWaves) {
-    const int g = i / ROWS;
-    ls[i] = p.a_scale[(int64_t)g * p.a_rows + m0 + i - g * ROWS];
-  }
-  int32_t* lid = reinterpret_cast<int32_t*>(ls + G * ROWS);
-  float* ltw = reinterpret_cast<float*>(lid + ROWS);
-  load_slots(p, m0, ROWS, lid, ltw, tid, 64 * kWaves);
-  uint8_t* buf = reinterpret_cast<uint8_t*>(ltw + ROWS) + wave * rows_lds(4);
-
-  u4_t braw[ST][4];
-  uint32_t sraw[ST][4];
-  int col = c0 + 64 * wave, g = 0;  // of the step being multiplied
-  int acol = col, ag = 0;           // of the step being loaded
-  auto issue = [&](auto slot_c) {
-    constexpr int slot = decltype(slot_c)::value;
-    const int nb = min(acol, c1 - 64) / 16;  // past the end: loaded again, not stored
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int f = (nb + j) * G + ag;
-      braw[slot][j] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16, f * 1024, 0));
-      sraw[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(rws, lane & ~3, f * 64, 0);
-    }
-    if (++ag == G) {
-      ag = 0;
-      acol += 256;
-    }
-  };
-  f4_t acc[MB][4];
-  auto zero = [&] {
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[mb][j] = f4_t{0.f, 0.f, 0.f, 0.f};
-  };
-  zero();
-  [&]<int... I>(std::integer_sequence<int, I...>) {
-    (issue(std::integral_constant<int, I>{}), ...);
-  }(std::make_integer_sequence<int, ST - 1>{});
-  __builtin_amdgcn_s_waitcnt(0);  // this wave's loads into LDS have landed
-  __syncthreads();
-  auto step = [&](auto slot_c) {
-    constexpr int slot = decltype(slot_c)::value;
-    issue(std::integral_constant<int, (slot + ST - 1) % ST>{});
-    __builtin_amdgcn_sched_barrier(0);
-    uint32_t sw[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sw[j] = sraw[slot][j] >> (8 * (lane & 3));
-    const uint8_t* at = lds + g * ROWS * 64 + c16 * 64 + swz<4>(c16, kq) * 16;
-    const uint8_t* st = reinterpret_cast<const uint8_t*>(ls + g * ROWS + c16) + kq;
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      const u4_t av = *reinterpret_cast<const u4_t*>(at + mb * 1024);
-      const uint32_t sa = st[mb * 64];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[mb][j] = mx4_mfma(braw[slot][j], av, acc[mb][j], sw[j], sa);
-    }
-    if (++g == G) {
-      if (col < c1) store_slot_rows<MB>(p, lid, ltw, buf, col, lane, acc);
-      zero();
-      g = 0;
-      col += 256;
-    }
-  };
-  const int steps = (c1 - c0 + 255) / 256 * G;
-  for (int s = 0; s < steps; s += ST) {
-    [&]<int... I>(std::integer_sequence<int, I...>) {
-      ((s + I < steps ? step(std::integral_constant<int, I>{}) : void()), ...);
-    }(std::make_integer_sequence<int, ST>{});
-  }
-#endif
-}
-
-template <int MB>
-__device__ __forceinline__ void mx4_down_rows(const Mx4Args& p, uint8_t* lds, int m0, int64_t ex, int c0, int c1, int rows) {
-  if constexpr (MB > 1) {
-    if (rows <= 8 * MB) {
-      mx4_down_rows<MB / 2>(p, lds, m0, ex, c0, c1, rows);
-      return;
-    }
-  }
-  mx4_down_tiles<MB>(p, lds, m0, ex, c0, c1);
-}
-
-template <int MB>
-__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) mx4_down_short(Mx4Args p) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  int tm, tn;
-  if (!grouped_place(p, 16 * MB, tm, tn)) return;
-  const int m0 = tm * 16 * MB;
+  const int m0 = tm * bm, kb = p.K / 2;
   const int64_t ex = p.block_expert[tm];
-  const int c0 = p.col0 + tn * p.cols_wg, c1 = min(c0 + p.cols_wg, p.col0 + p.ncol);
+  const int c0 = p.col0 + tn * 256, c1 = min(c0 + 256, p.col0 + p.ncol);
   if (ex < 0 || ex >= p.experts) {
-    zero_slot_rows(p, m0, 16 * MB, c0, c1, threadIdx.x, 256);
+    zero_slot_rows(p, m0, bm, c0, c1, tid, 64 * kWaves);
     return;
   }
-  mx4_down_rows<MB>(p, lds, m0, ex, c0, c1, block_rows(p, m0, 16 * MB, threadIdx.x & 63));
+  uint32_t* ls = reinterpret_cast<uint32_t*>(lds + G * bm * 64);  // powers of two [G][bm]
+  int32_t* lid = reinterpret_cast<int32_t*>(ls + G * bm);
+  float* ltw = reinterpret_cast<float*>(lid + bm);
+  const int id = tid < bm ? p.sorted_ids[m0 + tid] : p.n_slots;
+  const auto ra = mx4_rsrc(p.a, (int64_t)p.a_rows * kb);
+  for (int i = wave; i < G * bm / 16; i += kWaves) {
+    const int s = i / (bm / SEG_ROWS), r = (i - s * (bm / SEG_ROWS)) * SEG_ROWS + lane / CHUNKS;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(lds + i * 1024), 16, (m0 + r) * kb + swz<CHUNKS>(r, lane % CHUNKS) * 16, s * 64 * Q, 0, 0);
+  }
+  const int col = c0 + 64 * wave, at = min(col, c1 - 64) / 64 * G * kMx4GroupBytes;
+  const auto rw = mx4_rsrc(p.w + ex * p.w_expert, p.w_expert);
+  u4_t w[G][4];
+  Mx4Scales<Q> sw[G / Q];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[g][j] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16 + j * 1024, at + g / Q * Q * kMx4GroupBytes + g % Q * 4096, 0));
+#pragma unroll
+  for (int s = 0; s < G / Q; ++s) sw[s].template load<0>(rw, lane, at + s * Q * kMx4GroupBytes);
+  if (tid < bm) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) ls[g * bm + tid] = p.a_scale[(int64_t)g * p.a_rows + m0 + tid];
+    lid[tid] = id;
+    ltw[tid] = id < p.n_slots ? p.topk_w[id] : 0.f;
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // this wave's loads into LDS have landed
+  __syncthreads();
+  if (col >= c1) return;
+  int live = 0;  // rows that hold a slot: a prefix of the block
+  for (int b = 0; b < bm; b += 64) live += __popcll(__ballot(b + lane < bm && lid[min(b + lane, bm - 1)] < p.n_slots));
+  for (int r = 0; r < live; r += 16) {
+    f4_t acc[1][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[0][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const u4_t a = *reinterpret_cast<const u4_t*>(lds + ((g / Q) * bm + r + c16) * 64 * Q + swz<CHUNKS>(c16, 4 * (g % Q) + kq) * 16);
+      mx4_strip(w[g], a, acc[0], sw[g / Q].v[g % Q], ls[g * bm + r + c16] >> (8 * kq));
+    }
+    store_slot_rows<1>(p, lid + r, ltw + r, col, lane, acc);
+  }
 #endif
 }
 
-template <int MB, int MODE>
+__global__ void repack_mx4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ e8m0, uint8_t* __restrict__ out, int64_t N,
+                                  int64_t K, int paired, int64_t per, int64_t total) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t e = i / per;
+    alignas(16) uint8_t v[16];
+    mx4_repack_chunk(codes + e * N * (K / 2), e8m0 + e * N * (K / 32), N, K, paired, i - e * per, v);
+    reinterpret_cast<u4_t*>(out)[i] = *reinterpret_cast<const u4_t*>(v);
+  }
+}
+
+template <int MB, int H, int Q, int MODE>
 hipError_t launch_tiles(const Mx4Args& a, dim3 grid, hipStream_t s) {
   // the largest ring of the row counts a block may run with
   constexpr int LOW = MB < 4 ? MB : 4;
-  constexpr size_t lds = std::max<size_t>(Mx4Cfg<MB, mx4_stages(MB)>::LDS, Mx4Cfg<LOW, mx4_stages(LOW)>::LDS);
-  const hipError_t e = allow_lds<mx4_grouped<MB, MODE>>(lds);
-  return e != hipSuccess ? e : launch_timed(mx4_grouped<MB, MODE>, grid, dim3(64 * kWaves), lds, s, a);
+  constexpr size_t lds = std::max<size_t>(Mx4Cfg<MB, H, mx4_stages(MB, H), Q>::LDS, Mx4Cfg<LOW, H, mx4_stages(LOW, H), Q>::LDS);
+  const hipError_t e = allow_lds<mx4_grouped<MB, H, Q, MODE>>(lds);
+  return e != hipSuccess ? e : launch_timed(mx4_grouped<MB, H, Q, MODE>, grid, dim3(64 * kWaves * H), lds, s, a);
 }
 
-template <int MB>
-hipError_t launch_short(const Mx4Args& a, dim3 grid, hipStream_t s) {
-  const hipError_t e = allow_lds<mx4_down_short<MB>>(kShortLds);
-  return e != hipSuccess ? e : launch_timed(mx4_down_short<MB>, grid, dim3(64 * kWaves), (size_t)short_lds(16 * MB, a.G), s, a);
+template <int MB, int H>
+hipError_t launch_block(int mode, const Mx4Args& a, dim3 grid, hipStream_t s) {
+  if (mx4_groups(a.G) == 2) return mode == MX4_DOWN ? launch_tiles<MB, H, 2, MX4_DOWN>(a, grid, s) : launch_tiles<MB, H, 2, MX4_GATE_UP>(a, grid, s);
+  return mode == MX4_DOWN ? launch_tiles<MB, H, 1, MX4_DOWN>(a, grid, s) : launch_tiles<MB, H, 1, MX4_GATE_UP>(a, grid, s);
 }
 
-template <int MB>
-hipError_t launch_block(int mode, bool whole, const Mx4Args& a, dim3 grid, hipStream_t s) {
-  if (whole) return launch_short<MB>(a, grid, s);
-  return mode == MX4_DOWN ? launch_tiles<MB, MX4_DOWN>(a, grid, s) : launch_tiles<MB, MX4_GATE_UP>(a, grid, s);
+template <int G>
+hipError_t launch_short(const Mx4Args& a, int bm, dim3 grid, hipStream_t s) {
+  if constexpr (G <= kShortGroups) {
+    if (a.G != G) return launch_short<G + 1>(a, bm, grid, s);
+    const hipError_t e = allow_lds<mx4_down_short<G>>(short_lds(256, G));
+    return e != hipSuccess ? e : launch_timed(mx4_down_short<G>, grid, dim3(64 * kWaves), (size_t)short_lds(bm, G), s, a, bm);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
+
+int launch_mx4_repack(int64_t N, int64_t K, int64_t E, bool paired, const void* codes, const void* e8m0, void* w_out, void* stream) {
+  const int64_t per = mx4_weight_bytes(N, K) / 16;
+  hipLaunchKernelGGL(repack_mx4_kernel, dim3((unsigned)std::min<int64_t>((per * E + 255) / 256, 65536)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(e8m0),
+                     static_cast<uint8_t*>(w_out), N, K, (int)paired, per, per * E);
+  return (int)hipGetLastError();
+}
 
 int launch_mx4_grouped(int mode, int bm, const Mx4Args& a, int64_t blocks, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.G < 1 || a.N % (mode == MX4_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
   if (mode == MX4_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
+  if (bm != 16 && bm != 64 && bm != 128 && bm != 256) return (int)hipErrorInvalidValue;
   Mx4Args b = a;
-  const bool whole = mode == MX4_DOWN && short_lds(bm, a.G) <= kShortLds;
-  if (whole) {
-    const int64_t tiles = (a.ncol + 255) / 256;
-    const int64_t per = tiles * blocks >= 1536 ? 2 : 1;  // column tiles a workgroup walks
-    b.cols_wg = (int)(256 * per);
-    b.tiles_n = (int)((tiles + per - 1) / per);
-  } else {
-    b.tiles_n = (int)((mode == MX4_DOWN ? a.ncol : a.N) + 255) / 256;
-  }
+  b.tiles_n = (int)((mode == MX4_DOWN ? a.ncol : a.N) + 255) / 256;
   if (blocks * b.tiles_n > INT32_MAX) return (int)hipErrorInvalidValue;
   const dim3 grid((unsigned)(blocks * b.tiles_n));
+  if (mode == MX4_DOWN && a.G <= kShortGroups) return (int)launch_short<1>(b, bm, grid, s);
   switch (bm) {
-    case 16: return (int)launch_block<1>(mode, whole, b, grid, s);
-    case 64: return (int)launch_block<4>(mode, whole, b, grid, s);
-    case 128: return (int)launch_block<8>(mode, whole, b, grid, s);
+    case 16: return (int)launch_block<1, 1>(mode, b, grid, s);
+    case 64: return (int)launch_block<4, 1>(mode, b, grid, s);
+    case 128: return (int)launch_block<8, 1>(mode, b, grid, s);
   }
-  return (int)hipErrorInvalidValue;
+  return (int)launch_block<8, 2>(mode, b, grid, s);
 }
 
 }  // namespace hq

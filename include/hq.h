@@ -288,7 +288,9 @@ hq_status hq_repacked_bytes(const hq_plan* plan, size_t* w_bytes, size_t* meta_b
  * the 4-bit codes in gfx950 MFMA operand order.  All pointers are device
  * pointers; the work is a kernel on `stream`.  `zeros_or_e8m0` is NULL for
  * HQ_ZP_FIXED.  The output is a private layout: only hq_gemm / hq_moe_gemm
- * of a plan with the same layer description and activation type read it. */
+ * of a plan with the same layer description and activation type read it (W4A4: and of
+ * the same GEMM kind and epilogue; its grouped plans keep the scales among the codes
+ * and meta_bytes is 0). */
 hq_status hq_repack(const hq_plan* plan, const void* codes, const void* scales,
                     const void* zeros_or_e8m0, void* w_out, void* meta_out, void* stream);
 /* The same permutation on host memory (for preparing weights offline on a
