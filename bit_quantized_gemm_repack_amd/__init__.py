@@ -218,6 +218,10 @@ _SIGS = {
     "hq_route_experts": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
                                         ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                         ctypes.c_float] + [ctypes.c_void_p] * 3),
+    "hq_moe_mxfp4_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                                    ctypes.POINTER(ctypes.c_size_t)]),
+    "hq_moe_layer_mxfp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int] +
+                           [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
     "hq_moe_few_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_size_t)]),
     "hq_moe_layer_few": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
@@ -1242,16 +1246,32 @@ def _moe_mx4(gate_up, down, x, x_scale, ids, w, w1, m1, w2, m2):
     t, topk = ids.shape
     if t == 0:
         return x.new_empty((0, down.n), dtype=_TORCH_OUT[down.quant.out])
+    k = gate_up.k
     if x_scale is None:
-        if x.dtype not in (torch.float16, torch.bfloat16) or x.shape != (t, gate_up.k):
-            raise ValueError(f"x must be fp16 / bf16 [{t}, {gate_up.k}], or MXFP4 codes with x_scale")
-        x, x_scale = quantize_mxfp4(x)
-    bm = gate_up.block_m(t, topk)
-    if down.block_m(t, topk) != bm:
-        raise ValueError("the gate_up and down plans must share one alignment block size (equal tuning)")
-    sid, bex, npad = moe_align(ids, gate_up.num_experts, bm)
-    act, scale = gate_up.moe_gemm(x, t, topk, sid, bex, npad, w1, m1, a_scale=x_scale)
-    return down.moe_gemm(act, t, topk, sid, bex, npad, w2, m2, a_scale=scale, topk_w=w)
+        if x.dtype not in (torch.float16, torch.bfloat16) or x.shape != (t, k):
+            raise ValueError(f"x must be fp16 / bf16 [{t}, {k}], or MXFP4 codes with x_scale")
+        xt = BF16 if x.dtype == torch.bfloat16 else F16
+    else:
+        if x.shape != (t, k // 2) or x.element_size() != 1 or x.is_floating_point() or x_scale.dtype != torch.uint8 or \
+                x_scale.shape != (k // 128, t, 4):
+            raise ValueError(f"x must hold [{t}, {k // 2}] bytes of packed E2M1 codes and x_scale be uint8 [{k // 128}, {t}, 4]")
+        xt = FP4_E2M1
+    if ids.dtype != torch.int32 or w.shape != (t, topk) or w.dtype != torch.float32:
+        raise ValueError(f"topk_ids / topk_w must be int32 / float32 [{t}, {topk}]")
+    dev = x.device
+    if not _same_device(dev, x, ids, w, w1, w2) or x_scale is not None and not _same_device(dev, x_scale):
+        raise ValueError("the tensors of a w4a4_mxfp4 layer must be contiguous and on x's device")
+    gate_up._check_mx4_layout(w1, m1), down._check_mx4_layout(w2, m2)
+    need = gate_up._few_need.get((t, topk, down.k))
+    if need is None:
+        n = ctypes.c_size_t()
+        _check(lib().hq_moe_mxfp4_workspace_bytes(gate_up._h, down._h, t, topk, ctypes.byref(n)))
+        need = gate_up._few_need[t, topk, down.k] = n.value
+    ws = x.new_empty(need, dtype=torch.uint8)
+    out = x.new_empty((t, down.n), dtype=_TORCH_OUT[down.quant.out])
+    _run(dev, lib().hq_moe_layer_mxfp4, gate_up._h, down._h, t, topk, xt, x.data_ptr(), _ptr(x_scale), ids.data_ptr(), w.data_ptr(),
+         w1.data_ptr(), w2.data_ptr(), out.data_ptr(), ws.data_ptr(), need)
+    return out
 
 
 def moe_layer_routed(gate_up: "MoePlan", down: "MoePlan", x: torch.Tensor, logits: torch.Tensor, topk: int,

@@ -1853,6 +1853,153 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
   return ok();
 }
 
+// ---- the whole layer in MXFP4 ----
+static hq_status mx4_layer_check(const hq_plan* gu, const hq_plan* dn, int64_t t, int topk) {
+  if (!gu || !dn) return fail(HQ_ERR_INVALID_ARG, "null plan");
+  if (!hq::mx4_layout(gu) || !hq::mx4_layout(dn)) return fail(HQ_ERR_UNSUPPORTED, "the layer takes grouped MXFP4 x MXFP4 plans");
+  if (gu->compute.epi != HQ_EPI_SILU_MUL_QMX4 || dn->compute.epi != HQ_EPI_TOPK_COMBINE)
+    return fail(HQ_ERR_INVALID_ARG, "the layer takes a gate_up (SILU_MUL_QMX4) and a down (TOPK_COMBINE) plan");
+  if (gu->layer.num_experts != dn->layer.num_experts || gu->layer.n != 2 * dn->layer.k || gu->layer.k != dn->layer.n)
+    return fail(HQ_ERR_INVALID_ARG, "gate_up must be [2 I, H] and down [H, I] over the same experts");
+  if (t < 0 || t > gu->max_m || t > dn->max_m) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, max_m]");
+  if (topk < 1 || topk > 64) return fail(HQ_ERR_INVALID_ARG, "topk must be 1..64");
+  if (gu->layer.num_experts > 4096) return fail(HQ_ERR_UNSUPPORTED, "more than 4096 experts");
+  if (t * topk > (int64_t(1) << 20)) return fail(HQ_ERR_UNSUPPORTED, "t * topk above 2^20");
+  if (moe_choice(gu, t, topk).bm != moe_choice(dn, t, topk).bm)
+    return fail(HQ_ERR_INVALID_ARG, "the plans' tunings fix different block heights");
+  return HQ_OK;
+}
+
+// Whether the two kernels for a few tokens run the layer (a tuned block height asks for the
+// aligned path).
+static bool mx4_layer_few(const hq_plan* gu, int64_t t, int topk) {
+  return !gu->user.tile_m && (int64_t)gu->w_bytes_per_expert < (int64_t(1) << 31) &&
+         hq::mx4_few_ok(t, topk, gu->layer.num_experts, gu->layer.k, gu->layer.n / 2);
+}
+
+// Byte offsets into the layer's workspace; units and act alone for a few tokens.
+struct Mx4LayerWs {
+  size_t units, act, act_scale, x, x_scale, sorted, blocks, padded, gemm, total;
+};
+
+static Mx4LayerWs mx4_layer_ws(const hq_plan* gu, const hq_plan* dn, int64_t t, int topk) {
+  Mx4LayerWs w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at += align256(bytes);
+    return was;
+  };
+  const int64_t H = gu->layer.k, I = dn->layer.k;
+  if (mx4_layer_few(gu, t, topk)) {
+    w.units = take((size_t)((t + 15) / 16) * hq::kB8FewUnitInts * 4);
+    w.act = take(hq::mx4_few_act_bytes(t, topk, I));
+  } else {
+    const int bm = moe_choice(gu, t, topk).bm;
+    const int64_t mp = moe_max_padded(t, topk, gu->layer.num_experts, bm);
+    w.x = take((size_t)(t * H / 2));
+    w.x_scale = take((size_t)(t * H / 32));
+    w.sorted = take((size_t)mp * 4);
+    w.blocks = take((size_t)(mp / bm) * 4);
+    w.padded = take(4);
+    w.act = take((size_t)(mp * I / 2));
+    w.act_scale = take((size_t)(mp * I / 32));
+    w.gemm = take(moe_ws(dn, t, topk).total);
+  }
+  w.total = at;
+  return w;
+}
+
+hq_status hq_moe_mxfp4_workspace_bytes(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, size_t* bytes) {
+  if (!bytes) return fail(HQ_ERR_INVALID_ARG, "null argument");
+  const hq_status s = mx4_layer_check(gate_up, down, t, topk);
+  if (s != HQ_OK) return s;
+  *bytes = t ? mx4_layer_ws(gate_up, down, t, topk).total : 0;
+  return ok();
+}
+
+hq_status hq_moe_layer_mxfp4(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, hq_dtype x_type, const void* x,
+                             const void* x_scale, const int32_t* topk_ids, const float* topk_w, const void* w1, const void* w2,
+                             void* out, void* ws, size_t ws_bytes, void* stream) {
+  const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens
+  hq_status st = mx4_layer_check(gate_up, down, t, topk);
+  if (st != HQ_OK) return st;
+  if (x_type != HQ_F16 && x_type != HQ_BF16 && x_type != HQ_FP4_E2M1)
+    return fail(HQ_ERR_UNSUPPORTED, "x must be fp16, bf16 or MXFP4 codes");
+  if ((x_type == HQ_FP4_E2M1) != (x_scale != nullptr)) return fail(HQ_ERR_INVALID_ARG, "x_scale goes with MXFP4 codes");
+  if (t == 0) return ok();
+  if (!x || !topk_ids || !topk_w || !w1 || !w2 || !out) return fail(HQ_ERR_INVALID_ARG, "null device pointer");
+  for (const void* p : {x, x_scale, w1, w2, (const void*)out})
+    if (!aligned16(p)) return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  if (!aligned4(topk_ids) || !aligned4(topk_w)) return fail(HQ_ERR_INVALID_ARG, "topk_ids and topk_w must be aligned to their elements");
+  const Mx4LayerWs w = mx4_layer_ws(gate_up, down, t, topk);
+  if (!ws || ws_bytes < w.total) return fail(HQ_ERR_WORKSPACE, "this call needs %zu workspace bytes", w.total);
+  if (!aligned16(ws)) return fail(HQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  const int64_t H = gate_up->layer.k, I = down->layer.k;
+  const int E = gate_up->layer.num_experts;
+  if (mx4_layer_few(gate_up, t, topk)) {
+    hq::Mx4FewArgs a{};
+    a.x = x;
+    a.x_scale = static_cast<const uint32_t*>(x_scale);
+    a.topk_ids = topk_ids;
+    a.topk_w = topk_w;
+    a.w1 = static_cast<const uint8_t*>(w1);
+    a.w2 = static_cast<const uint8_t*>(w2);
+    a.units = reinterpret_cast<int32_t*>(wsb + w.units);
+    a.h = reinterpret_cast<float*>(wsb + w.act);
+    a.act = wsb + w.act;
+    a.act_scale = a.act + t * topk * (I / 2);
+    a.out = out;
+    a.w1_expert = (int64_t)gate_up->w_bytes_per_expert;
+    a.w2_expert = (int64_t)down->w_bytes_per_expert;
+    a.t = (int)t;
+    a.topk = topk;
+    a.E = E;
+    a.H = (int)H;
+    a.I = (int)I;
+    a.input = x_type == HQ_FP4_E2M1 ? hq::MX4_CODES : (x_type == HQ_BF16 ? hq::MX4_BF16 : hq::MX4_F16);
+    a.out_bf16 = down->layer.q.out == HQ_BF16;
+    hq::arm_timing(ev);
+    const int err = hq::launch_mx4_few(a, stream);
+    hq::arm_timing({nullptr, nullptr});
+    if (err != hipSuccess) return fail(HQ_ERR_HIP, "layer launch: %s", hipGetErrorString((hipError_t)err));
+    return ok();
+  }
+  const int bm = moe_choice(gate_up, t, topk).bm;
+  int32_t* sorted = reinterpret_cast<int32_t*>(wsb + w.sorted);
+  int32_t* blocks = reinterpret_cast<int32_t*>(wsb + w.blocks);
+  int32_t* padded = reinterpret_cast<int32_t*>(wsb + w.padded);
+  hq::Mx4PrepareArgs a{};
+  if (!x_scale) {
+    a.x = x;
+    x = wsb + w.x;
+    x_scale = wsb + w.x_scale;
+  }
+  a.codes = reinterpret_cast<uint32_t*>(wsb + w.x);
+  a.e8m0 = reinterpret_cast<uint32_t*>(wsb + w.x_scale);
+  a.ids = topk_ids;
+  a.sorted = sorted;
+  a.blocks = blocks;
+  a.padded = padded;
+  a.m = (uint32_t)t;
+  a.k8 = (uint32_t)(H / 8);
+  a.x_bf16 = x_type == HQ_BF16;
+  a.n_slots = (int)(t * topk);
+  a.E = E;
+  a.bm = bm;
+  hq::arm_timing({ev.start, nullptr});
+  const int err = hq::launch_mx4_prepare(a, stream);
+  hq::arm_timing({nullptr, nullptr});
+  if (err != hipSuccess) return fail(HQ_ERR_HIP, "layer launch: %s", hipGetErrorString((hipError_t)err));
+  // (the metadata of these plans is empty; their GEMMs ask for a pointer all the same)
+  st = hq_moe_gemm(gate_up, t, topk, x, x_scale, sorted, blocks, padded, nullptr, w1, w1, wsb + w.act, wsb + w.act_scale, nullptr, 0, stream);
+  if (st != HQ_OK) return st;
+  hq::arm_timing({nullptr, ev.stop});
+  return hq_moe_gemm(down, t, topk, wsb + w.act, wsb + w.act_scale, sorted, blocks, padded, topk_w, w2, w2, out, nullptr, wsb + w.gemm,
+                     w.total - w.gemm, stream);
+}
+
 hq_status hq_quantize_per_token(int64_t m, int64_t k, hq_dtype in, hq_dtype out, const void* x, void* codes,
                                 float* scales, void* stream) {
   const hq::TimingEvents ev = hq::take_timing();  // consumed by this call whatever happens

@@ -82,4 +82,47 @@ int launch_mx4_repack(int64_t N, int64_t K, int64_t E, bool paired, const void* 
 // Aligned blocks of bm rows (16, 64, 128) by 256 columns.
 int launch_mx4_grouped(int mode, int bm, const Mx4Args& a, int64_t blocks, void* stream);
 
+// Before the products of a layer (mx4_prepare.hip): x in MXFP4 (not where x is null), and the
+// slots by expert in blocks of bm rows, as hq_moe_align sorts them.
+struct Mx4PrepareArgs {
+  const void* x;  // 16-bit [m][8 k8]
+  uint32_t* codes;
+  uint32_t* e8m0;
+  const int32_t* ids;
+  int32_t* sorted;
+  int32_t* blocks;
+  int32_t* padded;
+  uint32_t m, k8;
+  int x_bf16;
+  int n_slots, E, bm;
+  int sorters;  // set by the launcher
+};
+int launch_mx4_prepare(const Mx4PrepareArgs& a, void* stream);
+
+// An experts' layer for a few tokens in two kernels (mx4_few.hip).
+enum Mx4Input : int { MX4_F16 = 0, MX4_BF16 = 1, MX4_CODES = 2 };
+constexpr int kMx4FewTokens = 64, kMx4FewTopk = 16;
+struct Mx4FewArgs {
+  const void* x;             // [t][H] 16-bit, or codes [t][H / 2]
+  const uint32_t* x_scale;   // of codes: [H / 128][t]
+  const int32_t* topk_ids;   // [t][topk]
+  const float* topk_w;
+  const uint8_t* w1;         // 2I x H per expert
+  const uint8_t* w2;         // H x I
+  float* h;                  // gate and up [t * topk][2 I], or
+  uint8_t* act;              // codes [t * topk][I / 2] and, behind them, their
+  uint8_t* act_scale;        // powers of two [t * topk][I / 32]: the launcher's choice, in the same place
+  void* out;                 // [t][H]
+  int32_t* units;            // per tile of 16 tokens kB8FewUnitInts, for t > 1
+  int64_t w1_expert, w2_expert;
+  int t, topk, E, H, I;
+  int input, out_bf16;
+  int rows;                  // rows of x a gate_up workgroup holds (set by its launcher)
+};
+// Whether the two kernels take t tokens of this layer.
+bool mx4_few_ok(int64_t t, int64_t topk, int64_t E, int64_t H, int64_t I);
+// Bytes of h, or of act and act_scale.
+size_t mx4_few_act_bytes(int64_t t, int64_t topk, int64_t I);
+int launch_mx4_few(const Mx4FewArgs& a, void* stream);
+
 }  // namespace hq

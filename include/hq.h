@@ -548,6 +548,29 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
                            float* topk_w, const void* w1, const void* meta1, const void* w2, const void* meta2,
                            void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* A whole experts' layer in MXFP4 (W4A4 plans: gate_up [2 I, H] with SILU_MUL_QMX4, down
+ * [H, I] with TOPK_COMBINE, the same experts):
+ *   y[i] = sum_j topk_w[i, j] q(SiLU(g) * u) W2[e]^T,  (g, u) = halves of q(x[i]) W1[e]^T,
+ * e = topk_ids[i, j], q as hq_quantize_mxfp4.  A few tokens run in two kernels, others as
+ * hq_quantize_mxfp4, hq_moe_align and the two GEMMs do, with the same roundings but for a
+ * slot's row of down, which only they round (to fp16 with a scale by 64 columns).
+ *   x         device [t, H] fp16 / bf16, or E2M1 codes [t, H/2] (x_type HQ_FP4_E2M1)
+ *   x_scale   of codes: device E8M0 [H/128, t, 4], as hq_quantize_mxfp4 and hq_rms_norm
+ *             write them; NULL for 16 bits
+ *   topk_ids, topk_w  device [t, topk]: ids outside [0, num_experts) contribute zero, an id
+ *             may come twice in a row
+ *   w1, w2    as hq_plan_repack wrote them (their metadata is empty)
+ *   out       device [t, H] in the down plan's out dtype
+ *   ws        hq_moe_mxfp4_workspace_bytes bytes, no initialisation needed; two calls
+ *             that overlap in time must not share one
+ * topk_ids and topk_w are aligned to their elements, the others to 16 bytes.
+ * Deterministic.  topk <= 64, t * topk <= 2^20, num_experts <= 4096; t = 0 is a no-op.
+ * Honours hq_time_next_launch (first kernel to last). */
+hq_status hq_moe_mxfp4_workspace_bytes(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, size_t* bytes);
+hq_status hq_moe_layer_mxfp4(const hq_plan* gate_up, const hq_plan* down, int64_t t, int topk, hq_dtype x_type, const void* x,
+                             const void* x_scale, const int32_t* topk_ids, const float* topk_w, const void* w1, const void* w2,
+                             void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Per-token activation quantiser: the step before a W4A8 GEMM, which takes
  * 8-bit activations with one fp32 scale per row (W4A8: INT8 or FP8

@@ -175,6 +175,36 @@ def test_layer(t, e, topk, h, i, dt):
     assert torch.equal(y, L.run(x, ids, w)), "twice"
 
 
+@pytest.mark.parametrize("t,e,topk,h,i", [(1, 20, 16, 2048, 640), (1, 8, 1, 2048, 128), (2, 8, 8, 2176, 384), (4, 8, 8, 4096, 256), (5, 12, 8, 4096, 128),
+                                          (9, 256, 8, 7168, 256), (16, 3, 2, 7168, 384), (17, 3, 1, 7168, 128), (33, 40, 2, 7168, 512), (64, 5, 1, 7168, 256),
+                                          (15, 1, 4, 7168, 128), (2, 8, 1, 2048, 7168)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_layer_of_few_tokens(t, e, topk, h, i, dt):
+    """The two kernels: slots without an expert, an expert twice in a row, NaN rows, one expert for many."""
+    print(f"[gpu case] few {t} {e} {topk} {h} {i} {dt}", flush=True)
+    L = Layer(t + e, e, h, i, t, dt)
+    x = _x(L.g, t, h, DT[dt])
+    ids = torch.randint(-1, e + 1, (t, topk), generator=L.g, device=DEV).to(torch.int32)
+    w = torch.randn(t, topk, generator=L.g, device=DEV)
+    y = L.run(x, ids, w)
+    torch.cuda.synchronize()
+    L.check(y, x, ids, w, "random ids")
+    codes, s = hq.quantize_mxfp4(x)
+    assert torch.equal(y, L.run(codes, ids, w, x_scale=s)), "quantised outside"
+    hit = ((ids >= 0) & (ids < e)).any(-1)
+    assert (y[~hit] == 0).all()
+    if t > 1:
+        bad = x.clone()
+        bad[t - 1, 7] = float("nan")
+        z = L.run(bad, ids, w)
+        torch.cuda.synchronize()
+        assert torch.equal(z[: t - 1], y[: t - 1]) and z[t - 1].isnan().all() == hit[t - 1]
+    one = torch.full_like(ids, e - 1)
+    y = L.run(x, one, w)
+    torch.cuda.synchronize()
+    L.check(y, x, one, w, "one expert")
+
+
 def test_layer_windows():
     """Enough slots for two column windows of the down product (240 MiB of rows)."""
     t, e, topk, h, i = 9000, 8, 8, 2048, 128
