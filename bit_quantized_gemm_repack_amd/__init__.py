@@ -304,7 +304,8 @@ def _bind_calls(L):
         if native.built_for != torch.__version__:
             raise ImportError(f"built for torch {native.built_for}, this is {torch.__version__}")
         native.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes)))
+                      for f in (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes, L.hq_rms_norm,
+                                L.hq_route_experts)))
     except Exception as e:  # a damaged file, another torch's: every call works without it
         warnings.warn(f"{CALLS_PATH} is not used ({e}): short calls go through ctypes; build again to have it", RuntimeWarning)
         return
@@ -865,6 +866,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     Returns y, or (codes, scales); with a residual h comes last: (y, h) or (codes,
     scales, h), written into residual_out where that is given (which may be x or
     the residual)."""
+    if _calls is not None:
+        r = _calls.rms_norm(x, weight, eps, residual, _NORM.get(out), residual_out)
+        if r is not None:
+            return r
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
     if x.dim() != 2 or x.dtype not in (torch.float16, torch.bfloat16) or (x.shape[1] > 1 and x.stride(1) != 1):
@@ -1175,6 +1180,10 @@ def route_experts(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] 
     only experts of the group_topk best groups are chosen, a group's score being the
     sum of its group_best (1 or 2) best.  Returns (ids int32 [t, topk], weights
     float32 [t, topk]), the (topk_ids, topk_w) of moe_layer."""
+    if _calls is not None:
+        r = _calls.route_experts(logits, topk, bias, _SCORE.get(scoring), groups, group_topk, group_best, renormalize, scale)
+        if r is not None:
+            return r
     _dev(logits, "logits")
     if logits.dim() != 2 or logits.dtype not in _LOGITS:
         raise ValueError("logits must be fp32 / fp16 / bf16 [t, experts]")

@@ -25,6 +25,8 @@ decltype(&hq_quantize_blocks) quantize_fn;
 decltype(&hq_route_topk) route_fn;
 decltype(&hq_gemm) gemm_fn;
 decltype(&hq_plan_workspace_bytes) workspace_fn;
+decltype(&hq_rms_norm) norm_fn;
+decltype(&hq_route_experts) route_experts_fn;
 
 const at::Tensor* tensor(PyObject* o) {
   if (!THPVariable_Check(o)) return nullptr;
@@ -109,6 +111,100 @@ PyObject* route_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Rows [m, k] of x's type and device, contiguous inside; the step from one to the next (of one
+// row it says nothing).
+const at::Tensor* rows(PyObject* o, const at::Tensor* like) {
+  if (!THPVariable_Check(o)) return nullptr;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda() || t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1)) return nullptr;
+  if (like && (t.device() != like->device() || t.scalar_type() != like->scalar_type() || t.sizes() != like->sizes())) return nullptr;
+  return &t;
+}
+int64_t row_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
+// rms_norm(x, weight, eps, residual or None, kind, residual_out or None)
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor* x = n == 6 && PyFloat_Check(a[2]) && PyLong_Check(a[4]) ? rows(a[0], nullptr) : nullptr;
+    if (!x || act_type(*x) < 0 || !current(*x)) return nullptr;
+    const int64_t m = x->size(0), k = x->size(1);
+    const at::Tensor* w = tensor(a[1]);
+    if (!w || w->dim() != 1 || w->size(0) != k || w->device() != x->device() ||
+        (w->scalar_type() != x->scalar_type() && w->scalar_type() != at::kFloat))
+      return nullptr;
+    const bool add = a[3] != Py_None, given = a[5] != Py_None;
+    const at::Tensor* res = add ? rows(a[3], x) : nullptr;
+    const at::Tensor* into = given ? rows(a[5], x) : nullptr;
+    if ((add && !res) || (given && (!into || !add))) return nullptr;
+    const auto kind = (hq_norm_kind)PyLong_AsLong(a[4]);
+    const float eps = (float)PyFloat_AS_DOUBLE(a[2]);
+    const bool blocks = kind == HQ_NORM_FP8_BLOCK || kind == HQ_NORM_MXFP4;
+    if (kind < HQ_NORM_SAME || kind > HQ_NORM_MXFP4 || (blocks && k % 128)) return nullptr;
+    at::Tensor h, y, scale;
+    {
+      const Unlocked unlocked;
+      if (add) h = given ? *into : at::empty({m, k}, x->options());
+      if (kind == HQ_NORM_SAME)
+        y = at::empty({m, k}, x->options());
+      else
+        y = at::empty({m, kind == HQ_NORM_MXFP4 ? k / 2 : k}, x->options().dtype(kind == HQ_NORM_INT8 ? at::kChar : at::kByte));
+      if (kind == HQ_NORM_MXFP4)
+        scale = at::empty({k / 128, m, 4}, x->options().dtype(at::kByte));
+      else if (blocks)
+        scale = at::empty({k / 128, m}, x->options().dtype(at::kFloat));
+      else if (kind != HQ_NORM_SAME)
+        scale = at::empty({m}, x->options().dtype(at::kFloat));
+      const auto type = (hq_dtype)act_type(*x);
+      if (norm_fn(m, k, type, x->data_ptr(), row_stride(*x), add ? res->data_ptr() : nullptr, add ? row_stride(*res) : 0,
+                  w->scalar_type() == at::kFloat ? HQ_F32 : type, w->data_ptr(), eps, kind, add ? h.data_ptr() : nullptr,
+                  add ? row_stride(h) : 0, y.data_ptr(), scale.defined() ? scale.data_ptr() : nullptr, stream(*x)) != HQ_OK)
+        return nullptr;
+    }
+    if (!add) return scale.defined() ? pair(std::move(y), std::move(scale)) : THPVariable_Wrap(std::move(y));
+    if (!scale.defined()) return pair(std::move(y), std::move(h));
+    PyObject* r = PyTuple_New(3);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(y)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(scale)));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(h)));
+    return r;
+  });
+}
+
+// route_experts(logits, topk, bias or None, scoring, groups, group_topk, group_best, renormalize, scale)
+PyObject* route_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor* x = n == 9 ? tensor(a[0]) : nullptr;
+    if (!x || x->dim() != 2 || !current(*x) || !PyFloat_Check(a[8])) return nullptr;
+    for (int i : {1, 3, 4, 5, 6})
+      if (!PyLong_Check(a[i])) return nullptr;
+    const int type = x->scalar_type() == at::kFloat ? HQ_F32 : act_type(*x);
+    const int64_t t = x->size(0), experts = x->size(1), topk = PyLong_AsLongLong(a[1]);
+    int64_t v[4];
+    for (int i = 0; i < 4; ++i) {
+      v[i] = PyLong_AsLongLong(a[3 + i]);
+      if (v[i] < 0 || v[i] > 1024) return nullptr;
+    }
+    const int renorm = PyObject_IsTrue(a[7]);
+    if (type < 0 || topk < 1 || topk > 64 || experts > 1024 || renorm < 0) return nullptr;
+    const at::Tensor* bias = a[2] != Py_None ? tensor(a[2]) : nullptr;
+    if (a[2] != Py_None && (!bias || bias->device() != x->device() || bias->scalar_type() != at::kFloat || bias->dim() != 1 || bias->size(0) != experts))
+      return nullptr;
+    at::Tensor ids, w;
+    {
+      const Unlocked unlocked;
+      ids = at::empty({t, topk}, x->options().dtype(at::kInt));
+      w = at::empty({t, topk}, x->options().dtype(at::kFloat));
+      if (route_experts_fn(t, (int)experts, (int)topk, (hq_dtype)type, x->data_ptr(), (hq_score)v[0],
+                           bias ? static_cast<const float*>(bias->data_ptr()) : nullptr, (int)v[1], (int)v[2], (int)v[3], renorm,
+                           (float)PyFloat_AS_DOUBLE(a[8]), static_cast<int32_t*>(ids.data_ptr()), static_cast<float*>(w.data_ptr()),
+                           stream(*x)) != HQ_OK)
+        return nullptr;
+    }
+    return pair(std::move(ids), std::move(w));
+  });
+}
+
 // gemm_block(plan, n, k, bf16, a, a_scale, w, meta): a w8a8_block GEMM with its
 // output and workspace
 PyObject* gemm_block(PyObject*, PyObject* const* v, Py_ssize_t count) {
@@ -141,16 +237,18 @@ PyObject* gemm_block(PyObject*, PyObject* const* v, Py_ssize_t count) {
   });
 }
 
-// bind(addresses of hq_quantize_blocks, hq_route_topk, hq_gemm, hq_plan_workspace_bytes)
+// bind(addresses of hq_quantize_blocks, hq_route_topk, hq_gemm, hq_plan_workspace_bytes, hq_rms_norm, hq_route_experts)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
     return nullptr;
   }
   quantize_fn = reinterpret_cast<decltype(quantize_fn)>(PyLong_AsVoidPtr(a[0]));
   route_fn = reinterpret_cast<decltype(route_fn)>(PyLong_AsVoidPtr(a[1]));
   gemm_fn = reinterpret_cast<decltype(gemm_fn)>(PyLong_AsVoidPtr(a[2]));
   workspace_fn = reinterpret_cast<decltype(workspace_fn)>(PyLong_AsVoidPtr(a[3]));
+  norm_fn = reinterpret_cast<decltype(norm_fn)>(PyLong_AsVoidPtr(a[4]));
+  route_experts_fn = reinterpret_cast<decltype(route_experts_fn)>(PyLong_AsVoidPtr(a[5]));
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -161,6 +259,8 @@ PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"quantize_blocks", fast(quantize_blocks), METH_FASTCALL, nullptr},
                          {"route_topk", fast(route_topk), METH_FASTCALL, nullptr},
+                         {"rms_norm", fast(rms_norm), METH_FASTCALL, nullptr},
+                         {"route_experts", fast(route_experts), METH_FASTCALL, nullptr},
                          {"gemm_block", fast(gemm_block), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -90,3 +90,14 @@ def test_oracle_sees_a_step():
 
 def test_oracle_values4():
     assert on.values4(torch.tensor([[0x21, 0xF8]], dtype=torch.uint8)).tolist() == [[0.5, 1.0, -0.0, -6.0]]
+
+
+def test_native_call_takes_nothing_else():
+    """What is no GPU tensor of the right kind is left to the Python checks."""
+    hq.lib()
+    if hq._calls is None:
+        pytest.skip("the native calls are not built")
+    x, w = torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(256)
+    for args in ((), (x,), (None, w, 1e-6, None, 0, None), (x, w, 1e-6, None, 0, None), (x, w, 1, None, 0, None), (x, w, 1e-6, None, None, None),
+                 (x, w, 1e-6, None, 1 << 70, None), ("x", "w", 1e-6, 3, 0, 4)):
+        assert hq._calls.rms_norm(*args) is None

@@ -185,3 +185,40 @@ def test_refusals():
         kw = dict(dict(weight=w), **kw)
         with pytest.raises(hq.HQError):
             hq.rms_norm(kw.pop("x"), kw.pop("weight"), **kw)
+
+
+def test_native_calls_are_the_same(monkeypatch):
+    """The binding's native call against the same call through ctypes, on another stream
+    too: each output, strided rows, h written in place, no rows."""
+    g = _gen(40)
+    x, wide, odd = _x(g, 9, 512, torch.bfloat16), _x(g, 9, 1104, torch.bfloat16), _x(g, 9, 1100, torch.bfloat16)
+    w, w32 = torch.randn(512, device=DEV).bfloat16(), torch.randn(512, device=DEV)
+
+    def calls():
+        r = []
+        for out in KINDS:
+            for a in (x, wide[:, 8:520], x[3:4], x[:0]):
+                y = hq.rms_norm(a, w, out=out)
+                r += y if isinstance(y, tuple) else (y,)
+                r += hq.rms_norm(a, w32, 1e-5, residual=wide[: len(a), 520:1032], out=out)
+            h = x.clone()
+            y = hq.rms_norm(x, w, residual=h, out=out, residual_out=h)
+            assert y[-1] is h or y[-1].data_ptr() == h.data_ptr()
+            r += y
+        return r
+    assert hq._calls is not None and hq._calls.rms_norm(x, w, 1e-6, None, 4, None) is not None
+    native = calls()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        other = calls()
+    torch.cuda.synchronize()
+    assert hq._calls.rms_norm(odd[:, :512], w, 1e-6, None, 0, None) is None                 # rows of 1100
+    assert hq._calls.rms_norm(x.t(), w, 1e-6, None, 0, None) is None and hq._calls.rms_norm(x, w[1:], 1e-6, None, 0, None) is None
+    assert hq._calls.rms_norm(x, w, 1e-6, None, 0, x) is None and hq._calls.rms_norm(x, w, -1.0, None, 0, None) is None
+    assert hq._calls.rms_norm(x, w, 1e-6, x[1:], 0, None) is None and hq._calls.rms_norm(wide, wide[0], 1e-6, None, 3, None) is None
+    monkeypatch.setattr(hq, "_calls", None)
+    plain = calls()
+    torch.cuda.synchronize()
+    assert len(native) == len(plain)
+    for p, q, r in zip(native, other, plain):
+        assert p.dtype == r.dtype and p.shape == r.shape and torch.equal(p, r) and torch.equal(q, r)

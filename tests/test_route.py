@@ -74,3 +74,14 @@ def test_oracle_values():
     assert ids.tolist() == [[2, 3]]                                   # two good ones beat one
     ids, _ = orr.route(torch.tensor([[3.0, -9.0, 2.0, 2.0]]), 2, groups=2, group_topk=1, group_best=1, scoring="softmax")
     assert ids.tolist() == [[0, 1]]
+
+
+def test_native_call_takes_nothing_else():
+    """What is no GPU tensor of the right kind is left to the Python checks."""
+    hq.lib()
+    if hq._calls is None:
+        pytest.skip("the native calls are not built")
+    x = torch.zeros(2, 8)
+    for args in ((), (x,), (x, 2, None, 0, 1, 1, 2, True, 1.0), (x, 2, x, None, 1, 1, 2, True, 1.0), (3, 2, None, 0, 1, 1, 2, True, 1.0),
+                 (x, 1 << 70, None, 0, 1, 1, 2, True, 1.0), (x, 2, None, 0, 1, 1, 1 << 70, True, 1.0), (x, 2, None, 0, 1, 1, 2, True, 1)):
+        assert hq._calls.route_experts(*args) is None

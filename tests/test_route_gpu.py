@@ -156,3 +156,26 @@ def test_refusals():
                dict(scale=math.inf)):
         with pytest.raises(hq.HQError):
             hq.route_experts(x, **dict(dict(topk=4), **kw))
+
+
+def test_native_calls_are_the_same(monkeypatch):
+    """The binding's native call against the same call through ctypes, on another stream too."""
+    x = torch.randn(9, 64, generator=_gen(41), device=DEV)
+    b = torch.randn(64, generator=_gen(42), device=DEV)
+
+    def calls():
+        return [*hq.route_experts(x, 4), *hq.route_experts(x.half(), 6, b, "softmax", 8, 3, 1, False, 2.5), *hq.route_experts(x.bfloat16(), 1, b),
+                *hq.route_experts(x[:0], 3), *hq.route_experts(x, 8, bias=b, groups=4, group_topk=2, scale=0.5)]
+    assert hq._calls is not None and hq._calls.route_experts(x, 4, b, 0, 1, 1, 2, True, 1.0) is not None
+    native = calls()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        other = calls()
+    torch.cuda.synchronize()
+    assert hq._calls.route_experts(x.t(), 4, None, 0, 1, 1, 2, True, 1.0) is None and hq._calls.route_experts(x, 65, None, 0, 1, 1, 2, True, 1.0) is None
+    assert hq._calls.route_experts(x, 4, b[1:], 0, 1, 1, 2, True, 1.0) is None and hq._calls.route_experts(x, 4, b, 0, 7, 1, 2, True, 1.0) is None
+    monkeypatch.setattr(hq, "_calls", None)
+    plain = calls()
+    torch.cuda.synchronize()
+    for p, q, r in zip(native, other, plain):
+        assert p.dtype == r.dtype and p.shape == r.shape and torch.equal(p, r) and torch.equal(q, r)
