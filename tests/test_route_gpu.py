@@ -158,6 +158,32 @@ def test_refusals():
             hq.route_experts(x, **dict(dict(topk=4), **kw))
 
 
+@pytest.mark.parametrize("t,e,topk,kw,dt", [(4096, 64, 6, dict(), "bf16"), (4100, 8, 2, dict(scoring="softmax"), "f32"),
+                                           (5121, 128, 16, dict(groups=16, group_topk=5, group_best=1), "f16"), (7001, 160, 6, dict(scoring="softmax", groups=8, group_topk=3), "bf16"),
+                                           (10241, 256, 8, dict(bias=True, groups=8, group_topk=4, scale=2.5), "f32"), (10250, 250, 1, dict(renormalize=False), "f32"),
+                                           (4111, 100, 10, dict(groups=10, group_topk=2, bias=True), "f32"), (4097, 17, 16, dict(scoring="softmax", bias=True), "f32")])
+def test_many_tokens_are_single_ones(t, e, topk, kw, dt):
+    """The kernel of many tokens gives the bits of the other one, for ties, experts shut off and rows without any."""
+    print(f"[gpu case] many {t} {e} {topk} {kw} {dt}", flush=True)
+    g = _gen(e)
+    x = torch.randn(t, e, generator=g, device=DEV)
+    x[::3] = (x[::3] * 2).round() / 2                              # ties
+    x[torch.rand(t, e, generator=g, device=DEV) < 0.05] = -math.inf
+    x[5], x[6, 1:], x[t - 1, 0] = -math.inf, float("nan"), float("nan")
+    x = x.to(DT[dt])
+    if kw.get("bias"):
+        kw = dict(kw, bias=torch.randn(e, generator=g, device=DEV))
+    ids, w = hq.route_experts(x, topk, **kw)
+    parts = [hq.route_experts(x[i:i + 1500], topk, **kw) for i in range(0, t, 1500)]
+    torch.cuda.synchronize()
+    assert torch.equal(ids, torch.cat([p[0] for p in parts])) and torch.equal(w, torch.cat([p[1] for p in parts]))
+    rows = torch.cat([torch.arange(40, device=DEV), torch.arange(t - 40, t, device=DEV)])
+    kw = {k: v.cpu() if k == "bias" else v for k, v in kw.items()}
+    wi, ww = orr.route(x[rows].cpu(), topk, **kw)
+    assert torch.equal(ids[rows].cpu(), wi)
+    assert ((w[rows].cpu().double() - ww).abs() <= orr.WEIGHT * ww.abs() + 2.0 ** -149).all()
+
+
 def test_native_calls_are_the_same(monkeypatch):
     """The binding's native call against the same call through ctypes, on another stream too."""
     x = torch.randn(9, 64, generator=_gen(41), device=DEV)
