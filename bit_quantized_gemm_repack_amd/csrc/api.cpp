@@ -622,7 +622,7 @@ hq_status hq_plan_create(const hq_layer_desc* layer, const hq_compute* compute, 
         return fail(HQ_ERR_UNSUPPORTED, "the combining down GEMM needs n a multiple of 64");
       if (tuning) {
         const int tm = tuning->tile_m, tn = tuning->tile_n;
-        if (tm != 0 && tm != 16 && tm != 32 && tm != 64 && tm != 128 && !(tm == 256 && fmt == hq::FMT_F44))
+        if (tm != 0 && tm != 16 && tm != 32 && tm != 64 && tm != 128)
           return fail(HQ_ERR_UNSUPPORTED, "grouped tile_m must be 16 or 32 (skinny), 64 or 128 (tiled)");
         if (tuning->kernel == hq::KER_SKINNY && tm > 32)
           return fail(HQ_ERR_UNSUPPORTED, "the skinny grouped kernel uses 16- or 32-row blocks");
@@ -1072,18 +1072,31 @@ static MoeChoice moe_choice(const hq_plan* p, int64_t t, int topk) {
   const double per_expert = (double)t * topk / p->layer.num_experts;
   if (hq::block_grouped(p->fmt)) {
     c.tiled = true;
-    // blocks a little taller than what lands on an expert: a block is run with
-    // as many rows as it holds, but one more block reads the weights again
-    // (256 experts, top 8, H = 7168, I = 256, us a layer with 16 / 64 / 128-row
-    // blocks: 128 tokens 230 / 234 / 233, 509 336 / 311 / 322, 1024 427 / 379 /
-    // 383, 2048 606 / 498 / 470) ...
-    c.bm = per_expert <= 6 ? 16 : (per_expert <= 64 ? 64 : 128);
-    // ... and lower ones where gate_up would leave CUs idle (16 experts, top 2, H
-    // = 4096, I = 512: 300 tokens 46.8 / 63.1 / 69.1, 700 66.0 / 68.2 / 77.7, 1500
-    // 116 / 84 / 87).  Both plans of a layer come to the same block.
     const int64_t inter = p->compute.epi == HQ_EPI_TOPK_COMBINE ? p->layer.k : N / 2;
     const double hit = std::min<double>(p->layer.num_experts, (double)t * topk);
-    while (c.bm > 16 && hit * std::ceil(per_expert / c.bm) * (double)(inter / 128) < 150) c.bm = c.bm == 128 ? 64 : 16;
+    auto tiles = [&] { return hit * std::ceil(per_expert / c.bm) * (double)(inter / 128); };  // of gate_up
+    if (p->fmt == hq::FMT_F44) {
+      // as below, with the heights where MXFP4's products meet (256 experts, top 8, H =
+      // 7168, I = 256, us a layer with 16 / 64 / 128-row blocks: 128 tokens 131 / 132 / 133,
+      // 300 157 / 140 / 142, 1000 236 / 187 / 192, 2048 359 / 299 / 264, 4096 625 / 453 / 455) ...
+      c.bm = per_expert <= 6 ? 16 : (per_expert <= 48 ? 64 : 128);
+      // ... and with two workgroups a CU to fill (64 experts, H = 2048, I = 768: 509 tokens
+      // 63.2 / 60.5 / 62.0, 1000 96.0 / 70.6 / 75.1; 16 experts, top 2, H = 4096, I = 512: 300
+      // tokens 27.7 / 35.8 / 36.5, 509 38.0 / 40.9 / 51.3, 1000 51.5 / 42.5 / 60.0, 2048 76 / 60 / 62)
+      if (c.bm == 128 && tiles() < 400) c.bm = 64;
+      if (c.bm == 64 && tiles() < 100) c.bm = 16;
+    } else {
+      // blocks a little taller than what lands on an expert: a block is run with
+      // as many rows as it holds, but one more block reads the weights again
+      // (256 experts, top 8, H = 7168, I = 256, us a layer with 16 / 64 / 128-row
+      // blocks: 128 tokens 230 / 234 / 233, 509 336 / 311 / 322, 1024 427 / 379 /
+      // 383, 2048 606 / 498 / 470) ...
+      c.bm = per_expert <= 6 ? 16 : (per_expert <= 64 ? 64 : 128);
+      // ... and lower ones where gate_up would leave CUs idle (16 experts, top 2, H
+      // = 4096, I = 512: 300 tokens 46.8 / 63.1 / 69.1, 700 66.0 / 68.2 / 77.7, 1500
+      // 116 / 84 / 87).  Both plans of a layer come to the same block.
+      while (c.bm > 16 && tiles() < 150) c.bm = c.bm == 128 ? 64 : 16;
+    }
     if (u.tile_m) c.bm = u.tile_m;
     c.tl.bm = c.bm;
     c.tl.nbw = 4;

@@ -24,19 +24,19 @@ namespace hq {
 
 namespace {
 
-// A workgroup of 4 H waves computes BM = 16 MB H rows by 256 columns: each wave MB row
-// blocks and a strip of 64 columns, whose weights go straight to registers; with H = 2 two
-// waves share a strip, and the second finds it in the first-level cache.  A step covers Q
-// groups of 128 k: with two, an activation row is a whole 128-byte line.
+// A workgroup of four waves computes BM = 16 MB rows by 256 columns: each wave the rows by a
+// strip of 64 columns, whose weights go straight to registers.  A step covers Q groups of 128
+// k: with two, an activation row is a whole 128-byte line.  (Blocks of 256 rows by eight waves
+// read an expert's weights less often, but wait more for their rows: 4096 tokens of 256 experts
+// gate_up 196 us against 160.)
 constexpr int kWaves = 4;
-template <int MB, int H, int ST, int Q>
+template <int MB, int ST, int Q>
 struct Mx4Cfg {
-  static constexpr int WAVES = kWaves * H;
-  static constexpr int BM = 16 * MB * H;
+  static constexpr int BM = 16 * MB;
   static constexpr int CHUNKS = 4 * Q;                                    // 16-byte chunks of a row
   static constexpr int SEG_ROWS = 64 / CHUNKS;                            // rows of a 1 KiB load
   static constexpr int SEGS = BM / SEG_ROWS;
-  static constexpr int SEGW = SEGS > WAVES ? SEGS / WAVES : 1;            // such loads a wave
+  static constexpr int SEGW = SEGS > kWaves ? SEGS / kWaves : 1;            // such loads a wave
   static constexpr int SROWS = BM < 64 ? 64 : BM;                         // row scales a group (whole 64-lane loads)
   static constexpr int SCALES = BM * 64 * Q;                              // where they lie in a stage
   static constexpr int STAGE = SCALES + Q * SROWS * 4;
@@ -48,16 +48,15 @@ __device__ inline __amdgpu_buffer_rsrc_t mx4_rsrc(const void* base, int64_t byte
 }
 
 // One tile: rows m0 .. m0 + 16 MB - 1, column tile tn.
-template <int MB, int H, int ST, int Q, int MODE, int AUX>
+template <int MB, int ST, int Q, int MODE, int AUX>
 __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0, int64_t ex, int tn) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  using C = Mx4Cfg<MB, H, ST, Q>;
+  using C = Mx4Cfg<MB, ST, Q>;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kq = lane >> 4;
   const int N = p.N, G = p.G, kb = p.K / 2, steps = G / Q;
-  const int sw = wave % kWaves, r0 = H > 1 ? wave / kWaves * 16 * MB : 0;  // strip of the tile, first row of this wave's
-  const int strip = (MODE == MX4_DOWN ? p.col0 / 64 : 0) + tn * 4 + sw;
+  const int strip = (MODE == MX4_DOWN ? p.col0 / 64 : 0) + tn * 4 + wave;
   const int first = __builtin_amdgcn_readfirstlane(min(strip, N / 64 - 1) * steps * Q * kMx4GroupBytes);  // past N: loaded again, not stored
 
   const auto ra = mx4_rsrc(p.a, (int64_t)p.a_rows * kb);
@@ -77,7 +76,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
   int aoff[C::SEGW], alds[C::SEGW];
 #pragma unroll
   for (int s = 0; s < C::SEGW; ++s) {
-    const int seg = (wave + C::WAVES * s) % C::SEGS;
+    const int seg = (wave + kWaves * s) % C::SEGS;
     const int r = seg * C::SEG_ROWS + lane / C::CHUNKS;
     aoff[s] = row_of(r) * kb + swz<C::CHUNKS>(r, lane % C::CHUNKS) * 16;
     alds[s] = seg * 1024;
@@ -114,8 +113,8 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
 
   auto compute = [&](auto slot_c) {
     constexpr int slot = decltype(slot_c)::value;
-    const uint8_t* at = lds + slot * C::STAGE + (r0 + c16) * 64 * Q;
-    const uint8_t* st = lds + slot * C::STAGE + C::SCALES + (r0 + c16) * 4 + kq;
+    const uint8_t* at = lds + slot * C::STAGE + c16 * 64 * Q;
+    const uint8_t* st = lds + slot * C::STAGE + C::SCALES + c16 * 4 + kq;
 #pragma unroll
     for (int u = 0; u < Q; ++u)
 #pragma unroll
@@ -162,10 +161,10 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
       for (int i = 0; i < 8; ++i) v[i] = b8_silu_mul(acc[mb][i >> 2][i & 3], acc[mb][2 + (i >> 2)][i & 3]);
       uint32_t s;
       const uint32_t codes = mx4_block_codes(v, kq, s);
-      const int row = m0 + r0 + 16 * mb + c16;
+      const int row = m0 + 16 * mb + c16;
       if (p.sorted_ids[row] >= p.n_slots) continue;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (int64_t)row * (N / 4) + tn * 64 + sw * 16 + (kq & 1) * 8 + (kq >> 1) * 4) = codes;
-      if (kq == 0) p.out_scale[((int64_t)tn * p.out_rows + row) * 4 + sw] = (uint8_t)s;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + (int64_t)row * (N / 4) + tn * 64 + wave * 16 + (kq & 1) * 8 + (kq >> 1) * 4) = codes;
+      if (kq == 0) p.out_scale[((int64_t)tn * p.out_rows + row) * 4 + wave] = (uint8_t)s;
     }
   } else {
     const int col = strip * 64;
@@ -174,48 +173,48 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
     int32_t* lid = reinterpret_cast<int32_t*>(lds);
     float* ltw = reinterpret_cast<float*>(lid + C::BM);
     __syncthreads();  // every wave is done with the stage ring
-    load_slots(p, m0, C::BM, lid, ltw, tid, 64 * C::WAVES);
+    load_slots(p, m0, C::BM, lid, ltw, tid, 64 * kWaves);
     __syncthreads();
-    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid + r0, ltw + r0, col, lane, acc);
+    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid, ltw, col, lane, acc);
   }
 #endif
 }
 
-constexpr int mx4_stages(int MB, int H) { return MB <= 4 || H > 1 ? 3 : 2; }
+constexpr int mx4_stages(int MB) { return MB <= 4 ? 3 : 2; }
 
 // An aligned block is run with as many row blocks (a power of two) as hold slots, so that
 // the half-empty blocks that end each expert's segment cost what they hold.
-template <int MB, int H, int Q, int MODE, int AUX>
+template <int MB, int Q, int MODE, int AUX>
 __device__ __forceinline__ void mx4_tile_rows(const Mx4Args& p, uint8_t* lds, int m0, int64_t ex, int tn, int rows) {
   if constexpr (MB > 1) {
-    if (rows <= 8 * MB * H) {
-      mx4_tile_rows<MB / 2, H, Q, MODE, AUX>(p, lds, m0, ex, tn, rows);
+    if (rows <= 8 * MB) {
+      mx4_tile_rows<MB / 2, Q, MODE, AUX>(p, lds, m0, ex, tn, rows);
       return;
     }
   }
-  mx4_tile<MB, H, mx4_stages(MB, H), Q, MODE, AUX>(p, lds, m0, ex, tn);
+  mx4_tile<MB, mx4_stages(MB), Q, MODE, AUX>(p, lds, m0, ex, tn);
 }
 
-template <int MB, int H, int Q, int MODE>
-__global__ void __launch_bounds__(64 * kWaves * H) __attribute__((amdgpu_waves_per_eu(2))) mx4_grouped(Mx4Args p) {
+template <int MB, int Q, int MODE>
+__global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) mx4_grouped(Mx4Args p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int tm, tn;
-  if (!grouped_place(p, 16 * MB * H, tm, tn)) return;
-  const int m0 = tm * 16 * MB * H;
+  if (!grouped_place(p, 16 * MB, tm, tn)) return;
+  const int m0 = tm * 16 * MB;
   const int64_t ex = p.block_expert[tm];
   if (ex < 0 || ex >= p.experts) {
     if constexpr (MODE == MX4_DOWN)
-      zero_slot_rows(p, m0, 16 * MB * H, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 64 * kWaves * H);
+      zero_slot_rows(p, m0, 16 * MB, p.col0 + tn * 256, min(p.col0 + p.ncol, p.col0 + tn * 256 + 256), threadIdx.x, 64 * kWaves);
     return;
   }
-  const int rows = block_rows(p, m0, 16 * MB * H, threadIdx.x & 63);
+  const int rows = block_rows(p, m0, 16 * MB, threadIdx.x & 63);
   // weights that no other block reads go past the caches
-  const bool alone = (tm == 0 || p.block_expert[tm - 1] != ex) && ((tm + 1) * 16 * MB * H >= *p.num_padded || p.block_expert[tm + 1] != ex);
+  const bool alone = (tm == 0 || p.block_expert[tm - 1] != ex) && ((tm + 1) * 16 * MB >= *p.num_padded || p.block_expert[tm + 1] != ex);
   if (alone)
-    mx4_tile_rows<MB, H, Q, MODE, kReadOnce>(p, lds, m0, ex, tn, rows);
+    mx4_tile_rows<MB, Q, MODE, kReadOnce>(p, lds, m0, ex, tn, rows);
   else
-    mx4_tile_rows<MB, H, Q, MODE, 0>(p, lds, m0, ex, tn, rows);
+    mx4_tile_rows<MB, Q, MODE, 0>(p, lds, m0, ex, tn, rows);
 #endif
 }
 
@@ -299,26 +298,26 @@ __global__ void repack_mx4_kernel(const uint8_t* __restrict__ codes, const uint8
   }
 }
 
-template <int MB, int H, int Q, int MODE>
+template <int MB, int Q, int MODE>
 hipError_t launch_tiles(const Mx4Args& a, dim3 grid, hipStream_t s) {
   // the largest ring of the row counts a block may run with
   constexpr int LOW = MB < 4 ? MB : 4;
-  constexpr size_t lds = std::max<size_t>(Mx4Cfg<MB, H, mx4_stages(MB, H), Q>::LDS, Mx4Cfg<LOW, H, mx4_stages(LOW, H), Q>::LDS);
-  const hipError_t e = allow_lds<mx4_grouped<MB, H, Q, MODE>>(lds);
-  return e != hipSuccess ? e : launch_timed(mx4_grouped<MB, H, Q, MODE>, grid, dim3(64 * kWaves * H), lds, s, a);
+  constexpr size_t lds = std::max<size_t>(Mx4Cfg<MB, mx4_stages(MB), Q>::LDS, Mx4Cfg<LOW, mx4_stages(LOW), Q>::LDS);
+  const hipError_t e = allow_lds<mx4_grouped<MB, Q, MODE>>(lds);
+  return e != hipSuccess ? e : launch_timed(mx4_grouped<MB, Q, MODE>, grid, dim3(64 * kWaves), lds, s, a);
 }
 
-template <int MB, int H>
+template <int MB>
 hipError_t launch_block(int mode, const Mx4Args& a, dim3 grid, hipStream_t s) {
-  if (mx4_groups(a.G) == 2) return mode == MX4_DOWN ? launch_tiles<MB, H, 2, MX4_DOWN>(a, grid, s) : launch_tiles<MB, H, 2, MX4_GATE_UP>(a, grid, s);
-  return mode == MX4_DOWN ? launch_tiles<MB, H, 1, MX4_DOWN>(a, grid, s) : launch_tiles<MB, H, 1, MX4_GATE_UP>(a, grid, s);
+  if (mx4_groups(a.G) == 2) return mode == MX4_DOWN ? launch_tiles<MB, 2, MX4_DOWN>(a, grid, s) : launch_tiles<MB, 2, MX4_GATE_UP>(a, grid, s);
+  return mode == MX4_DOWN ? launch_tiles<MB, 1, MX4_DOWN>(a, grid, s) : launch_tiles<MB, 1, MX4_GATE_UP>(a, grid, s);
 }
 
 template <int G>
 hipError_t launch_short(const Mx4Args& a, int bm, dim3 grid, hipStream_t s) {
   if constexpr (G <= kShortGroups) {
     if (a.G != G) return launch_short<G + 1>(a, bm, grid, s);
-    const hipError_t e = allow_lds<mx4_down_short<G>>(short_lds(256, G));
+    const hipError_t e = allow_lds<mx4_down_short<G>>(short_lds(128, G));
     return e != hipSuccess ? e : launch_timed(mx4_down_short<G>, grid, dim3(64 * kWaves), (size_t)short_lds(bm, G), s, a, bm);
   }
   return hipErrorInvalidValue;
@@ -338,18 +337,17 @@ int launch_mx4_grouped(int mode, int bm, const Mx4Args& a, int64_t blocks, void*
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.G < 1 || a.N % (mode == MX4_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
   if (mode == MX4_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
-  if (bm != 16 && bm != 64 && bm != 128 && bm != 256) return (int)hipErrorInvalidValue;
+  if (bm != 16 && bm != 64 && bm != 128) return (int)hipErrorInvalidValue;
   Mx4Args b = a;
   b.tiles_n = (int)((mode == MX4_DOWN ? a.ncol : a.N) + 255) / 256;
   if (blocks * b.tiles_n > INT32_MAX) return (int)hipErrorInvalidValue;
   const dim3 grid((unsigned)(blocks * b.tiles_n));
   if (mode == MX4_DOWN && a.G <= kShortGroups) return (int)launch_short<1>(b, bm, grid, s);
   switch (bm) {
-    case 16: return (int)launch_block<1, 1>(mode, b, grid, s);
-    case 64: return (int)launch_block<4, 1>(mode, b, grid, s);
-    case 128: return (int)launch_block<8, 1>(mode, b, grid, s);
+    case 16: return (int)launch_block<1>(mode, b, grid, s);
+    case 64: return (int)launch_block<4>(mode, b, grid, s);
   }
-  return (int)launch_block<8, 2>(mode, b, grid, s);
+  return (int)launch_block<8>(mode, b, grid, s);
 }
 
 }  // namespace hq
