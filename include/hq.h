@@ -768,8 +768,8 @@ typedef struct hq_jit_stats {
 } hq_jit_stats;
 hq_status hq_jit_get_stats(hq_jit_stats* stats);
 
-/* Kernel timing: the next hq_gemm, hq_moe_align, hq_moe_gemm,
- * hq_quantize_per_token, hq_quantize_mxfp4, hq_stream_read or hq_mfma_peak call on this
+/* Kernel timing: the next hq_gemm, hq_moe_align, hq_moe_gemm, hq_moe_layer_mxfp4, hq_rms_norm,
+ * hq_route_experts, hq_quantize_per_token, hq_quantize_mxfp4, hq_stream_read or hq_mfma_peak call on this
  * thread records `start` (hipEvent_t, created by the caller with timing
  * enabled) when its first kernel starts and `stop` when its last kernel ends
  * (the split-K reduce, the fp8 requant or the combine's final pass included;
