@@ -455,7 +455,7 @@ class Plan:
         self._block8 = self.quant.act_scale == ASCALE_BLOCK_F32
         self._mx4_grouped = kind != "dense" and self.quant.act == FP4_E2M1
         self._ws_need = {}  # rows -> workspace bytes of a block-scaled GEMM
-        self._few_need = {}  # (tokens, topk, down's k) -> workspace bytes of a layer of a few tokens
+        self._few_need = {}  # (tokens, topk, down's k and, for MXFP4, n) -> workspace bytes of a layer
         self._ws = {}
         self._act_buf = {}
 
@@ -1271,11 +1271,11 @@ def _moe_mx4(gate_up, down, x, x_scale, ids, w, w1, m1, w2, m2):
     if not _same_device(dev, x, ids, w, w1, w2) or x_scale is not None and not _same_device(dev, x_scale):
         raise ValueError("the tensors of a w4a4_mxfp4 layer must be contiguous and on x's device")
     gate_up._check_mx4_layout(w1, m1), down._check_mx4_layout(w2, m2)
-    need = gate_up._few_need.get((t, topk, down.k))
+    need = gate_up._few_need.get((t, topk, down.k, down.n))
     if need is None:
         n = ctypes.c_size_t()
         _check(lib().hq_moe_mxfp4_workspace_bytes(gate_up._h, down._h, t, topk, ctypes.byref(n)))
-        need = gate_up._few_need[t, topk, down.k] = n.value
+        need = gate_up._few_need[t, topk, down.k, down.n] = n.value
     ws = x.new_empty(need, dtype=torch.uint8)
     out = x.new_empty((t, down.n), dtype=_TORCH_OUT[down.quant.out])
     _run(dev, lib().hq_moe_layer_mxfp4, gate_up._h, down._h, t, topk, xt, x.data_ptr(), _ptr(x_scale), ids.data_ptr(), w.data_ptr(),

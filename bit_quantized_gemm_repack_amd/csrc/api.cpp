@@ -1872,8 +1872,8 @@ static hq_status mx4_layer_check(const hq_plan* gu, const hq_plan* dn, int64_t t
   if (!hq::mx4_layout(gu) || !hq::mx4_layout(dn)) return fail(HQ_ERR_UNSUPPORTED, "the layer takes grouped MXFP4 x MXFP4 plans");
   if (gu->compute.epi != HQ_EPI_SILU_MUL_QMX4 || dn->compute.epi != HQ_EPI_TOPK_COMBINE)
     return fail(HQ_ERR_INVALID_ARG, "the layer takes a gate_up (SILU_MUL_QMX4) and a down (TOPK_COMBINE) plan");
-  if (gu->layer.num_experts != dn->layer.num_experts || gu->layer.n != 2 * dn->layer.k || gu->layer.k != dn->layer.n)
-    return fail(HQ_ERR_INVALID_ARG, "gate_up must be [2 I, H] and down [H, I] over the same experts");
+  if (gu->layer.num_experts != dn->layer.num_experts || gu->layer.n != 2 * dn->layer.k)
+    return fail(HQ_ERR_INVALID_ARG, "gate_up must be [2 I, H] and down [N, I] over the same experts");
   if (t < 0 || t > gu->max_m || t > dn->max_m) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, max_m]");
   if (topk < 1 || topk > 64) return fail(HQ_ERR_INVALID_ARG, "topk must be 1..64");
   if (gu->layer.num_experts > 4096) return fail(HQ_ERR_UNSUPPORTED, "more than 4096 experts");
@@ -1885,8 +1885,8 @@ static hq_status mx4_layer_check(const hq_plan* gu, const hq_plan* dn, int64_t t
 
 // Whether the two kernels for a few tokens run the layer (a tuned block height asks for the
 // aligned path).
-static bool mx4_layer_few(const hq_plan* gu, int64_t t, int topk) {
-  return !gu->user.tile_m && (int64_t)gu->w_bytes_per_expert < (int64_t(1) << 31) &&
+static bool mx4_layer_few(const hq_plan* gu, const hq_plan* dn, int64_t t, int topk) {
+  return !gu->user.tile_m && gu->layer.k == dn->layer.n && (int64_t)gu->w_bytes_per_expert < (int64_t(1) << 31) &&
          hq::mx4_few_ok(t, topk, gu->layer.num_experts, gu->layer.k, gu->layer.n / 2);
 }
 
@@ -1904,7 +1904,7 @@ static Mx4LayerWs mx4_layer_ws(const hq_plan* gu, const hq_plan* dn, int64_t t, 
     return was;
   };
   const int64_t H = gu->layer.k, I = dn->layer.k;
-  if (mx4_layer_few(gu, t, topk)) {
+  if (mx4_layer_few(gu, dn, t, topk)) {
     w.units = take((size_t)((t + 15) / 16) * hq::kB8FewUnitInts * 4);
     w.act = take(hq::mx4_few_act_bytes(t, topk, I));
   } else {
@@ -1951,7 +1951,7 @@ hq_status hq_moe_layer_mxfp4(const hq_plan* gate_up, const hq_plan* down, int64_
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   const int64_t H = gate_up->layer.k, I = down->layer.k;
   const int E = gate_up->layer.num_experts;
-  if (mx4_layer_few(gate_up, t, topk)) {
+  if (mx4_layer_few(gate_up, down, t, topk)) {
     hq::Mx4FewArgs a{};
     a.x = x;
     a.x_scale = static_cast<const uint32_t*>(x_scale);

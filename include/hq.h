@@ -549,9 +549,9 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
                            void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* A whole experts' layer in MXFP4 (W4A4 plans: gate_up [2 I, H] with SILU_MUL_QMX4, down
- * [H, I] with TOPK_COMBINE, the same experts):
+ * [N, I] with TOPK_COMBINE, the same experts):
  *   y[i] = sum_j topk_w[i, j] q(SiLU(g) * u) W2[e]^T,  (g, u) = halves of q(x[i]) W1[e]^T,
- * e = topk_ids[i, j], q as hq_quantize_mxfp4.  A few tokens run in two kernels, others as
+ * e = topk_ids[i, j], q as hq_quantize_mxfp4.  A few tokens (N = H) run in two kernels, others as
  * hq_quantize_mxfp4, hq_moe_align and the two GEMMs do, with the same roundings but for a
  * slot's row of down, which only they round (to fp16 with a scale by 64 columns).
  *   x         device [t, H] fp16 / bf16, or E2M1 codes [t, H/2] (x_type HQ_FP4_E2M1)
@@ -560,7 +560,7 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
  *   topk_ids, topk_w  device [t, topk]: ids outside [0, num_experts) contribute zero, an id
  *             may come twice in a row
  *   w1, w2    as hq_plan_repack wrote them (their metadata is empty)
- *   out       device [t, H] in the down plan's out dtype
+ *   out       device [t, N] in the down plan's out dtype
  *   ws        hq_moe_mxfp4_workspace_bytes bytes, no initialisation needed; two calls
  *             that overlap in time must not share one
  * topk_ids and topk_w are aligned to their elements, the others to 16 bytes.

@@ -177,7 +177,7 @@ def test_layer(t, e, topk, h, i, dt):
 
 @pytest.mark.parametrize("t,e,topk,h,i", [(1, 20, 16, 2048, 640), (1, 8, 1, 2048, 128), (2, 8, 8, 2176, 384), (4, 8, 8, 4096, 256), (5, 12, 8, 4096, 128),
                                           (9, 256, 8, 7168, 256), (16, 3, 2, 7168, 384), (17, 3, 1, 7168, 128), (33, 40, 2, 7168, 512), (64, 5, 1, 7168, 256),
-                                          (15, 1, 4, 7168, 128), (2, 8, 1, 2048, 7168)])
+                                          (15, 1, 4, 7168, 128), (2, 8, 1, 2048, 7168), (2, 2, 8, 2048, 7168), (4, 2, 2, 24576, 128)])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_layer_of_few_tokens(t, e, topk, h, i, dt):
     """The two kernels: slots without an expert, an expert twice in a row, NaN rows, one expert for many."""
@@ -203,6 +203,44 @@ def test_layer_of_few_tokens(t, e, topk, h, i, dt):
     y = L.run(x, one, w)
     torch.cuda.synchronize()
     L.check(y, x, one, w, "one expert")
+
+
+@pytest.mark.parametrize("t,h", [(2, 2176), (5, 4096)])
+def test_nan_weights_of_few_tokens(t, h):
+    """A NaN column of one expert's gate_up, and one of its down: tokens elsewhere keep their bits."""
+    e, i = 6, 128
+    L = Layer(4, e, h, i, t)
+    x = _x(L.g, t, h, torch.bfloat16)
+    ids = torch.tensor([[4, 1], [0, 2], [3, 4], [5, 0], [1, 2]], dtype=torch.int32, device=DEV)[:t].contiguous()
+    w = torch.rand(t, 2, generator=L.g, device=DEV) + 0.1
+    y = L.run(x, ids, w)
+    hit = (ids == 4).any(-1)
+    e1, e2 = L.e1.clone(), L.e2.clone()
+    e1[4, 0, 0], e2[4, 7, 1] = 255, 255
+    z = hq.moe_layer(L.gu, L.dn, x, ids, w, *L.gu.repack(L.w1, e8m0=e1), *L.wm[2:])
+    u = hq.moe_layer(L.gu, L.dn, x, ids, w, *L.wm[:2], *L.dn.repack(L.w2, e8m0=e2))
+    torch.cuda.synchronize()
+    assert z[hit].isnan().all() and torch.equal(z[~hit], y[~hit])
+    assert u[hit][:, 7].isnan().all() and torch.equal(u[~hit], y[~hit])
+    u[:, 7], y[:, 7] = 0, 0
+    assert torch.equal(u, y)
+
+
+@pytest.mark.parametrize("t", [1, 3, 70])
+def test_layer_to_another_width(t):
+    """down's n need not be gate_up's k."""
+    e, h, i, n, topk = 6, 2048, 256, 640, 3
+    L = Layer(8, e, h, i, t)
+    w2, e2 = _quant(torch.randn(e, n, i, generator=L.g, device=DEV) / i ** 0.5)
+    dn = hq.MoePlan(n, i, hq.w4a4_mxfp4("bf16"), e, t, "topk_combine")
+    x = _x(L.g, t, h, torch.bfloat16)
+    ids, w = _routing(L.g, t, e, topk)
+    y0 = L.run(x, ids, w)
+    y = hq.moe_layer(L.gu, dn, x, ids, w, *L.wm[:2], *dn.repack(w2, e8m0=e2))
+    torch.cuda.synchronize()
+    want, tol = om.layer(om.rows(*om.quantize(x.double())), ids, w, L.w1, L.e1, w2, e2)
+    assert y.shape == (t, n) and y0.shape == (t, h)
+    _check(y, want, tol + om.half_step(want.abs() + tol, torch.bfloat16) + 1e-30, "to 640")
 
 
 def test_layer_windows():
