@@ -121,6 +121,47 @@ def test_layer_plans_belong_together():
         hq.moe_layer(gu, dn, x, ids, w, x, x, x, x, by_slot=True)
 
 
+LAYER = dict(t=2, topk=2, type=hq.BF16, x=4096, xs=None, ids=8192, w=12288, w1=16384, w2=20480, out=24576, ws=28672, ws_bytes=1 << 20)
+
+
+def _layer(gu, dn, **kw):
+    a = dict(LAYER, **kw)
+    return hq.lib().hq_moe_layer_mxfp4(gu._h if gu else None, dn._h if dn else None, a["t"], a["topk"], a["type"], a["x"], a["xs"], a["ids"], a["w"],
+                                       a["w1"], a["w2"], a["out"], a["ws"], a["ws_bytes"], None)
+
+
+def test_layer_refusals():
+    """Every refusal of hq_moe_layer_mxfp4 comes before a launch."""
+    import ctypes
+    gu, dn = hq.MoePlan(512, 2048, Q, 4, 64, "silu_mul_qmxfp4"), hq.MoePlan(2048, 256, Q, 4, 64, "topk_combine")
+    n = ctypes.c_size_t()
+    need = {}
+    for t, topk in ((0, 2), (1, 2), (2, 2), (40, 2), (64, 64)):
+        assert hq.lib().hq_moe_mxfp4_workspace_bytes(gu._h, dn._h, t, topk, ctypes.byref(n)) == hq.HQ_OK
+        need[t] = n.value
+    assert need[0] == 0 < need[1] <= need[2] < need[40] < need[64]
+    assert _layer(gu, dn, t=0, x=None, ws=None, ws_bytes=0) == hq.HQ_OK
+    arg, un, ws = hq.HQ_ERR_INVALID_ARG, hq.HQ_ERR_UNSUPPORTED, hq.HQ_ERR_WORKSPACE
+    for kw, want in ((dict(t=65), arg), (dict(t=-1), arg), (dict(topk=0), arg), (dict(topk=65), arg), (dict(type=hq.F32), un), (dict(type=hq.FP8_E4M3), un),
+                     (dict(type=hq.FP4_E2M1), arg), (dict(xs=4096), arg), (dict(x=None), arg), (dict(ids=None), arg), (dict(w=None), arg),
+                     (dict(w1=None), arg), (dict(w2=None), arg), (dict(out=None), arg), (dict(x=4104), arg), (dict(type=hq.FP4_E2M1, xs=4100), arg),
+                     (dict(w1=16392), arg), (dict(w2=20488), arg), (dict(out=24584), arg), (dict(ids=8193), arg), (dict(w=12290), arg),
+                     (dict(ws=None), ws), (dict(ws_bytes=need[2] - 1), ws), (dict(t=40, ws_bytes=need[40] - 1), ws), (dict(ws=28680), arg)):
+        assert _layer(gu, dn, **kw) == want, kw
+        assert hq.lib().hq_last_error()
+    assert _layer(None, dn) == arg and _layer(gu, None) == arg and _layer(dn, gu) == arg and _layer(gu, gu) == arg
+    assert hq.lib().hq_moe_mxfp4_workspace_bytes(gu._h, dn._h, 1, 2, None) == arg
+    assert _layer(gu, hq.MoePlan(2048, 256, Q, 5, 64, "topk_combine")) == arg
+    assert _layer(gu, hq.MoePlan(2048, 128, Q, 4, 64, "topk_combine")) == arg
+    assert _layer(gu, hq.MoePlan(2048, 256, Q, 4, 64, "topk_combine", tuning=dict(tile_m=128))) == arg      # another block height
+    assert _layer(gu, hq.MoePlan(2048, 256, Q, 4, 1, "topk_combine")) == arg
+    assert _layer(gu, hq.MoePlan(2048, 256, hq.w8a8_block(), 4, 64, "topk_combine")) == un
+    big = [hq.MoePlan(n, k, Q, 4, 1 << 20, epi) for n, k, epi in ((512, 2048, "silu_mul_qmxfp4"), (2048, 256, "topk_combine"))]
+    assert _layer(*big, t=1 << 20) == un
+    many = [hq.MoePlan(n, k, Q, 4097, 64, epi) for n, k, epi in ((512, 128, "silu_mul_qmxfp4"), (128, 256, "topk_combine"))]
+    assert _layer(*many) == un
+
+
 def test_host_repack_checks_shapes():
     gu = hq.MoePlan(512, 256, Q, 2, 64, "silu_mul_qmxfp4")
     codes, e = torch.zeros(2, 512, 128, dtype=torch.uint8), torch.full((2, 512, 8), 127, dtype=torch.uint8)
