@@ -303,9 +303,9 @@ def _bind_calls(L):
         native = importlib.import_module("._calls", __package__)
         if native.built_for != torch.__version__:
             raise ImportError(f"built for torch {native.built_for}, this is {torch.__version__}")
-        native.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes, L.hq_rms_norm,
-                                L.hq_route_experts)))
+        for bind, fns in ((native.bind, (L.hq_quantize_blocks, L.hq_route_topk, L.hq_gemm, L.hq_plan_workspace_bytes)),
+                          (native.bind_norm_route, (L.hq_rms_norm, L.hq_route_experts))):
+            bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
     except Exception as e:  # a damaged file, another torch's: every call works without it
         warnings.warn(f"{CALLS_PATH} is not used ({e}): short calls go through ctypes; build again to have it", RuntimeWarning)
         return

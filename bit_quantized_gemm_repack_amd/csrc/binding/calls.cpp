@@ -237,18 +237,28 @@ PyObject* gemm_block(PyObject*, PyObject* const* v, Py_ssize_t count) {
   });
 }
 
-// bind(addresses of hq_quantize_blocks, hq_route_topk, hq_gemm, hq_plan_workspace_bytes, hq_rms_norm, hq_route_experts)
+// bind(addresses of hq_quantize_blocks, hq_route_topk, hq_gemm, hq_plan_workspace_bytes)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
     return nullptr;
   }
   quantize_fn = reinterpret_cast<decltype(quantize_fn)>(PyLong_AsVoidPtr(a[0]));
   route_fn = reinterpret_cast<decltype(route_fn)>(PyLong_AsVoidPtr(a[1]));
   gemm_fn = reinterpret_cast<decltype(gemm_fn)>(PyLong_AsVoidPtr(a[2]));
   workspace_fn = reinterpret_cast<decltype(workspace_fn)>(PyLong_AsVoidPtr(a[3]));
-  norm_fn = reinterpret_cast<decltype(norm_fn)>(PyLong_AsVoidPtr(a[4]));
-  route_experts_fn = reinterpret_cast<decltype(route_experts_fn)>(PyLong_AsVoidPtr(a[5]));
+  if (PyErr_Occurred()) return nullptr;
+  Py_RETURN_NONE;
+}
+
+// bind_norm_route(addresses of hq_rms_norm, hq_route_experts)
+PyObject* bind_norm_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 2) {
+    PyErr_SetString(PyExc_TypeError, "bind_norm_route takes two addresses");
+    return nullptr;
+  }
+  norm_fn = reinterpret_cast<decltype(norm_fn)>(PyLong_AsVoidPtr(a[0]));
+  route_experts_fn = reinterpret_cast<decltype(route_experts_fn)>(PyLong_AsVoidPtr(a[1]));
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -257,6 +267,7 @@ PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
+                         {"bind_norm_route", fast(bind_norm_route), METH_FASTCALL, nullptr},
                          {"quantize_blocks", fast(quantize_blocks), METH_FASTCALL, nullptr},
                          {"route_topk", fast(route_topk), METH_FASTCALL, nullptr},
                          {"rms_norm", fast(rms_norm), METH_FASTCALL, nullptr},
