@@ -226,6 +226,19 @@ def test_nan_weights_of_few_tokens(t, h):
     assert torch.equal(u, y)
 
 
+@pytest.mark.parametrize("t,topk", [(40, 4), (3, 64), (900, 2)])
+def test_layer_of_most_experts(t, topk):
+    """4096 experts, the most; 64 slots a token, the most."""
+    print(f"[gpu case] 4096 experts {t} {topk}", flush=True)
+    L = Layer(t, 4096, 128, 128, t)
+    x = _x(L.g, t, 128, torch.bfloat16)
+    ids, w = _routing(L.g, t, 4096, topk)
+    ids[0, 0], ids[1, :2] = 4095, 7
+    y = L.run(x, ids, w)
+    torch.cuda.synchronize()
+    L.check(y, x, ids, w, "4096 experts")
+
+
 @pytest.mark.parametrize("t", [1, 3, 70])
 def test_layer_to_another_width(t):
     """down's n need not be gate_up's k."""
