@@ -1880,6 +1880,11 @@ static hq_status mx4_layer_check(const hq_plan* gu, const hq_plan* dn, int64_t t
   if (t * topk > (int64_t(1) << 20)) return fail(HQ_ERR_UNSUPPORTED, "t * topk above 2^20");
   if (moe_choice(gu, t, topk).bm != moe_choice(dn, t, topk).bm)
     return fail(HQ_ERR_INVALID_ARG, "the plans' tunings fix different block heights");
+  // what the two products would refuse, before the first launch
+  const int64_t mp = moe_max_padded(t, topk, gu->layer.num_experts, moe_choice(gu, t, topk).bm), most = int64_t(1) << 31;
+  if (t * gu->layer.k / 2 >= most || mp * dn->layer.k / 2 >= most || (int64_t)gu->w_bytes_per_expert >= most || (int64_t)dn->w_bytes_per_expert >= most)
+    return fail(HQ_ERR_UNSUPPORTED, "activations and one expert's weights must each stay below 2 GiB");
+  if (t * topk * block_window(dn, t, topk) * 2 >= (int64_t)hq::kSlotRowsMost) return fail(HQ_ERR_UNSUPPORTED, "the slots' rows must stay below 4 GiB");
   return HQ_OK;
 }
 

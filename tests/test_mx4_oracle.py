@@ -158,6 +158,10 @@ def test_layer_refusals():
     assert _layer(gu, hq.MoePlan(2048, 256, hq.w8a8_block(), 4, 64, "topk_combine")) == un
     big = [hq.MoePlan(n, k, Q, 4, 1 << 20, epi) for n, k, epi in ((512, 2048, "silu_mul_qmxfp4"), (2048, 256, "topk_combine"))]
     assert _layer(*big, t=1 << 20) == un
+    for h, i, t in ((65536, 32768, 2), (65536, 128, 70000), (128, 65536, 40000)):      # an expert, x, the intermediate of 2 GiB
+        big = [hq.MoePlan(n, k, Q, 1, 1 << 17, epi) for n, k, epi in ((2 * i, h, "silu_mul_qmxfp4"), (h, i, "topk_combine"))]
+        assert hq.lib().hq_moe_mxfp4_workspace_bytes(*(p._h for p in big), t, 2, ctypes.byref(n)) == un
+        assert _layer(*big, t=t, ws_bytes=1 << 50) == un
     many = [hq.MoePlan(n, k, Q, 4097, 64, epi) for n, k, epi in ((512, 128, "silu_mul_qmxfp4"), (128, 256, "topk_combine"))]
     assert _layer(*many) == un
 
