@@ -15,6 +15,9 @@ namespace hq {
 template <typename Kern, typename... Args>
 inline hipError_t launch_timed(Kern kern, dim3 grid, dim3 block, size_t lds, hipStream_t s, Args... args) {
   const TimingEvents ev = take_timing();
+  // a dispatch counts its work-items in 32 bits a dimension: a longer one would run in part
+  if ((uint64_t)grid.x * block.x > UINT32_MAX || (uint64_t)grid.y * block.y > UINT32_MAX || (uint64_t)grid.z * block.z > UINT32_MAX)
+    return hipErrorInvalidConfiguration;
   if (ev.start || ev.stop)
     hipExtLaunchKernelGGL(kern, grid, block, (uint32_t)lds, s, static_cast<hipEvent_t>(ev.start),
                           static_cast<hipEvent_t>(ev.stop), 0, args...);
@@ -22,6 +25,15 @@ inline hipError_t launch_timed(Kern kern, dim3 grid, dim3 block, size_t lds, hip
     hipLaunchKernelGGL(kern, grid, block, lds, s, args...);
   return hipGetLastError();
 }
+
+// The workgroups of a long input, whose work-items are more than a dimension of a dispatch
+// counts: runs of kGridRun (of up to 1024 threads) along x, the runs along y.  The kernel takes
+// grid_block() for its number and leaves at once past the last one.
+constexpr unsigned kGridRun = 1u << 20;
+inline dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridRun ? dim3((unsigned)blocks) : dim3(kGridRun, (unsigned)((blocks + kGridRun - 1) / kGridRun));
+}
+__device__ inline uint32_t grid_block() { return blockIdx.y * kGridRun + blockIdx.x; }
 
 // Raises a kernel's dynamic LDS limit to `bytes` on the current device, once
 // per kernel and device (from any thread; setting it twice is harmless).

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const u4_t* __restr
 template <bool BF16>
 __global__ void __launch_bounds__(256) quantize_mx_kernel(const u4_t* __restrict__ x, uint32_t m, uint32_t k8,
                                                           uint32_t* __restrict__ codes, uint32_t* __restrict__ e8m0) {
-  const uint32_t G = k8 / 16, quads = (G + 3) / 4, rq = blockIdx.x / quads;
-  const uint32_t g = (blockIdx.x - rq * quads) * 4 + (threadIdx.x >> 6), row = rq * 4 + ((threadIdx.x >> 4) & 3);
+  const uint32_t G = k8 / 16, quads = (G + 3) / 4, block = grid_block(), rq = block / quads;
+  const uint32_t g = (block - rq * quads) * 4 + (threadIdx.x >> 6), row = rq * 4 + ((threadIdx.x >> 4) & 3);
   if (g >= G || row >= m) return;
   const int64_t at = (int64_t)row * k8 + g * 16 + (threadIdx.x & 15);
   const u4_t raw = x[at];
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) quantize_mx_kernel(const u4_t* __restrict
 }  // namespace
 
 int launch_quantize_mx(int64_t m, int64_t k, int in_bf16, const void* x, void* codes, uint8_t* e8m0, void* stream) {
-  const dim3 grid((unsigned)((k / 128 + 3) / 4 * ((m + 3) / 4))), block(256);
+  const dim3 grid = grid_of((k / 128 + 3) / 4 * ((m + 3) / 4)), block(256);
   const auto xs = static_cast<const u4_t*>(x);
   const auto cs = static_cast<uint32_t*>(codes);
   const auto es = reinterpret_cast<uint32_t*>(e8m0);

@@ -1,0 +1,49 @@
+"""Row-wise operators on inputs whose launch has more work-items than one of its dimensions
+holds (2^32): rows from the whole input against the same rows by themselves."""
+import pytest
+import torch
+
+import bit_quantized_gemm_repack_amd as hq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _room(gib):
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    if free < gib * 2 ** 30:
+        pytest.skip(f"needs {gib} GiB of device memory, {free / 2 ** 30:.0f} are free")
+
+
+def _parts(m, n):
+    """Where to look: the start, the end, and either side of every power of two of rows, n rows each."""
+    at = {0, m - n} | {min(max(0, 2 ** i - n // 2), m - n) for i in range(10, m.bit_length())}
+    return sorted(at)
+
+
+def _long_rows(m, k, dt, seed):
+    """[m, k] contiguous, rows unlike each other, made in pieces."""
+    g = torch.Generator(DEV)
+    g.manual_seed(seed)
+    base = torch.randn(1 << 20, generator=g, device=DEV).to(dt)
+    x = torch.empty(m * k, dtype=dt, device=DEV)
+    for i in range(0, m * k, 1 << 20):
+        n = min(1 << 20, m * k - i)
+        torch.mul(base[:n], 2.0 ** (i // (1 << 20) % 13 - 6), out=x[i:i + n])
+    return x.view(m, k)
+
+
+@pytest.mark.parametrize("m,k", [((1 << 24) - 3, 2176), ((1 << 17) + 5, 1 << 18)])
+def test_quantize_mxfp4(m, k):
+    """2^35 values and more; 2^36 are allowed."""
+    print(f"[gpu case] quantize_mxfp4 {m} x {k}", flush=True)
+    _room(100)
+    x = _long_rows(m, k, torch.bfloat16, 1)
+    codes, e = hq.quantize_mxfp4(x)
+    torch.cuda.synchronize()
+    for r in _parts(m, 8):
+        c1, e1 = hq.quantize_mxfp4(x[r:r + 8].clone())
+        assert torch.equal(codes[r:r + 8], c1) and torch.equal(e[:, r:r + 8], e1), f"rows from {r}"
+    del x, codes, e
+    torch.cuda.empty_cache()
