@@ -6,6 +6,7 @@
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "hq_internal.h"
@@ -34,6 +35,21 @@ inline dim3 grid_of(int64_t blocks) {
   return blocks <= kGridRun ? dim3((unsigned)blocks) : dim3(kGridRun, (unsigned)((blocks + kGridRun - 1) / kGridRun));
 }
 __device__ inline uint32_t grid_block() { return blockIdx.y * kGridRun + blockIdx.x; }
+
+// `rows` of `threads` work-items each in as few launches as hold them, go(first, count) being
+// one: for kernels whose grid is their rows, without a check in them.
+template <typename Go>
+inline hipError_t launch_rows(int64_t rows, int threads, Go&& go) {
+  const int64_t most = UINT32_MAX / threads;
+  const TimingEvents ev = take_timing();
+  hipError_t e = hipSuccess;
+  for (int64_t r = 0; r < rows && e == hipSuccess; r += most) {
+    const int64_t n = std::min(most, rows - r);
+    arm_timing({r ? nullptr : ev.start, r + n < rows ? nullptr : ev.stop});
+    e = go(r, n);
+  }
+  return e;
+}
 
 // Raises a kernel's dynamic LDS limit to `bytes` on the current device, once
 // per kernel and device (from any thread; setting it twice is harmless).

@@ -199,11 +199,30 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_kernel(NormArgs p)
 #endif
 }
 
+// The rows from `first` on; m stays the whole's, as the scales' layout goes by it.
+template <int OUT>
+NormArgs rows_from(NormArgs a, int64_t first) {
+  constexpr int64_t CHUNK = OUT == NORM_16 ? 16 : (OUT == NORM_MXFP4 ? 4 : 8);  // bytes of 8 outputs
+  a.x = static_cast<const u4_t*>(a.x) + first * a.x_stride;
+  if (a.residual) {
+    a.residual = static_cast<const u4_t*>(a.residual) + first * a.r_stride;
+    a.h = static_cast<u4_t*>(a.h) + first * a.h_stride;
+  }
+  a.out = static_cast<char*>(a.out) + first * a.k8 * CHUNK;
+  if (OUT != NORM_16) a.scale = static_cast<float*>(a.scale) + first;
+  return a;
+}
+
 template <bool BF16, int OUT>
 int launch_out(const NormArgs& a, hipStream_t s) {
   auto go = [&]<int T, int C>() -> int {
     constexpr int ROWS = T < 256 ? 256 / T : 1;
-    return (int)launch_timed(rms_norm_kernel<BF16, OUT, T, C>, dim3((unsigned)((a.m + ROWS - 1) / ROWS)), dim3(T < 256 ? 256 : T), 0, s, a);
+    if constexpr (ROWS > 1)  // (at most 2^30 work-items)
+      return (int)launch_timed(rms_norm_kernel<BF16, OUT, T, C>, dim3((unsigned)((a.m + ROWS - 1) / ROWS)), dim3(256), 0, s, a);
+    else
+      return (int)launch_rows(a.m, T, [&](int64_t first, int64_t rows) {
+        return launch_timed(rms_norm_kernel<BF16, OUT, T, C>, dim3((unsigned)rows), dim3(T), 0, s, rows_from<OUT>(a, first));
+      });
   };
   // The shape that leaves the fewest threads idle, with the more threads the fewer
   // rows there are (us, bf16 with residual, to 16 bits / e4m3 by row / MXFP4):

@@ -659,7 +659,7 @@ hq_status hq_quantize_mxfp4(int64_t m, int64_t k, hq_dtype in, const void* x, vo
  * zeros or NaN.
  * k must be a multiple of 8 (128 for _FP8_BLOCK and _MXFP4) up to 65536, the
  * strides multiples of 8, the pointers 16-byte aligned, m at most 2^24, eps at least 0;
- * m = 0 is a no-op.  Honours hq_time_next_launch (one kernel). */
+ * m = 0 is a no-op.  Honours hq_time_next_launch (one kernel; more from 2^22 rows on). */
 typedef enum hq_norm_kind {
   HQ_NORM_SAME = 0,
   HQ_NORM_FP8 = 1,

@@ -47,3 +47,28 @@ def test_quantize_mxfp4(m, k):
         assert torch.equal(codes[r:r + 8], c1) and torch.equal(e[:, r:r + 8], e1), f"rows from {r}"
     del x, codes, e
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m,k,kind", [(1 << 24, 1152, "mxfp4"), ((1 << 23) + 1, 4224, "mxfp4"), ((1 << 22) + 3, 8320, "fp8_block"), ((1 << 22) + 1, 8200, "int8"),
+                                      ((1 << 22) + 1, 16392, "fp8"), ((1 << 23) + 7, 4104, None)])
+def test_rms_norm(m, k, kind):
+    """Workgroups of 256, 512 and 1024 threads a row; the rows overlap in memory, eight elements apart.  In 16
+    bits with a residual of one row for all."""
+    print(f"[gpu case] rms_norm {m} x {k} {kind}", flush=True)
+    _room(150)
+    g = torch.Generator(DEV)
+    g.manual_seed(2)
+    base = torch.randn(8 * m + k, generator=g, device=DEV).bfloat16()
+    x = base.as_strided((m, k), (8, 1))
+    w = (1 + 0.1 * torch.randn(k, generator=g, device=DEV)).bfloat16()
+    residual = None if kind else x.new_ones(k).expand(m, k)
+    out = hq.rms_norm(x, w, out=kind, residual=residual)
+    torch.cuda.synchronize()
+    n = 300  # (few rows may be summed by other threads than many)
+    for r in _parts(m, n):
+        part = hq.rms_norm(x[r:r + n], w, out=kind, residual=None if kind else residual[r:r + n])
+        for whole, one in zip(out, part):
+            rows = whole[:, r:r + n] if kind in ("mxfp4", "fp8_block") and whole is out[1] else whole[r:r + n]
+            assert torch.equal(rows, one), f"rows from {r}"
+    del x, base, out, part, whole, one, rows
+    torch.cuda.empty_cache()
