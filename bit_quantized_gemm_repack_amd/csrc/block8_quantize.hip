@@ -29,8 +29,8 @@ template <bool BF16, bool SILU>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const u4_t* __restrict__ x, uint32_t m, uint32_t k8,
                                                               uint2* __restrict__ codes, float* __restrict__ scales) {
   // a workgroup takes 4 rows by 4 block columns, a wave 4 rows of one column
-  const uint32_t G = k8 / 16, quads = (G + 3) / 4, rq = blockIdx.x / quads;
-  const uint32_t g = (blockIdx.x - rq * quads) * 4 + (threadIdx.x >> 6), row = rq * 4 + ((threadIdx.x >> 4) & 3);
+  const uint32_t G = k8 / 16, quads = (G + 3) / 4, block = grid_block(), rq = block / quads;
+  const uint32_t g = (block - rq * quads) * 4 + (threadIdx.x >> 6), row = rq * 4 + ((threadIdx.x >> 4) & 3);
   if (g >= G || row >= m) return;
   const uint32_t c = g * 16 + (threadIdx.x & 15);
   float v[8];
@@ -75,7 +75,7 @@ int launch_quantize_blocks(int64_t m, int64_t k, int in_bf16, int silu, const vo
                            void* stream) {
   const int64_t blocks = m * (k / 128);
   if (blocks < 1 || blocks > INT32_MAX - 16) return (int)hipErrorInvalidValue;
-  const dim3 grid((unsigned)((k / 128 + 3) / 4 * ((m + 3) / 4))), block(256);
+  const dim3 grid = grid_of((k / 128 + 3) / 4 * ((m + 3) / 4)), block(256);
   const auto xs = static_cast<const u4_t*>(x);
   const auto cs = static_cast<uint2*>(codes);
   const hipStream_t s = static_cast<hipStream_t>(stream);

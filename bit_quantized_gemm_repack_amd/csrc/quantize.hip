@@ -180,12 +180,17 @@ int launch_quantize_rows(int64_t m, int64_t k, int in_bf16, int out_fp8, const v
   const auto xs = static_cast<const u4_t*>(x);
   const auto cs = static_cast<uint2*>(codes);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)m), block((unsigned)threads);
-  if (in_bf16)
-    return out_fp8 ? (int)launch_timed(quantize_rows_kernel<true, true>, grid, block, 0, s, xs, k8, cs, scales)
-                   : (int)launch_timed(quantize_rows_kernel<true, false>, grid, block, 0, s, xs, k8, cs, scales);
-  return out_fp8 ? (int)launch_timed(quantize_rows_kernel<false, true>, grid, block, 0, s, xs, k8, cs, scales)
-                 : (int)launch_timed(quantize_rows_kernel<false, false>, grid, block, 0, s, xs, k8, cs, scales);
+  return (int)launch_rows(m, threads, [&](int64_t first, int64_t rows) {
+    const dim3 grid((unsigned)rows), block((unsigned)threads);
+    const u4_t* xr = xs + first * k8;
+    uint2* cr = cs + first * k8;
+    float* sr = scales + first;
+    if (in_bf16)
+      return out_fp8 ? launch_timed(quantize_rows_kernel<true, true>, grid, block, 0, s, xr, k8, cr, sr)
+                     : launch_timed(quantize_rows_kernel<true, false>, grid, block, 0, s, xr, k8, cr, sr);
+    return out_fp8 ? launch_timed(quantize_rows_kernel<false, true>, grid, block, 0, s, xr, k8, cr, sr)
+                   : launch_timed(quantize_rows_kernel<false, false>, grid, block, 0, s, xr, k8, cr, sr);
+  });
 }
 
 }  // namespace hq

@@ -72,3 +72,19 @@ def test_rms_norm(m, k, kind):
             assert torch.equal(rows, one), f"rows from {r}"
     del x, base, out, part, whole, one, rows
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("way,m,k", [("int8", 1 << 24, 1544), ("blocks", (1 << 24) - 3, 2176), ("blocks", (1 << 17) + 5, 1 << 18)])
+def test_other_quantisers(way, m, k):
+    print(f"[gpu case] quantize {way} {m} x {k}", flush=True)
+    _room(130)
+    f = (lambda v: hq.quantize_per_token(v, out="int8")) if way == "int8" else hq.quantize_blocks
+    x = _long_rows(m, k, torch.float16, 3)
+    codes, scale = f(x)
+    torch.cuda.synchronize()
+    for r in _parts(m, 260):
+        c1, s1 = f(x[r:r + 260].clone())
+        s = scale[r:r + 260] if scale.dim() == 1 else scale[:, r:r + 260]
+        assert torch.equal(codes[r:r + 260], c1) and torch.equal(s, s1), f"rows from {r}"
+    del x, codes, scale
+    torch.cuda.empty_cache()
