@@ -720,7 +720,7 @@ hq_status hq_repacked_bytes(const hq_plan* p, size_t* w_bytes, size_t* meta_byte
 
 static hq_status check_repack_args(const hq_plan* p, const void* codes, const void* scales, const void* zx,
                                    const void* w_out, const void* meta_out) {
-  if (!p || !codes || !w_out || !meta_out) return fail(HQ_ERR_INVALID_ARG, "null argument");
+  if (!p || !codes || !w_out || (!meta_out && p->meta_bytes_per_expert)) return fail(HQ_ERR_INVALID_ARG, "null argument");
   if (p->fmt == hq::FMT_B8) {
     if (!scales) return fail(HQ_ERR_INVALID_ARG, "fp8 repack needs the fp32 block scales");
   } else if (hq::nvfp4_weights(p->fmt)) {
@@ -1270,7 +1270,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
     if (t < 0 || t > p->max_m) return fail(HQ_ERR_INVALID_ARG, "t out of range [0, max_m]");
     if (topk < 1 || topk > 64) return fail(HQ_ERR_INVALID_ARG, "topk must be 1..64");
     if (t == 0) return ok();
-    if (!a || !sorted_ids || !block_expert || !num_padded || !w || !meta || !out)
+    if (!a || !sorted_ids || !block_expert || !num_padded || !w || (!meta && p->meta_bytes_per_expert) || !out)
       return fail(HQ_ERR_INVALID_ARG, "null device pointer");
     if (!aligned16(a) || !aligned16(w) || !aligned16(meta) || !aligned16(out))
       return fail(HQ_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
@@ -2010,11 +2010,10 @@ hq_status hq_moe_layer_mxfp4(const hq_plan* gate_up, const hq_plan* down, int64_
   const int err = hq::launch_mx4_prepare(a, stream);
   hq::arm_timing({nullptr, nullptr});
   if (err != hipSuccess) return fail(HQ_ERR_HIP, "layer launch: %s", hipGetErrorString((hipError_t)err));
-  // (the metadata of these plans is empty; their GEMMs ask for a pointer all the same)
-  st = hq_moe_gemm(gate_up, t, topk, x, x_scale, sorted, blocks, padded, nullptr, w1, w1, wsb + w.act, wsb + w.act_scale, nullptr, 0, stream);
+  st = hq_moe_gemm(gate_up, t, topk, x, x_scale, sorted, blocks, padded, nullptr, w1, nullptr, wsb + w.act, wsb + w.act_scale, nullptr, 0, stream);
   if (st != HQ_OK) return st;
   hq::arm_timing({nullptr, ev.stop});
-  return hq_moe_gemm(down, t, topk, wsb + w.act, wsb + w.act_scale, sorted, blocks, padded, topk_w, w2, w2, out, nullptr, wsb + w.gemm,
+  return hq_moe_gemm(down, t, topk, wsb + w.act, wsb + w.act_scale, sorted, blocks, padded, topk_w, w2, nullptr, out, nullptr, wsb + w.gemm,
                      w.total - w.gemm, stream);
 }
 

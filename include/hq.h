@@ -289,8 +289,8 @@ hq_status hq_repacked_bytes(const hq_plan* plan, size_t* w_bytes, size_t* meta_b
  * pointers; the work is a kernel on `stream`.  `zeros_or_e8m0` is NULL for
  * HQ_ZP_FIXED.  The output is a private layout: only hq_gemm / hq_moe_gemm
  * of a plan with the same layer description and activation type read it (W4A4: and of
- * the same GEMM kind and epilogue; its grouped plans keep the scales among the codes
- * and meta_bytes is 0). */
+ * the same GEMM kind and epilogue; its grouped plans keep the scales among the codes,
+ * meta_bytes is 0, and meta may be NULL here, for hq_repack_host and for hq_moe_gemm). */
 hq_status hq_repack(const hq_plan* plan, const void* codes, const void* scales,
                     const void* zeros_or_e8m0, void* w_out, void* meta_out, void* stream);
 /* The same permutation on host memory (for preparing weights offline on a
@@ -559,7 +559,7 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
  *             write them; NULL for 16 bits
  *   topk_ids, topk_w  device [t, topk]: ids outside [0, num_experts) contribute zero, an id
  *             may come twice in a row
- *   w1, w2    as hq_plan_repack wrote them (their metadata is empty)
+ *   w1, w2    as hq_repack wrote them (their metadata is empty)
  *   out       device [t, N] in the down plan's out dtype
  *   ws        hq_moe_mxfp4_workspace_bytes bytes, no initialisation needed; two calls
  *             that overlap in time must not share one
