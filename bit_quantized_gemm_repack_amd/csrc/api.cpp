@@ -1223,12 +1223,16 @@ static int64_t moe_down_cols(const hq_plan* p, int64_t t, int topk, int bm) {
 // Columns of a down launch of fp8 block and MXFP4 layers: windows whose slot rows fit the
 // last-level cache, so that the sum reads them from there and the workspace
 // stays small (4096 tokens, top 8, H = 7168: windows of 60 / 120 / 160 / 240 MiB
-// 424 / 355 / 328 / 311 us, one of 448 309).
+// 424 / 355 / 328 / 311 us, one of 448 309), and stay below what the kernels address with 32
+// bits: from 2^23 slots on that is less than a tile's 256 columns.
 static constexpr int64_t kBlockWindowBytes = int64_t(240) << 20;
 
 static int64_t block_window(const hq_plan* p, int64_t t, int topk) {
   const int64_t N = p->layer.n, per = std::max<int64_t>(1, t * topk * 2);
   if (N * per <= kBlockWindowBytes) return N;
+  int64_t cols = 256;
+  while (cols > 64 && cols * per >= (int64_t)hq::kSlotRowsMost) cols /= 2;  // (a's 2 GiB keep 64 of them below)
+  if (cols < 256) return std::min(cols, N);
   const int64_t n = cdiv(N, std::max<int64_t>(256, kBlockWindowBytes / per / 256 * 256));  // windows
   return cdiv(cdiv(N, n), 256) * 256;
 }
@@ -1300,8 +1304,6 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       const int64_t a_rows = epi == HQ_EPI_TOPK_COMBINE ? mp : t;
       if (a_rows * K * act_bytes2 / 2 >= (int64_t(1) << 31) || (int64_t)p->w_bytes_per_expert >= (int64_t(1) << 31))
         return fail(HQ_ERR_UNSUPPORTED, "activations and one expert's weights must each stay below 2 GiB");
-      if (epi == HQ_EPI_TOPK_COMBINE && hq::block_grouped(p->fmt) && t * topk * block_window(p, t, topk) * 2 >= (int64_t)hq::kSlotRowsMost)
-        return fail(HQ_ERR_UNSUPPORTED, "the slots' rows must stay below 4 GiB");
     }
     const uint32_t* zeros = p->layer.q.zp == HQ_ZP_PER_GROUP_U4
                                 ? reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(meta) +
@@ -1884,7 +1886,6 @@ static hq_status mx4_layer_check(const hq_plan* gu, const hq_plan* dn, int64_t t
   const int64_t mp = moe_max_padded(t, topk, gu->layer.num_experts, moe_choice(gu, t, topk).bm), most = int64_t(1) << 31;
   if (t * gu->layer.k / 2 >= most || mp * dn->layer.k / 2 >= most || (int64_t)gu->w_bytes_per_expert >= most || (int64_t)dn->w_bytes_per_expert >= most)
     return fail(HQ_ERR_UNSUPPORTED, "activations and one expert's weights must each stay below 2 GiB");
-  if (t * topk * block_window(dn, t, topk) * 2 >= (int64_t)hq::kSlotRowsMost) return fail(HQ_ERR_UNSUPPORTED, "the slots' rows must stay below 4 GiB");
   return HQ_OK;
 }
 

@@ -629,7 +629,7 @@ int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream) {
 int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.G < 1 || a.gps != a.G || a.N % (mode == B8_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
-  if (mode == B8_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
+  if (mode == B8_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 64 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
   B8Args b = a;
   const bool whole = mode == B8_DOWN && bm * (a.G * 132 + 8) <= kShortLds;
   if (whole) {

@@ -342,7 +342,7 @@ int launch_mx4_repack(int64_t N, int64_t K, int64_t E, bool paired, const void* 
 int launch_mx4_grouped(int mode, int bm, const Mx4Args& a, int64_t blocks, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.G < 1 || a.N % (mode == MX4_GATE_UP ? 256 : 64) || blocks < 1) return (int)hipErrorInvalidValue;
-  if (mode == MX4_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 256 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
+  if (mode == MX4_DOWN && (a.ncol < 64 || a.ncol % 64 || a.col0 % 64 || a.col0 + a.ncol > a.N)) return (int)hipErrorInvalidValue;
   if (bm != 16 && bm != 64 && bm != 128) return (int)hipErrorInvalidValue;
   Mx4Args b = a;
   b.tiles_n = (int)((mode == MX4_DOWN ? a.ncol : a.N) + 255) / 256;
