@@ -1227,11 +1227,18 @@ static int64_t moe_down_cols(const hq_plan* p, int64_t t, int topk, int bm) {
 // bits: from 2^23 slots on that is less than a tile's 256 columns.
 static constexpr int64_t kBlockWindowBytes = int64_t(240) << 20;
 
+// Bytes of a value of their slot rows.  fp8 block layers, and MXFP4 ones with outputs of bf16,
+// keep fp16 with a power of two per 64 columns, off by 2^-11 of a value at most, a quarter of
+// what rounding the output does.  To outputs of fp16 that adds as much as their own rounding
+// (1000 tokens of 64 experts, top 8: 2.8e-4 of the output's norm for 2.1e-4), so that MXFP4
+// layers keep 24 bits for them, off by 2^-16.
+static int64_t block_row_bytes(const hq_plan* p) { return p->fmt == hq::FMT_F44 && p->layer.q.out == HQ_F16 ? 3 : 2; }
+
 static int64_t block_window(const hq_plan* p, int64_t t, int topk) {
-  const int64_t N = p->layer.n, per = std::max<int64_t>(1, t * topk * 2);
+  const int64_t N = p->layer.n, slots = std::max<int64_t>(1, t * topk), per = slots * block_row_bytes(p);
   if (N * per <= kBlockWindowBytes) return N;
   int64_t cols = 256;
-  while (cols > 64 && cols * per >= (int64_t)hq::kSlotRowsMost) cols /= 2;  // (a's 2 GiB keep 64 of them below)
+  while (cols > 64 && cols * slots * 2 >= (int64_t)hq::kSlotRowsMost) cols /= 2;  // (a's 2 GiB keep 64 of them below)
   if (cols < 256) return std::min(cols, N);
   const int64_t n = cdiv(N, std::max<int64_t>(256, kBlockWindowBytes / per / 256 * 256));  // windows
   return cdiv(cdiv(N, n), 256) * 256;
@@ -1248,7 +1255,7 @@ static MoeWs moe_ws(const hq_plan* p, int64_t t, int topk) {
   if (p->compute.epi == HQ_EPI_SILU_MUL_QFP8 && p->fmt != hq::FMT_B8) w.act32 = align256((size_t)mp * (size_t)(p->layer.n / 2) * 4);
   if (p->compute.epi == HQ_EPI_TOPK_COMBINE && hq::block_grouped(p->fmt)) {
     const int64_t win = block_window(p, t, topk);
-    w.rows = align256((size_t)(t * topk * win) * 2) + align256((size_t)(t * topk * (win / 64)) * 4);
+    w.rows = align256((size_t)(t * topk * win * block_row_bytes(p))) + align256((size_t)(t * topk * (win / 64)) * 4);
   } else if (p->compute.epi == HQ_EPI_TOPK_COMBINE)
     w.rows = align256((size_t)t * topk * (size_t)moe_down_cols(p, t, topk, moe_choice(p, t, topk).bm) * 2);
   w.total = w.act32 + w.rows;
@@ -1364,7 +1371,8 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
       const int64_t win = down ? block_window(p, t, topk) : 1;
       hq::B8Args sum{};
       sum.rows16 = b.rows16 = rows16;
-      sum.row_scale = b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win) * 2));
+      if (down && block_row_bytes(p) == 3) b.rows8 = wsb + t * topk * win * 2;
+      sum.row_scale = b.row_scale = reinterpret_cast<float*>(wsb + align256((size_t)(t * topk * win * block_row_bytes(p))));
       sum.topk = topk;
       sum.N = (int)N;
       sum.out = out;
@@ -1376,7 +1384,7 @@ hq_status hq_moe_gemm(const hq_plan* p, int64_t t, int topk, const void* a, cons
         err = hq::launch_mx4_grouped(hq::MX4_DOWN, bm, b, blocks, stream);
         if (err != hipSuccess) break;
         hq::arm_timing({nullptr, c + win >= N ? ev.stop : nullptr});
-        err = hq::launch_b8_combine(sum, t, stream);
+        err = hq::launch_b8_combine(sum, t, stream, b.rows8);
       }
       hq::arm_timing({nullptr, nullptr});
       if (err != hipSuccess) return fail(HQ_ERR_HIP, "grouped gemm launch: %s", hipGetErrorString((hipError_t)err));

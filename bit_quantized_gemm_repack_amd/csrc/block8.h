@@ -63,8 +63,9 @@ bool b8_tile_ok(const B8Tile& t);
 int launch_b8_dense(const B8Tile& t, const B8Args& a, void* stream);
 // Grouped: aligned blocks of bm rows (16, 64, 128) by 256 columns.
 int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* stream);
-// y = the sum of a token's slot rows over the columns of a's window.
-int launch_b8_combine(const B8Args& a, int64_t t, void* stream);
+// y = the sum of a token's slot rows (fp16, or with rows8 24 bits a value) over the columns
+// of a's window.
+int launch_b8_combine(const B8Args& a, int64_t t, void* stream, const uint8_t* rows8 = nullptr);
 
 // Few rows: 16 rows by 16 nb columns a workgroup, K over its waves and over
 // `split` workgroups.

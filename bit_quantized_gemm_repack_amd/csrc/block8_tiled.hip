@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) b
 // reading the rows: a window of 4096 tokens, 235 MB, 43 us, 6.1 TB/s with its output.
 // The rows are done with once read: loads that do not keep them leave the cache to
 // the next window's (a layer of 4096 tokens 648 us against 661).
-__global__ void __launch_bounds__(256) b8_combine_kernel(const u4_t* __restrict__ rows, const float* __restrict__ scale,
+template <bool WIDE>
+__global__ void __launch_bounds__(256) b8_combine_kernel(const u4_t* __restrict__ rows, const u2_t* __restrict__ low, const float* __restrict__ scale,
                                                          int topk, int n, int col0, int ncol, int64_t elems,
                                                          uint4* __restrict__ y, int out_bf16) {
   const int ncol8 = ncol / 8, strips = ncol / 64;
@@ -542,6 +543,15 @@ __global__ void __launch_bounds__(256) b8_combine_kernel(const u4_t* __restrict_
     for (int j = 0; j < topk; ++j) {
       const u4_t w = __builtin_nontemporal_load(rows + (t * topk + j) * ncol8 + c);
       const float f = scale[(t * topk + j) * strips + c / 8];
+      if constexpr (WIDE) {
+        const u2_t l = __builtin_nontemporal_load(low + (t * topk + j) * ncol8 + c);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t hi = q & 1 ? w[q >> 1] & 0xFFFF0000u : w[q >> 1] << 16;
+          v[q] = fmaf(__uint_as_float(hi | ((l[q >> 2] >> (8 * (q & 3))) & 0xFFu) << 8), f, v[q]);
+        }
+        continue;
+      }
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] = fmaf(f16_bits_to_float((w[q >> 1] >> (16 * (q & 1))) & 0xFFFFu), f, v[q]);
     }
@@ -655,12 +665,14 @@ int launch_b8_grouped(int mode, int bm, const B8Args& a, int64_t blocks, void* s
   return (int)hipErrorInvalidValue;
 }
 
-int launch_b8_combine(const B8Args& a, int64_t t, void* stream) {
+int launch_b8_combine(const B8Args& a, int64_t t, void* stream, const uint8_t* rows8) {
   const int64_t elems = t * a.ncol / 8;
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((elems + 255) / 256, 16384));
-  return (int)launch_timed(b8_combine_kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
-                           reinterpret_cast<const u4_t*>(a.rows16), a.row_scale, a.topk, a.N, a.col0, a.ncol, elems,
-                           static_cast<uint4*>(a.out), a.out_bf16);
+  auto go = [&](auto kernel) {
+    return (int)launch_timed(kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream),
+                             reinterpret_cast<const u4_t*>(a.rows16), reinterpret_cast<const u2_t*>(rows8), a.row_scale, a.topk, a.N, a.col0, a.ncol, elems, static_cast<uint4*>(a.out), a.out_bf16);
+  };
+  return rows8 ? go(b8_combine_kernel<true>) : go(b8_combine_kernel<false>);
 }
 
 }  // namespace hq

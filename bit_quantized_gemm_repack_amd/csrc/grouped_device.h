@@ -1,7 +1,7 @@
 // Device helpers of the grouped products (aligned blocks of an expert's slots): where a
 // workgroup's tile lies, and the slots' rows on their way into the sum over a token's
 // experts.  Args: the kernel's arguments (sorted_ids, num_padded, topk_w, n_slots,
-// tiles_n, and for the rows col0, ncol, rows16, row_scale).
+// tiles_n, and for the rows col0, ncol, rows16, rows8, row_scale).
 #pragma once
 
 #include "block8_device.h"
@@ -115,6 +115,55 @@ __device__ __forceinline__ void store_slot_rows(const Args& p, const int32_t* id
 #endif
 }
 
+// The same rows in 24 bits a value, for sums that go on to fp16: the upper three bytes of the
+// rounded fp32, two of them in rows16 and one in rows8, and topk_w as their scale.  Each value
+// is off by at most 2^-16 of itself.
+template <int MB, typename Args>
+__device__ __forceinline__ void store_slot_rows24(const Args& p, const int32_t* ids, const float* tw, int col, int lane, const f4_t (&acc)[MB][4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int c16 = lane & 15, kq = lane >> 4;
+  const uint32_t ncol = (uint32_t)p.ncol, n = (uint32_t)p.n_slots;
+  const auto high = __builtin_amdgcn_make_buffer_rsrc(p.rows16, (short)0, (int)(n * (2 * ncol)), 0x00020000);
+  const auto low = __builtin_amdgcn_make_buffer_rsrc(p.rows8, (short)0, (int)(n * ncol), 0x00020000);
+  const auto scales = __builtin_amdgcn_make_buffer_rsrc(p.row_scale, (short)0, (int)(n * (ncol / 16)), 0x00020000);
+  const uint32_t at = (col - p.col0) + (kq & 1) * 16 + (kq >> 1) * 8;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const uint32_t id = (uint32_t)ids[16 * mb + c16];
+    const bool live = id < n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t hi[2][2], lo[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float v = acc[mb][2 * h + j][q];
+          b[q] = v == v ? __float_as_uint(v) + 0x80u : 0x7FC00000u;
+        }
+        hi[j][0] = __builtin_amdgcn_perm(b[1], b[0], 0x07060302);
+        hi[j][1] = __builtin_amdgcn_perm(b[3], b[2], 0x07060302);
+        lo[j] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0501), __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0501), 0x05040100);
+      }
+      // lanes of odd kq give their first four columns for their neighbour's second four
+      u4_t o;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const auto x = __builtin_amdgcn_permlane16_swap(hi[0][q], hi[1][q], false, false);
+        o[q] = x[0];
+        o[2 + q] = x[1];
+      }
+      const auto y = __builtin_amdgcn_permlane16_swap(lo[0], lo[1], false, false);
+      __builtin_amdgcn_raw_buffer_store_b128(o, high, live ? id * (2 * ncol) + 2 * at : kSlotRowsMost, 64 * h, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(u2_t{y[0], y[1]}, low, live ? id * ncol + at : kSlotRowsMost, 32 * h, 0);
+    }
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tw[16 * mb + c16]), scales,
+                                          live && kq == 0 ? id * (ncol / 16) + (col - p.col0) / 16 : kSlotRowsMost, 0, 0);
+  }
+#endif
+}
+
 // Slots and top-k weights of a block's rows, into LDS.
 template <typename Args>
 __device__ inline void load_slots(const Args& p, int m0, int rows, int32_t* ids, float* tw, int tid, int threads) {
@@ -134,7 +183,10 @@ __device__ inline void zero_slot_rows(const Args& p, int m0, int rows, int c0, i
     const int id = p.sorted_ids[m0 + r];
     if (id >= p.n_slots) continue;
     const int col = c0 + 64 * strip - p.col0;
-    *reinterpret_cast<uint2*>(p.rows16 + (int64_t)id * p.ncol + col + 4 * (i & 15)) = uint2{0u, 0u};
+    const int64_t at = (int64_t)id * p.ncol + col + 4 * (i & 15);
+    *reinterpret_cast<uint2*>(p.rows16 + at) = uint2{0u, 0u};
+    if constexpr (requires { p.rows8; })
+      if (p.rows8) *reinterpret_cast<uint32_t*>(p.rows8 + at) = 0u;
     if ((i & 15) == 0) p.row_scale[(int64_t)id * (p.ncol / 64) + col / 64] = 0.f;
   }
 }

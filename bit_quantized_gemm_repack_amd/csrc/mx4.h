@@ -42,7 +42,8 @@ struct Mx4Args {
   // down: this launch's columns [col0, col0 + ncol) of N, col0 a multiple of
   // 64; the slots' rows with a scale per 64 columns
   int col0, ncol;
-  uint16_t* rows16;          // [n_slots][ncol] fp16
+  uint16_t* rows16;          // [n_slots][ncol] fp16, or with rows8 the upper bytes of 24-bit values
+  uint8_t* rows8;            // [n_slots][ncol] their lowest bytes, or null
   float* row_scale;          // [n_slots][ncol / 64]
 };
 

@@ -175,7 +175,11 @@ __device__ __forceinline__ void mx4_tile(const Mx4Args& p, uint8_t* lds, int m0,
     __syncthreads();  // every wave is done with the stage ring
     load_slots(p, m0, C::BM, lid, ltw, tid, 64 * kWaves);
     __syncthreads();
-    if (col < p.col0 + p.ncol) store_slot_rows<MB>(p, lid, ltw, col, lane, acc);
+    if (col >= p.col0 + p.ncol) return;
+    if (p.rows8)
+      store_slot_rows24<MB>(p, lid, ltw, col, lane, acc);
+    else
+      store_slot_rows<MB>(p, lid, ltw, col, lane, acc);
   }
 #endif
 }
@@ -289,7 +293,10 @@ __global__ void __launch_bounds__(64 * kWaves) mx4_down_short(Mx4Args p, int bm)
       const u4_t a = *reinterpret_cast<const u4_t*>(lds + ((g / Q) * bm + r + c16) * 64 * Q + swz<CHUNKS>(c16, 4 * (g % Q) + kq) * 16);
       mx4_strip(w[g], a, acc[0], sw[g / Q].v[g % Q], ls[g * bm + r + c16] >> (8 * kq));
     }
-    store_slot_rows<1>(p, lid + r, ltw + r, col, lane, acc);
+    if (p.rows8)
+      store_slot_rows24<1>(p, lid + r, ltw + r, col, lane, acc);
+    else
+      store_slot_rows<1>(p, lid + r, ltw + r, col, lane, acc);
   }
 #endif
 }

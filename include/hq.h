@@ -422,7 +422,8 @@ hq_status hq_moe_align(int64_t t, int topk, int num_experts, int block_m, const 
  *                             (W8A8-BLOCK, W4A4: to fp16 with a power of two per 64
  *                             columns, each value off by at most 2^-11 of itself
  *                             down to 2^-29 of the 64 columns' largest, and below
- *                             by 2^-39 of that one), goes
+ *                             by 2^-39 of that one; W4A4 with fp16 outputs: to
+ *                             24 bits, off by at most 2^-16 of itself), goes
  *                             to the workspace, then a second kernel sums a
  *                             token's topk rows in fp32 in slot order and
  *                             rounds once, so the result is deterministic.
@@ -553,7 +554,7 @@ hq_status hq_moe_layer_few(const hq_plan* gate_up, const hq_plan* down, int64_t 
  *   y[i] = sum_j topk_w[i, j] q(SiLU(g) * u) W2[e]^T,  (g, u) = halves of q(x[i]) W1[e]^T,
  * e = topk_ids[i, j], q as hq_quantize_mxfp4.  A few tokens (N = H) run in two kernels, others as
  * hq_quantize_mxfp4, hq_moe_align and the two GEMMs do, with the same roundings but for a
- * slot's row of down, which only they round (to fp16 with a scale by 64 columns).
+ * slot's row of down, which only they round (as hq_moe_gemm's TOPK_COMBINE does).
  *   x         device [t, H] fp16 / bf16, or E2M1 codes [t, H/2] (x_type HQ_FP4_E2M1)
  *   x_scale   of codes: device E8M0 [H/128, t, 4], as hq_quantize_mxfp4 and hq_rms_norm
  *             write them; NULL for 16 bits

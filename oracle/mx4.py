@@ -26,6 +26,8 @@ E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 # value is off by at most 2^-11 of itself down to 2^-29 of the 64 columns' largest, and
 # below by 2^-39 of that one.
 ROW_SELF, ROW_TOP = 2.0 ** -11, 2.0 ** -39
+# The same on its way to outputs of fp16: 24 bits a value, 16 of them significant.
+ROW_24 = 2.0 ** -16
 
 
 def values(codes: torch.Tensor) -> torch.Tensor:
