@@ -102,7 +102,7 @@ int launch_mx4_prepare(const Mx4PrepareArgs& a, void* stream);
 
 // An experts' layer for a few tokens in two kernels (mx4_few.hip).
 enum Mx4Input : int { MX4_F16 = 0, MX4_BF16 = 1, MX4_CODES = 2 };
-constexpr int kMx4FewTokens = 64, kMx4FewTopk = 16;
+constexpr int kMx4FewTokens = 32, kMx4FewTopk = 16;
 struct Mx4FewArgs {
   const void* x;             // [t][H] 16-bit, or codes [t][H / 2]
   const uint32_t* x_scale;   // of codes: [H / 128][t]

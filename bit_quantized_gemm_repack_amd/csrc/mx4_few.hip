@@ -385,11 +385,25 @@ hipError_t down(const Mx4FewArgs& a, hipStream_t s) {
 
 bool mx4_few_ok(int64_t t, int64_t topk, int64_t E, int64_t H, int64_t I) {
   // The aligned path starts two kernels more, and its gate_up walks all of K in each wave; but
-  // its workgroups are larger, which many slots pay for.  Top 8, us a layer here / there: H =
-  // 7168, I = 256: 1 token 13.5 / 36.8, 4 tokens 25.0 / 42.0, 9 tokens 48.1 / 49.7, 10 tokens
-  // 51.4 / 50.7, 13 tokens 62 / 56; H = 2048, I = 768: 2 tokens 22.1 / 26.0, 3 tokens 28.3 / 25.7.
-  return t >= 1 && t <= kMx4FewTokens && t * topk * 96 <= H && topk >= 1 && topk <= kMx4FewTopk && E <= 4096 && row_bytes(H) <= kFewLds &&
-         std::min<int64_t>(t, 16) * topk * row_bytes(I) <= kFewLds;
+  // its workgroups are larger, which many slots pay for.  us a layer here / there (bf16, uniform
+  // routing, in a graph), by what each limit below is drawn from:
+  //   slots by H: top 8 of 256 experts, H = 7168, I = 256: 1 token 12.7 / 35.2, 4 tokens 25.0 /
+  //     41.7, 9 tokens 46.8 / 48.7, 13 tokens 62 / 56; H = 2048, I = 768: 2 tokens 20.9 / 25.6,
+  //     3 tokens 28.3 / 25.7
+  //   slots by I, as a down workgroup forms all its tile's codes first: 8 experts, H = 4096, I =
+  //     2048: top 1, 8 tokens 24.3 / 32.0, 12 tokens 31.6 / 33.1, 16 tokens 36.0 / 33.6; top 8,
+  //     1 token 28.0 / 35.6, 2 tokens 38.9 / 35.8; 64 experts, H = 4096, I = 512, top 4: 8 tokens
+  //     27.3 / 31.2, 10 tokens 34.3 / 32.9
+  //   rows an expert, as its weights are read again for each four: 8 experts, H = 7168, I = 256:
+  //     top 1, 17 tokens 27.9 / 31.4, 24 tokens 30.5 / 25.3; top 2, 10 tokens 26.1 / 30.5, 17
+  //     tokens 35.3 / 30.1; 16 experts, top 2, 16 tokens 24.9 / 32.7, 24 tokens 38.7 / 32.1; four
+  //     tokens are four rows at most: 8 experts, top 8 21.8 / 30.3
+  //   tiles of 16 tokens, each of which reads down's weights: top 1, H = 7168, I = 256: 16 / 64 /
+  //     256 experts, 32 tokens 27.9 / 32.5, 27.0 / 36.7, 27.9 / 39.6; 40 tokens 40.0 / 33.1, 35.4 /
+  //     38.3, 36.9 / 41.7; 64 tokens 52.6 / 33.3, 47.7 / 41.3, 47.9 / 45.9
+  const int64_t slots = t * topk;
+  return t >= 1 && t <= kMx4FewTokens && topk >= 1 && topk <= kMx4FewTopk && slots * 96 <= H && slots * I <= 20000 &&
+         (2 * slots <= 5 * E || t <= 4) && E <= 4096 && row_bytes(H) <= kFewLds && std::min<int64_t>(t, 16) * topk * row_bytes(I) <= kFewLds;
 }
 
 size_t mx4_few_act_bytes(int64_t t, int64_t topk, int64_t I) {
@@ -405,7 +419,8 @@ int launch_mx4_few(const Mx4FewArgs& a, void* stream) {
   else
     b.h = nullptr;
   // rows of x a gate_up workgroup keeps at a time (the weights are read again for each
-  // further so many): four cover an expert's tokens of a small batch nearly always
+  // further so many): four cover an expert's tokens where routing is even, as mx4_few_ok
+  // allows 2.5 an expert
   b.rows = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)a.t, 4, kFewLds / row_bytes(a.H)}));
   const TimingEvents ev = take_timing();
   arm_timing({ev.start, nullptr});
