@@ -1179,7 +1179,9 @@ def route_experts(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] 
     "softmax"; bias float32 [experts] counts for the choice only.  With groups > 1
     only experts of the group_topk best groups are chosen, a group's score being the
     sum of its group_best (1 or 2) best.  Returns (ids int32 [t, topk], weights
-    float32 [t, topk]), the (topk_ids, topk_w) of moe_layer."""
+    float32 [t, topk]), the (topk_ids, topk_w) of moe_layer.  For plain softmax
+    routing route_topk is the shorter kernel; it orders by the logits themselves,
+    this by scores rounded to float32, so that near ties may fall otherwise."""
     if _calls is not None:
         r = _calls.route_experts(logits, topk, bias, _SCORE.get(scoring), groups, group_topk, group_best, renormalize, scale)
         if r is not None:

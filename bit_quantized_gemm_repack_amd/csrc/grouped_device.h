@@ -50,8 +50,8 @@ __device__ __forceinline__ float lanes_max(float v) {
 // A slot's row of the down GEMM, 64 columns a wave, on its way into the sum over
 // the token's experts: fp16 values o / 2^e, with the 2^e that brings the 64 columns'
 // largest finite one to [2^14, 2^15), and topk_w * 2^e as their scale.  Half the
-// bytes of fp32 rows, which are a third of the layer's traffic (4096 tokens with
-// fp16 outputs: 980 us with fp32 rows, 739 with these).  Each value is off by at most
+// bytes of fp32 rows, which are a third of the layer's traffic (an fp8 block layer of 4096
+// tokens with fp16 outputs: 980 us with fp32 rows, 725 with these).  Each value is off by at most
 // 2^-11 of itself down to 2^-29 of the largest, and below that by 2^-39 of the
 // largest: an eighth of bf16's rounding, and as much as fp16's own.  (Integers of
 // one step for the 64 columns were finer beside a large column and lost the others.)
@@ -117,7 +117,9 @@ __device__ __forceinline__ void store_slot_rows(const Args& p, const int32_t* id
 
 // The same rows in 24 bits a value, for sums that go on to fp16: the upper three bytes of the
 // rounded fp32, two of them in rows16 and one in rows8, and topk_w as their scale.  Each value
-// is off by at most 2^-16 of itself.
+// is off by at most 2^-16 of itself.  In an MXFP4 layer of 4096 tokens of 256 experts (H = 7168)
+// 584 us against 457 with 16 bits and 692 with fp32; of 1000 tokens of 64 (H = 2048) 79 against
+// 74 and 84.
 template <int MB, typename Args>
 __device__ __forceinline__ void store_slot_rows24(const Args& p, const int32_t* ids, const float* tw, int col, int lane, const f4_t (&acc)[MB][4]) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -6,9 +6,9 @@
 // Both are bound by reading the chosen experts' weights, which every workgroup streams
 // straight to registers, its waves taking the steps along K in turn; tokens that picked the
 // same expert share one read (they are the columns of the matrix instruction).  One token of
-// top 8, H = 7168, I = 256: 7.0 + 6.2 us, of which the 23 MB of weights take 3.7 at the 6.4 TB/s
-// that plain reads reach and starting, ids, the row's quantisation and the sums over waves the
-// rest; 8 tokens 24 + 14.5 us for 164 MB (26 us).
+// top 8, H = 7168, I = 256: 6.6 + 6.1 us start to end, of which the 23 MB of weights take 3.7 at
+// the 6.4 TB/s that plain reads reach and starting, ids, the row's quantisation and the sums over
+// waves the rest; 4 tokens 15.3 + 8.9; 8 tokens 24.3 + 14.8 for 164 MB (26 us).
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -25,7 +25,7 @@ namespace hq {
 namespace {
 
 // Columns of gate_up by 16 rather than by strip: while that makes at most two workgroups a
-// CU (top 8, us a layer by column / by strip: H = 7168, I = 256: 2 tokens 19.7 / 22.5, 3 tokens
+// CU (top 8, us a layer in a graph by column / by strip: H = 7168, I = 256: 2 tokens 19.7 / 22.5, 3 tokens
 // 26.5 / 22.6, 4 tokens 31.8 / 25.0; H = 2048, I = 768: 1 token 16.7 / 15.8, 2 tokens 29.1 / 22.1).
 bool narrow(int64_t t, int64_t topk, int64_t I) { return t * topk * (I / 8) <= 512; }
 

@@ -1,6 +1,6 @@
 // What an MXFP4 experts' layer needs before its products, in one launch: x in MXFP4 and the
-// slots sorted by expert.  4096 x 7168 and 32768 slots of 256 experts 17.5 us, the quantiser's 74
-// MB alone 15 and one sorting workgroup alone 25.6; 13 tokens 5.7, two launches before 9.
+// slots sorted by expert.  4096 x 7168 and 32768 slots of 256 experts 17.4 us, the quantiser's 74
+// MB alone 15 and one sorting workgroup alone 25.6; 13 tokens 5.5, two launches before 9.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 

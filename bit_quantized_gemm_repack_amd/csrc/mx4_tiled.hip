@@ -200,7 +200,7 @@ __device__ __forceinline__ void mx4_tile_rows(const Mx4Args& p, uint8_t* lds, in
 }
 
 // gate_up is bound by its weights' way from beyond L2: 509 tokens of 256 experts (top 8, H =
-// 7168, I = 256) 84 us, 5.9 TB/s, 13 tokens 28; 4096 tokens 145 .. 160, 0.77 GB for 0.5 of need,
+// 7168, I = 256) 84 us, 5.9 TB/s, 13 tokens 28; 4096 tokens 159, 0.75 GB for 0.5 of need,
 // as an expert's further blocks seldom find them there.  64 experts, H = 2048, I = 768, 1000
 // tokens: 43, eight steps a tile whose start and end take as long.  Three workgroups a CU with
 // a ring of two are level (82 and 42), but 13 tokens take 39.
@@ -231,8 +231,9 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 // weights in registers whole, the block's activation rows lie in LDS, and sixteen of them
 // at a time are multiplied and stored.  Past its start a wave loads nothing more: loads and
 // stores return in one order, so that a load's wait would cover the stores before it (rows
-// straight from memory, a ring of three: 105 us a window of 4096 tokens, now 92: 125 MB of weights
-// read and 235 of slot rows written; 509 tokens 60).
+// straight from memory, a ring of three: 105 us a window of 4096 tokens, now 91: 125 MB of weights
+// read and 235 of slot rows written; 509 tokens 59; 1000 of 64 experts to fp16 33.7, 49 MB of
+// rows of 24 bits, with rows of 16 26.5).
 constexpr int kShortGroups = 8;
 constexpr int short_lds(int bm, int G) { return bm * (G * 68 + 8); }
 

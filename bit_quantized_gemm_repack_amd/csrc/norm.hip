@@ -13,10 +13,11 @@
 // maxima need one pass over registers and one meeting of the row's threads.  h w
 // is exact for 16-bit weights, so y rounds once more than the factor.
 //
-// Bound by memory: x, r and h are moved once.  bf16 with residual, in a graph: 8191
-// x 4096 to e4m3 by row 44.6 us, 5.3 TB/s (a large copy reaches 5.0), 8191 x 7168 to
-// MXFP4 70 us, 5.5 TB/s; one row of 7168 to MXFP4 3.1 us, a launch and a chain of
-// loads, sums and codes.
+// Bound by memory: x, r and h are moved once.  With residual, start to end of the kernel:
+// 8191 x 4096 fp16 to e4m3 by row 38.2 us, 6.1 TB/s (a streaming read reaches 6.4, a copy of
+// 1 GiB 5.2); 8191 x 7168 bf16 in 16 bits 81 us, 5.8 TB/s, to e4m3 by 128 76, to int8 by row
+// 75, to MXFP4 70, 5.5 TB/s.  Few rows are a chain of loads, sums and codes: one of 7168 to
+// e4m3 by 128 3.5 us; 509 to MXFP4 8.5, 2.8 TB/s, the waves waiting half of their time.
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -225,7 +226,7 @@ int launch_out(const NormArgs& a, hipStream_t s) {
       });
   };
   // The shape that leaves the fewest threads idle, with the more threads the fewer
-  // rows there are (us, bf16 with residual, to 16 bits / e4m3 by row / MXFP4):
+  // rows there are (us a call in a graph, bf16 with residual, to 16 bits / e4m3 by row / MXFP4):
   //   k = 7168, 1 row: 512 threads of two chunks 3.0 / 3.5 / 3.1, 256 of four 3.4 /
   //   4.3 / 3.7, 64 of fourteen 5.8 / 9.1 / 7.4; 8191 rows: 82 / 74 / 70, 82 / 74 / 70,
   //   91 / 121 / 80

@@ -10,8 +10,9 @@
 // The scores are formed in 64 bits and rounded once: a choice must not depend on how
 // an exponential was rounded, and scores one last bit apart occur (saturated sigmoids,
 // 16-bit logits, a few pairs among 16383 rows of 160 random ones).  The vector units
-// run 64-bit multiply-adds at the rate of 32-bit ones.  One token by 256 experts takes 4.9 us
-// in a graph of them, 4096 8.2; the library's exp() and quotients took 9.0.
+// run 64-bit multiply-adds at the rate of 32-bit ones.  Start to end of the kernel, one token by
+// 256 experts takes 4.4 us, 4096 8.6, 16383 by 160 13.4 (in a graph the library's exp() and
+// quotients took 9.0 for 8.2 at 4096).
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
@@ -201,8 +202,10 @@ __global__ void __launch_bounds__(256) route_experts_kernel(RouteArgs p) {
 
 // Many tokens: four to a wave, 16 lanes each; lane l of them holds experts l, l + 16, ...
 // The choices, which walk the row topk times, then cost a wave a quarter as many steps.  Bound
-// by issuing: 16383 x 160 reads and writes 6 MB, but the wave per four tokens issues some
-// thousand instructions, about half of them the choices' (11.9 us a call, 12.8 in a graph).
+// by issuing: 16383 x 160 reads and writes 6 MB, but a wave, four tokens, issues 1450 vector and
+// 430 scalar instructions, and the vector units are busy for 5800 of the kernel's 8000 periods
+// of four cycles.  The twelve exponentials a lane are 480 of them, half in 64 bits, the six
+// choices 444.
 template <int NPL>
 __global__ void __launch_bounds__(256) route_quarters_kernel(RouteArgs p) {
   __shared__ uint32_t keys[16][16 * NPL];
@@ -311,7 +314,7 @@ int launch_route_experts(const RouteArgs& a, void* stream) {
   if (a.t < 1 || a.E < 1 || a.E > 1024 || a.groups < 1 || a.groups > 64 || a.E % a.groups) return (int)hipErrorInvalidValue;
   const dim3 grid((unsigned)((a.t + 3) / 4)), block(256);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  // us with a wave / a quarter of one per token: 160 experts, top 6 of 3 of 8 groups: 4096 tokens
+  // us in a graph with a wave / a quarter of one per token: 160 experts, top 6 of 3 of 8 groups: 4096 tokens
   // 7.3 / 7.5, 8192 11.1 / 8.8, 16383 18.7 / 12.8; 256, top 8 of 4 of 8: 8192 13.0 / 14.0, 16383
   // 22.2 / 18.9; 128, top 8: 4096 5.6 / 5.7, 8192 8.2 / 6.5; 64, top 6: 2048 3.5 / 3.9, 4096 4.2 / 3.9
   if (a.t >= 4096 && a.t >= 40 * a.E && a.topk <= 16 && a.groups <= 16 && a.E <= 256) {

@@ -488,7 +488,10 @@ hq_status hq_moe_gemm_by_slot(const hq_plan* plan, int64_t t, int topk, const vo
  * others ends in ids of -1 with weight 0.  A logit of +inf gives unspecified
  * weights; one below 2^-126 may be zero.  topk_ids int32 and topk_w fp32 [t,
  * topk], fully overwritten, as
- * hq_moe_align / hq_moe_gemm take them.  num_experts <= 1024, topk <= 64,
+ * hq_moe_align / hq_moe_gemm take them.  (hq_route_experts by softmax orders by the
+ * rounded scores instead: logits that differ but round to one score are a tie there,
+ * so that its ids may differ from these; a model's router takes one or the other for
+ * good.)  num_experts <= 1024, topk <= 64,
  * t <= 2^24; t = 0 is a no-op.  The three are aligned to their elements (slices
  * of a batch may start at any row).  Honours hq_time_next_launch (one kernel). */
 hq_status hq_route_topk(int64_t t, int num_experts, int topk, hq_dtype logit_type, const void* logits, int renormalize,
@@ -657,7 +660,8 @@ hq_status hq_quantize_mxfp4(int64_t m, int64_t k, hq_dtype in, const void* x, vo
  * A row (HQ_NORM_FP8, _INT8) or block (the others) of y that holds an infinity or
  * a NaN gets the scale NaN, and unspecified codes, so that the product's row is
  * NaN.  The squares are summed in fp32: a row whose sum is past fp32's range gives
- * zeros or NaN.
+ * zeros or NaN, and one whose squares are all below it (|h| < 2^-75) counts as zeros,
+ * which with eps = 0 is NaN or infinite.
  * k must be a multiple of 8 (128 for _FP8_BLOCK and _MXFP4) up to 65536, the
  * strides multiples of 8, the pointers 16-byte aligned, m at most 2^24, eps at least 0;
  * m = 0 is a no-op.  Honours hq_time_next_launch (one kernel; more from 2^22 rows on). */
