@@ -26,3 +26,36 @@ def test_layer(t, e, topk, h, i, dt):
     L.check(y, x, ids, w, "16-bit x")
     codes, s = hq.quantize_mxfp4(x)
     assert torch.equal(y, L.run(codes, ids, w, x_scale=s)), "quantised outside"
+
+
+def test_graphs_and_streams_of_fp16_outputs():
+    """Two graphs of one layer, replayed with new inputs and eager calls between, and two streams at once."""
+    e, topk, h, i, t = 12, 4, 1024, 384, 300
+    L = Layer(3, e, h, i, t, "f16")
+    xs = [_x(L.g, t, h, torch.float16) for _ in range(3)]
+    rt = [_routing(L.g, t, e, topk) for _ in range(3)]
+    want = [L.run(x, *r) for x, r in zip(xs, rt)]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = [None] * 3
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+    for k in range(3):
+        with torch.cuda.stream(side[k % 2]):
+            got[k] = L.run(xs[k], *rt[k])
+    for s in side:
+        torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    x, ids, w = xs[0].clone(), rt[0][0].clone(), rt[0][1].clone()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = L.run(x, ids, w)
+        graphs.append((graph, out))
+    for k in (1, 2, 0, 1):
+        x.copy_(xs[k]), ids.copy_(rt[k][0]), w.copy_(rt[k][1])
+        for graph, out in graphs:
+            graph.replay()
+            assert torch.equal(L.run(xs[k], *rt[k]), want[k])
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want[k]) for _, out in graphs), f"replay of {k}"
