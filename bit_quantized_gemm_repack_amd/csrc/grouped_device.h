@@ -118,8 +118,8 @@ __device__ __forceinline__ void store_slot_rows(const Args& p, const int32_t* id
 // The same rows in 24 bits a value, for sums that go on to fp16: the upper three bytes of the
 // rounded fp32, two of them in rows16 and one in rows8, and topk_w as their scale.  Each value
 // is off by at most 2^-16 of itself.  In an MXFP4 layer of 4096 tokens of 256 experts (H = 7168)
-// 584 us against 457 with 16 bits and 692 with fp32; of 1000 tokens of 64 (H = 2048) 79 against
-// 74 and 84.
+// 556 us against 457 with 16 bits and 692 with fp32; of 1000 tokens of 64 (H = 2048) 78 against
+// 74 and 84.  (The lowest bytes in two stores of 8 a lane: 583, 79.)
 template <int MB, typename Args>
 __device__ __forceinline__ void store_slot_rows24(const Args& p, const int32_t* ids, const float* tw, int col, int lane, const f4_t (&acc)[MB][4]) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -133,6 +133,7 @@ __device__ __forceinline__ void store_slot_rows24(const Args& p, const int32_t* 
   for (int mb = 0; mb < MB; ++mb) {
     const uint32_t id = (uint32_t)ids[16 * mb + c16];
     const bool live = id < n;
+    uint32_t lows[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t hi[2][2], lo[2];
@@ -157,9 +158,15 @@ __device__ __forceinline__ void store_slot_rows24(const Args& p, const int32_t* 
         o[2 + q] = x[1];
       }
       const auto y = __builtin_amdgcn_permlane16_swap(lo[0], lo[1], false, false);
+      lows[h][0] = y[0];
+      lows[h][1] = y[1];
       __builtin_amdgcn_raw_buffer_store_b128(o, high, live ? id * (2 * ncol) + 2 * at : kSlotRowsMost, 64 * h, 0);
-      __builtin_amdgcn_raw_buffer_store_b64(u2_t{y[0], y[1]}, low, live ? id * ncol + at : kSlotRowsMost, 32 * h, 0);
     }
+    // lanes of kq >= 2 give their eight columns of the first half for their neighbour's of the second
+    const auto y0 = __builtin_amdgcn_permlane32_swap(lows[0][0], lows[1][0], false, false);
+    const auto y1 = __builtin_amdgcn_permlane32_swap(lows[0][1], lows[1][1], false, false);
+    __builtin_amdgcn_raw_buffer_store_b128(u4_t{y0[0], y1[0], y0[1], y1[1]}, low,
+                                           live ? id * ncol + (col - p.col0) + (kq & 1) * 16 + (kq >> 1) * 32 : kSlotRowsMost, 0, 0);
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(tw[16 * mb + c16]), scales,
                                           live && kq == 0 ? id * (ncol / 16) + (col - p.col0) / 16 : kSlotRowsMost, 0, 0);
   }

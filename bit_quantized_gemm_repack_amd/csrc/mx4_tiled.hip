@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_e
 // at a time are multiplied and stored.  Past its start a wave loads nothing more: loads and
 // stores return in one order, so that a load's wait would cover the stores before it (rows
 // straight from memory, a ring of three: 105 us a window of 4096 tokens, now 91: 125 MB of weights
-// read and 235 of slot rows written; 509 tokens 59; 1000 of 64 experts to fp16 33.7, 49 MB of
+// read and 235 of slot rows written; 509 tokens 59; 1000 of 64 experts to fp16 30.9, 49 MB of
 // rows of 24 bits, with rows of 16 26.5).
 constexpr int kShortGroups = 8;
 constexpr int short_lds(int bm, int G) { return bm * (G * 68 + 8); }
